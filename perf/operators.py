@@ -1,14 +1,14 @@
 """Cases for the 4-bit key / value cache of the M-FALCON candidate path.
 
 Four operators, reached through hstu_pointwise_attention_b200.ops:
-  append  quantise new tokens' keys and values into the cache (kv4_append),
-          read back as the values they stand for (kv4_read)
+  append  quantise new tokens' keys and values into the cache (qcache_append),
+          read back as the values they stand for (qcache_read)
   attend  candidates (or one new event) against the cached history
-          (attn_fwd_candidates_kv4), optionally adding up how much weight each
+          (attn_fwd_candidates_qcache), optionally adding up how much weight each
           cached row received
-  evict   keep a user's `budget` most used rows (kv4_evict), read back
+  evict   keep a user's `budget` most used rows (qcache_evict), read back
   layer   a whole HSTU layer on candidate rows over the cache
-          (layer_fwd_candidates_kv4)
+          (layer_fwd_candidates_qcache)
 
 The 4-bit format: groups of 32 values along the head dimension share a scale
 s (a float with 4 significant bits) and a zero point z in 0..15; a value is
@@ -268,30 +268,30 @@ def run(s):
 def _run_own(s, case):
     from hstu_pointwise_attention_b200 import ops
     if "handle" not in s:
-        s["handle"] = ops.Kv4Cache(**s["cache"])
+        s["handle"] = ops.QuantCache(**s["cache"])
         if "dst" in s:
-            s["dst_handle"] = ops.Kv4Cache(**s["dst"])
+            s["dst_handle"] = ops.QuantCache(**s["dst"])
     cache, off = s["handle"], s["off"]
     if case["op"] == "append":
-        ops.kv4_append(cache, s["k"], s["v"], s["ts"], off, s["rows"], s["pos"])
-        k, v = ops.kv4_read(cache, s["rows"], np.diff(off), dtype=s["dtype"])
+        ops.qcache_append(cache, s["k"], s["v"], s["ts"], off, s["rows"], s["pos"])
+        k, v = ops.qcache_read(cache, s["rows"], np.diff(off), dtype=s["dtype"])
         return k, v, cache.times, cache.pos
     if case["op"] == "evict":
         dst = s["dst_handle"]
-        ops.kv4_evict(cache, s["rows"], s["hist"], s["budget"], s["keep_pos"], dst=dst,
+        ops.qcache_evict(cache, s["rows"], s["hist"], s["budget"], s["keep_pos"], dst=dst,
                       dst_rows=s["dst_rows"])
-        k, v = ops.kv4_read(dst, s["dst_rows"], s["budget"], dtype=s["dtype"])
+        k, v = ops.qcache_read(dst, s["dst_rows"], s["budget"], dtype=s["dtype"])
         return k, v, dst.times, dst.pos, dst.weight
     kw = dict(max_seq_len=s["msl"], time_bucket_sub_bits=case["sub_bits"], alpha=s["alpha"],
               silu_scale=s["scale"])
     if case["op"] == "layer":
-        return ops.layer_fwd_candidates_kv4(
+        return ops.layer_fwd_candidates_qcache(
             s["x"], s["w1"], s["b1"], s["gamma"], s["beta"], s["w2"], s["b2"], s["rab_p"],
             s["rab_t"], cache, s["rows"], s["hist"], off, s["cand_pos"], s["cand_ts"],
             num_heads=case["heads"], d_qk=case["d"], d_v=case["d"], **kw)
     if case["weights"]:
         cache.weight.copy_(s["weight0"])
-    out = ops.attn_fwd_candidates_kv4(
+    out = ops.attn_fwd_candidates_qcache(
         s["q"], s["k"], s["v"], cache, s["rows"], s["hist"], off, s["cand_pos"], s["cand_ts"],
         s["rab_p"], s["rab_t"], rab_per_head=case["per_head"],
         weight_decay=0.5 if case["weights"] else None, **kw)
