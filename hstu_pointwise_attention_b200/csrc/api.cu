@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../include/hstu.h"
+#include "api_common.h"
 #include "internal.h"
 
 namespace hstu {
@@ -168,6 +169,14 @@ static hstu_status_t validate(const hstu_attn_params_t *p, const int64_t *off,
   const int64_t T = p->batch > 0 ? off[p->batch] : 0;
   if (T >= (int64_t(1) << 31)) return HSTU_ERR_UNSUPPORTED;
   return HSTU_OK;
+}
+
+hstu_status_t validate_shape(const hstu_attn_params_t *p) {
+  if (!p) return HSTU_ERR_INVALID_ARG;
+  hstu_attn_params_t q = *p;   // the shared checks with an empty batch
+  q.batch = 0;
+  q.mask = HSTU_MASK_CAUSAL;
+  return validate(&q, nullptr, nullptr, false);
 }
 
 // Work lists, longest first.  Forward: one item per (sequence, pair of
@@ -399,7 +408,7 @@ static cudaError_t stage_plan(const Plan &plan, const WsLayout &w, void *ws, Scr
 
 static hstu_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA; }
 
-static uint64_t wait_limit_ns() {
+uint64_t wait_limit_ns() {
   const uint64_t v = g_wait_limit_ns.load(std::memory_order_relaxed);
   return v ? v : kDefaultWaitNs;
 }
@@ -773,11 +782,7 @@ struct CachedWs {
 static hstu_status_t validate_cached(const hstu_attn_params_t *p, const int64_t *hoff,
                                      const int64_t *coff, int64_t kh_rs, int64_t vh_rs) {
   if (!p) return HSTU_ERR_INVALID_ARG;
-  // the shared checks (dimensions, buckets, scales, strides) with an empty batch
-  hstu_attn_params_t q = *p;
-  q.batch = 0;
-  q.mask = HSTU_MASK_CAUSAL;
-  hstu_status_t st = validate(&q, nullptr, nullptr, false);
+  hstu_status_t st = validate_shape(p);
   if (st != HSTU_OK) return st;
   if (p->batch < 0) return HSTU_ERR_INVALID_ARG;
   if (kh_rs < int64_t(p->num_heads) * p->d_qk || vh_rs < int64_t(p->num_heads) * p->d_v)

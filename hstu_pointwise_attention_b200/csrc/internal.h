@@ -135,6 +135,9 @@ constexpr bool kTraceBuild = true;
 constexpr bool kTraceBuild = false;
 #endif
 
+// The bound on one device-side wait that hstu_set_wait_limit set (nanoseconds).
+uint64_t wait_limit_ns();
+
 // --- launchers (return a cudaError_t of the launch) ---
 // Copies `bytes` (a multiple of 16) from host memory at src to the 16-byte
 // aligned device address dst through kernel parameters (no host wait); when

@@ -1,0 +1,411 @@
+// qcache.cu -- the 4-bit history cache: storing new rows (quantisation),
+// reading rows back, and trimming a user's rows to the ones that received the
+// most attention weight.  Format and rounding: qcache.cuh.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "qcache.cuh"
+#include "qcache_host.h"
+
+namespace hstu {
+namespace qc {
+
+// ---------------------------------------------------------------------------
+// Append: quantise rows of K and V, write codes, parameters, time, position.
+//
+// Four consecutive lanes hold one group of 32 values (8 each), so a warp reads
+// and writes consecutive addresses on both sides; the group's minimum and
+// maximum take two shuffles.
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]);
+
+template <>
+__device__ __forceinline__ void load8<float>(const float *p, bool vec, float (&x)[8]) {
+  if (vec) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = p[i];
+  }
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, bool vec,
+                                                      float (&x)[8]) {
+  if (vec) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(p[i]);
+  }
+}
+
+// rne(x / s) of the exact quotient, given inv ~ 1 / s: the product rounds to
+// within one of it, and the remainder x - y s (exact in one fma) settles it.
+__device__ __forceinline__ float rne_div(float x, float s, float inv) {
+  float y = rintf(x * inv);
+  const float rem = fmaf(-y, s, x), half = 0.5f * s;
+  if (rem > half || rem < -half || (fabsf(rem) == half && fmodf(y, 2.0f) != 0.0f))
+    y += rem > 0.f ? 1.f : -1.f;
+  return y;
+}
+
+// One group: this lane's 8 values, the other 24 in the lanes of its quad.
+__device__ __forceinline__ void quantise8(float (&x)[8], uint32_t &word, uint32_t &param) {
+  const uint32_t quad = 0xFu << (threadIdx.x & 28);   // other quads may have left the loop
+  float lo = 0.f, hi = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -0x1p126f), 0x1p126f);
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+  }
+#pragma unroll
+  for (int m = 1; m < 4; m <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(quad, lo, m));
+    hi = fmaxf(hi, __shfl_xor_sync(quad, hi, m));
+  }
+  // span = hi - lo exactly: rounded difference r plus its rounding error
+  const float r = hi - lo, bb = r - hi, err = (hi - (r - bb)) + (-lo - bb);
+  // the scale's 4 significant bits: truncate r / 15, one step up unless
+  // 15 s (exact) already covers the span
+  float s = __uint_as_float(__float_as_uint(r / 15.0f) & 0xFFF00000u);
+  const float p = 15.0f * s;
+  if (p < r || (p == r && err > 0.f)) s = __uint_as_float(__float_as_uint(s) + 0x00100000u);
+  s = fmaxf(s, 0x1p-126f);
+  word = 0;
+  param = 0;
+  if (hi > lo) {
+    const float inv = 1.0f / s;
+    const float z = rne_div(-lo, s, inv);
+    param = (__float_as_uint(s) >> 16) | uint32_t(z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = fminf(fmaxf(rne_div(x[i], s, inv) + z, 0.f), 15.f);
+      word |= uint32_t(q) << (4 * (i >> 1) + 16 * (i & 1));
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+    append_kernel(const __grid_constant__ QcRowsParams p) {
+  const QCacheView &c = p.cache;
+  const int kw = c.heads * (c.d_qk >> 3), units = kw + c.heads * (c.d_v >> 3);
+  // a block takes kRowThreads / units tokens side by side (units is a multiple
+  // of 4: a group's quad never straddles two tokens), or one token in steps
+  const int tpb = units < kRowThreads ? kRowThreads / units : 1;
+  const int tl = tpb > 1 ? int(threadIdx.x) / units : 0;
+  if (tl >= tpb) return;
+  const int u0 = int(threadIdx.x) - tl * units;
+  const int64_t tok = p.tok0 + int64_t(blockIdx.x) * tpb + tl;
+  if (tok >= p.tok_end) return;
+  const int sq = qc_find(p.seqs, p.n_seqs, tok, [](const QcRows &s) { return s.tok; });
+  const QcRows seq = p.seqs[sq];
+  const int64_t i = tok - seq.tok, row = seq.row + i;
+  for (int u = u0; u < units; u += (tpb > 1 ? units : kRowThreads)) {
+    const bool is_v = u >= kw;
+    const int d = is_v ? c.d_v : c.d_qk, e = (is_v ? u - kw : u) * 8;   // element of the row
+    const int h = e / d, ed = e - h * d;
+    const T *src = static_cast<const T *>(is_v ? p.v : p.k) + tok * (is_v ? p.v_rs : p.k_rs) + e;
+    float x[8];
+    load8<T>(src, p.vec, x);
+    uint32_t word, param;
+    quantise8(x, word, param);
+    const int64_t at = int64_t(h) * c.rows + row;
+    (is_v ? c.v_codes : c.k_codes)[at * (d >> 3) + (ed >> 3)] = word;
+    if ((ed & 31) == 0)
+      (is_v ? c.v_scales : c.k_scales)[at * (d >> 5) + (ed >> 5)] = uint16_t(param);
+  }
+  if (u0 == 0) {
+    c.times[row] = p.ts[tok];
+    c.pos[row] = int32_t(seq.pos + i);
+    if (c.weight) c.weight[row] = 0.f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Read: the values that rows stand for, 8 per lane.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+    read_kernel(const __grid_constant__ QcRowsParams p) {
+  const QCacheView &c = p.cache;
+  const int kw = c.heads * (c.d_qk >> 3), units = kw + c.heads * (c.d_v >> 3);
+  const int tpb = units < kRowThreads ? kRowThreads / units : 1;
+  const int tl = tpb > 1 ? int(threadIdx.x) / units : 0;
+  if (tl >= tpb) return;
+  const int u0 = int(threadIdx.x) - tl * units;
+  const int64_t tok = p.tok0 + int64_t(blockIdx.x) * tpb + tl;
+  if (tok >= p.tok_end) return;
+  const int sq = qc_find(p.seqs, p.n_seqs, tok, [](const QcRows &s) { return s.tok; });
+  const int64_t row = p.seqs[sq].row + (tok - p.seqs[sq].tok);
+  for (int u = u0; u < units; u += (tpb > 1 ? units : kRowThreads)) {
+    const bool is_v = u >= kw;
+    const int d = is_v ? c.d_v : c.d_qk, e = (is_v ? u - kw : u) * 8;
+    const int h = e / d, ed = e - h * d;
+    const int64_t at = int64_t(h) * c.rows + row;
+    const uint32_t w = (is_v ? c.v_codes : c.k_codes)[at * (d >> 3) + (ed >> 3)];
+    const uint32_t param = (is_v ? c.v_scales : c.k_scales)[at * (d >> 5) + (ed >> 5)];
+    T *dst = static_cast<T *>(const_cast<void *>(is_v ? p.v : p.k)) +
+             tok * (is_v ? p.v_rs : p.k_rs) + e;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t zz, ss, o[4];
+      q4_group(param, zz, ss);
+      q4_decode_bf16(w, zz, ss, o);
+      if (p.vec) {
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          reinterpret_cast<uint16_t *>(dst)[i] = uint16_t(o[i >> 1] >> (16 * (i & 1)));
+      }
+    } else {
+      const float s = q4_scale(param);
+      const int z = int(param & 15u);
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = s * float(q4_code(w, i) - z);
+      if (p.vec) {
+        reinterpret_cast<float4 *>(dst)[0] = make_float4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<float4 *>(dst)[1] = make_float4(o[4], o[5], o[6], o[7]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dst[i] = o[i];
+      }
+    }
+  }
+}
+
+template <typename T, bool APPEND>
+cudaError_t launch_rows_t(const QcRowsParams &p, cudaStream_t st) {
+  const int units = p.cache.heads * ((p.cache.d_qk + p.cache.d_v) >> 3);
+  const int tpb = units < kRowThreads ? kRowThreads / units : 1;
+  const int64_t blocks = (p.tok_end - p.tok0 + tpb - 1) / tpb;
+  if (blocks <= 0) return cudaSuccess;
+  if constexpr (APPEND)
+    append_kernel<T><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
+  else
+    read_kernel<T><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Eviction, step 1: which row every kept row comes from.
+//
+// One CTA per sequence.  A row's key is its weight as an ordered 32-bit
+// integer.  Four passes over 8-bit digits (highest first) find the n-th
+// largest key; of the rows that share it the lowest are kept.  A kept row
+// below n stays where it is; kept rows at or behind n fill the holes below n,
+// both in ascending order, so the result does not depend on timing.
+// ---------------------------------------------------------------------------
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+
+__device__ __forceinline__ uint32_t weight_key(float w, int32_t pos, int32_t keep_pos) {
+  if (pos >= keep_pos) w = __int_as_float(0x7F800000);       // as if +inf
+  if (w != w) w = -__int_as_float(0x7F800000);               // NaN as if -inf
+  const uint32_t b = __float_as_uint(w + 0.0f);              // -0 and 0 are equal
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Exclusive sum over the block of one value per thread; *total gets the sum.
+__device__ __forceinline__ uint32_t block_excl_sum(uint32_t v, uint32_t *warp_sums,
+                                                   uint32_t *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();   // warp_sums may still be read from the call before
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  uint32_t s = warp_sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  const uint32_t before = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0u;
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kSelThreads)
+    select_kernel(const __grid_constant__ QcEvictParams p) {
+  extern __shared__ uint32_t keys[];     // [len] when it fits
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t warp_sums[kSelWarps];
+  __shared__ uint32_t pick[2];           // chosen digit, keys above it
+  const QcEvictSeq sq = p.seqs[blockIdx.x];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int32_t L = sq.len, n = sq.keep;
+  int32_t *map = p.map + sq.map0;
+  if (n >= L) {
+    for (int32_t j = tid; j < n; j += kSelThreads) map[j] = j;
+    return;
+  }
+  if (n == 0) return;
+  const float *weight = p.src.weight + sq.row;
+  const int32_t *pos = p.src.pos + sq.row;
+  const bool cached = L <= p.key_cap;
+  auto key_of = [&](int32_t j) {
+    return cached ? keys[j] : weight_key(weight[j], pos[j], sq.keep_pos);
+  };
+  if (cached) {
+    for (int32_t j = tid; j < L; j += kSelThreads)
+      keys[j] = weight_key(weight[j], pos[j], sq.keep_pos);
+  }
+  // ---- the n-th largest key, digit by digit ----
+  uint32_t prefix = 0, want = uint32_t(n);   // want: rank inside the prefix's rows
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (tid < 256) hist[tid] = 0;
+    __syncthreads();
+    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    for (int32_t j0 = 0; j0 < L; j0 += kSelThreads) {
+      const int32_t j = j0 + tid;
+      const uint32_t k = j < L ? key_of(j) : 0u;
+      const bool in = j < L && (k & mask) == prefix;
+      // equal digits of a warp are counted once (weights share exponents)
+      const uint32_t d = in ? (k >> shift) & 255u : 256u + uint32_t(lane);
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[d], uint32_t(__popc(same)));
+    }
+    __syncthreads();
+    // digits from 255 down: the one where the running count reaches want
+    const uint32_t cnt = tid < 256 ? hist[255 - tid] : 0u;
+    uint32_t total;
+    const uint32_t before = block_excl_sum(cnt, warp_sums, &total);
+    if (tid < 256 && before < want && before + cnt >= want) {
+      pick[0] = uint32_t(255 - tid);
+      pick[1] = before;
+    }
+    __syncthreads();
+    prefix |= pick[0] << shift;
+    want -= pick[1];
+    __syncthreads();
+  }
+  // ---- kept rows: every key above the threshold, and the first `want` at it ----
+  // each thread owns a run of rows; an odd run length spreads the threads'
+  // shared-memory accesses over the banks
+  const int32_t run = ((L + kSelThreads - 1) / kSelThreads) | 1;
+  const int32_t j0 = min(int64_t(tid) * run, int64_t(L)), j1 = min(int64_t(j0) + run, int64_t(L));
+  uint32_t eq = 0, total;
+  for (int32_t j = j0; j < j1; ++j) eq += key_of(j) == prefix;
+  const uint32_t eq0 = block_excl_sum(eq, warp_sums, &total);
+  uint32_t holes = 0, movers = 0, e = eq0;
+  for (int32_t j = j0; j < j1; ++j) {
+    const uint32_t k = key_of(j);
+    const bool kept = k > prefix || (k == prefix && e++ < want);
+    holes += !kept && j < n;
+    movers += kept && j >= n;
+  }
+  const uint32_t hole0 = block_excl_sum(holes, warp_sums, &total);
+  const uint32_t mover0 = block_excl_sum(movers, warp_sums, &total);
+  int32_t *mov = p.movers + sq.map0;
+  uint32_t m = mover0;
+  e = eq0;
+  for (int32_t j = j0; j < j1; ++j) {
+    const uint32_t k = key_of(j);
+    const bool kept = k > prefix || (k == prefix && e++ < want);
+    if (kept && j >= n) mov[m++] = j;
+    if (kept && j < n) map[j] = j;
+  }
+  __syncthreads();   // the movers' list is complete (same block reads it below)
+  uint32_t hl = hole0;
+  e = eq0;
+  for (int32_t j = j0; j < min(j1, n); ++j) {
+    const uint32_t k = key_of(j);
+    const bool kept = k > prefix || (k == prefix && e++ < want);
+    if (!kept) map[j] = mov[hl++];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Eviction, step 2: copy the rows.  A unit is one group (16 bytes of codes and
+// its parameter); consecutive lanes write consecutive groups.  In place only
+// the holes are written, and every source lies at or behind `keep`.
+// ---------------------------------------------------------------------------
+constexpr int kMoveThreads = 256;
+
+__global__ void __launch_bounds__(kMoveThreads)
+    move_kernel(const __grid_constant__ QcEvictParams p) {
+  const int sqi = qc_find(p.seqs, p.n_seqs, int64_t(blockIdx.x),
+                          [](const QcEvictSeq &s) { return s.block0; });
+  const QcEvictSeq sq = p.seqs[sqi];
+  const QCacheView &a = p.src, &b = p.dst;
+  const int64_t r0 = (int64_t(blockIdx.x) - sq.block0) * kQcMoveRows;
+  const int rows = int(min(int64_t(kQcMoveRows), int64_t(sq.keep) - r0));
+  const int32_t *map = p.map + sq.map0 + r0;
+  for (int r = threadIdx.x; r < rows; r += kMoveThreads) {
+    const int32_t m = map[r];
+    if (p.in_place && m == r0 + r) continue;
+    b.times[sq.dst_row + r0 + r] = a.times[sq.row + m];
+    b.pos[sq.dst_row + r0 + r] = a.pos[sq.row + m];
+    b.weight[sq.dst_row + r0 + r] = a.weight[sq.row + m];
+  }
+  const int gk = a.d_qk >> 5, gv = a.d_v >> 5;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int gs = part ? gv : gk;
+    const uint4 *ac = reinterpret_cast<const uint4 *>(part ? a.v_codes : a.k_codes);
+    uint4 *bc = reinterpret_cast<uint4 *>(part ? b.v_codes : b.k_codes);
+    const uint16_t *as = part ? a.v_scales : a.k_scales;
+    uint16_t *bs = part ? b.v_scales : b.k_scales;
+    const int per_head = rows * gs, all = per_head * a.heads;
+    for (int x = threadIdx.x; x < all; x += kMoveThreads) {
+      const int h = x / per_head, y = x - h * per_head, r = y / gs, g = y - r * gs;
+      const int32_t m = map[r];
+      if (p.in_place && m == r0 + r) continue;
+      const int64_t from = (int64_t(h) * a.rows + sq.row + m) * gs + g;
+      const int64_t to = (int64_t(h) * b.rows + sq.dst_row + r0 + r) * gs + g;
+      bc[to] = ac[from];
+      bs[to] = as[from];
+    }
+  }
+}
+
+}  // namespace qc
+
+cudaError_t launch_qcache_append(const QcRowsParams &p, bool bf16, cudaStream_t st) {
+  return bf16 ? qc::launch_rows_t<__nv_bfloat16, true>(p, st)
+              : qc::launch_rows_t<float, true>(p, st);
+}
+cudaError_t launch_qcache_read(const QcRowsParams &p, bool bf16, cudaStream_t st) {
+  return bf16 ? qc::launch_rows_t<__nv_bfloat16, false>(p, st)
+              : qc::launch_rows_t<float, false>(p, st);
+}
+
+cudaError_t launch_qcache_evict(const QcEvictParams &p, int32_t max_len, int64_t move_blocks,
+                                cudaStream_t st) {
+  using namespace qc;
+  static PerDeviceOnce attr;
+  cudaError_t e = set_smem_once(attr, select_kernel, kQcSelectKeys * sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  const int32_t keys = max_len < kQcSelectKeys ? max_len : kQcSelectKeys;
+  QcEvictParams q = p;
+  q.key_cap = keys;
+  select_kernel<<<unsigned(p.n_seqs), kSelThreads, size_t(keys) * sizeof(uint32_t), st>>>(q);
+  count_launch();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || move_blocks == 0) return e;
+  move_kernel<<<unsigned(move_blocks), kMoveThreads, 0, st>>>(q);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace hstu

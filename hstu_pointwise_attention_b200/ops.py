@@ -37,6 +37,10 @@ EXPORTED = [
     "hstu_attn_candidates_workspace_size", "hstu_attn_fwd_candidates",
     "hstu_layer_candidates_workspace_size", "hstu_layer_fwd_candidates",
     "hstu_debug_trace_read", "hstu_debug_trace_clear", "hstu_debug_plan",
+    "hstu_qcache_append", "hstu_qcache_read", "hstu_qcache_evict_workspace_size",
+    "hstu_qcache_evict", "hstu_attn_candidates_qcache_workspace_size",
+    "hstu_attn_fwd_candidates_qcache", "hstu_layer_candidates_qcache_workspace_size",
+    "hstu_layer_fwd_candidates_qcache",
 ]
 
 
@@ -65,6 +69,15 @@ class LayerParams(ctypes.Structure):
     _fields_ = [("attn", AttnParams), ("d_model", ctypes.c_int32),
                 ("residual", ctypes.c_int32), ("ln_eps", ctypes.c_float),
                 ("reserved", ctypes.c_int32)]
+
+
+class _QCacheStruct(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("num_heads", ctypes.c_int32), ("d_qk", ctypes.c_int32),
+                ("d_v", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("times", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p)]
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -110,12 +123,29 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.hstu_debug_trace_clear.restype = ctypes.c_int
     lib.hstu_debug_plan.argtypes = [P, vp, vp, i32, vp, vp, vp, vp]
     lib.hstu_debug_plan.restype = ctypes.c_int
+    f32, QP = ctypes.c_float, ctypes.POINTER(_QCacheStruct)
+    lib.hstu_qcache_append.argtypes = [QP, i32, i32] + [vp] * 4 + [i64, vp, i64, vp, vp]
+    lib.hstu_qcache_read.argtypes = [QP, i32, i32, vp, vp, vp, i64, vp, i64, vp]
+    lib.hstu_qcache_evict_workspace_size.argtypes = [i32, vp, vp, ctypes.POINTER(sz)]
+    lib.hstu_qcache_evict.argtypes = [QP, QP, i32] + [vp] * 6 + [sz, vp]
+    lib.hstu_attn_candidates_qcache_workspace_size.argtypes = [P, vp, vp, i32,
+                                                               ctypes.POINTER(sz)]
+    lib.hstu_attn_fwd_candidates_qcache.argtypes = [P, QP] + [vp] * 10 + [i32, f32, vp, vp, sz,
+                                                                         vp]
+    lib.hstu_layer_candidates_qcache_workspace_size.argtypes = [LP, vp, vp, i32,
+                                                                ctypes.POINTER(sz)]
+    lib.hstu_layer_fwd_candidates_qcache.argtypes = [LP, QP] + [vp] * 14 + [i32, f32, vp, vp, vp,
+                                                                           sz, vp]
     for name in ("hstu_attn_workspace_size", "hstu_attn_fwd", "hstu_attn_bwd",
                  "hstu_layer_workspace_size", "hstu_layer_fwd", "hstu_debug_buckets",
                  "hstu_get_device_error", "hstu_layer_bwd_workspace_size", "hstu_layer_bwd",
                  "hstu_layer_fwd_keep_proj", "hstu_attn_candidates_workspace_size",
                  "hstu_attn_fwd_candidates", "hstu_layer_candidates_workspace_size",
-                 "hstu_layer_fwd_candidates"):
+                 "hstu_layer_fwd_candidates", "hstu_qcache_append", "hstu_qcache_read",
+                 "hstu_qcache_evict_workspace_size", "hstu_qcache_evict",
+                 "hstu_attn_candidates_qcache_workspace_size", "hstu_attn_fwd_candidates_qcache",
+                 "hstu_layer_candidates_qcache_workspace_size",
+                 "hstu_layer_fwd_candidates_qcache"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -148,6 +178,8 @@ def _host_i32(a) -> Optional[np.ndarray]:
 
 def _row_stride(t: torch.Tensor, H: int, d: int, name: str) -> int:
     """t is [T, H, d] (or a [T, H*d] view) with contiguous heads."""
+    if t.shape[0] == 0 and tuple(t.shape[1:]) in ((H, d), (H * d,)):
+        return H * d        # no rows: strides carry no meaning
     if t.dim() == 3:
         if t.shape[1] != H or t.shape[2] != d or t.stride(2) != 1 or t.stride(1) != d:
             raise ValueError(f"{name}: expected [T, {H}, {d}] with contiguous heads")
@@ -410,6 +442,289 @@ def layer_fwd_candidates(x_cand, w1, b1, ln_gamma, ln_beta, w2, b2, rab_pos, rab
         _ptr(cand_timestamps), _ptr(x_cand), _ptr(w1), _ptr(b1), _ptr(ln_gamma), _ptr(ln_beta),
         _ptr(w2), _ptr(b2), _ptr(rab_pos), _ptr(rab_time), _ptr(hist_proj), _ptr(out),
         _ptr(ws), ws.numel(), _stream(stream)), "hstu_layer_fwd_candidates")
+    return out
+
+
+class QuantCache:
+    """The buffers of one layer's 4-bit history cache (include/hstu.h,
+    hstu_qcache_t): k_codes, v_codes uint8 [H, rows, d / 2]; k_scales, v_scales
+    int16 [H, rows, d / 32]; times int64, pos int32, weight float32 [rows]
+    (weight may be None where no call updates or reads it).  Contiguous, on one
+    CUDA device.  ``QuantCache.empty`` allocates them."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, times, pos, weight=None):
+        H, rows, half_k = k_codes.shape
+        half_v = v_codes.shape[2]
+        want = [("k_codes", k_codes, (torch.uint8,), (H, rows, half_k)),
+                ("k_scales", k_scales, (torch.int16, torch.uint16), (H, rows, half_k // 16)),
+                ("v_codes", v_codes, (torch.uint8,), (H, rows, half_v)),
+                ("v_scales", v_scales, (torch.int16, torch.uint16), (H, rows, half_v // 16)),
+                ("times", times, (torch.int64,), (rows,)), ("pos", pos, (torch.int32,), (rows,)),
+                ("weight", weight, (torch.float32,), (rows,))]
+        for name, t, dtypes, shape in want:
+            if t is None and name == "weight":
+                continue
+            if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name}: expected contiguous {dtypes[0]} {list(shape)}, got "
+                                 f"{t.dtype} {list(t.shape)}")
+            if t.device != k_codes.device:
+                raise ValueError(f"{name} is on {t.device}, k_codes on {k_codes.device}")
+        if half_k % 16 or half_v % 16:
+            raise ValueError("head sizes must be multiples of 32")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
+                                                                     v_scales)
+        self.times, self.pos, self.weight = times, pos, weight
+        self.rows, self.num_heads, self.d_qk, self.d_v = rows, H, 2 * half_k, 2 * half_v
+        self.device = k_codes.device
+        self._c = _QCacheStruct(rows, H, self.d_qk, self.d_v, 0, _ptr(k_codes), _ptr(k_scales),
+                                _ptr(v_codes), _ptr(v_scales), _ptr(times), _ptr(pos),
+                                _ptr(weight))
+
+    @classmethod
+    def empty(cls, rows, num_heads, d_qk, d_v, device="cuda"):
+        z = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)
+        return cls(z((num_heads, rows, d_qk // 2), torch.uint8),
+                   z((num_heads, rows, d_qk // 32), torch.int16),
+                   z((num_heads, rows, d_v // 2), torch.uint8),
+                   z((num_heads, rows, d_v // 32), torch.int16), z((rows,), torch.int64),
+                   z((rows,), torch.int32), z((rows,), torch.float32))
+
+
+class _Launch:
+    """Makes the tensors' device current for a call, and the call's stream the
+    one its own allocations belong to (a workspace is then reused only behind
+    the work that uses it)."""
+
+    def __init__(self, device, stream, *tensors):
+        if device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got {device}")
+        for t in tensors:
+            if t is not None and t.device != device:
+                raise ValueError(f"tensors on {t.device} and {device}")
+        self._ctx = []
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream is not None:
+            self._ctx.append(torch.cuda.stream(stream))
+        elif device.index is not None and device.index != torch.cuda.current_device():
+            self._ctx.append(torch.cuda.device(device))
+        self._stream = stream
+
+    def __enter__(self):
+        for c in self._ctx:
+            c.__enter__()
+        return _stream(self._stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+        return False
+
+
+def _host_vec(a, n, dtype, name):
+    a = _host_i64(a) if dtype is np.int64 else _host_i32(a)
+    if a.shape != (n,):
+        raise ValueError(f"{name}: expected {n} entries, got shape {a.shape}")
+    return a
+
+
+def _typed(t, dtype, name):
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype}, got {t.dtype}")
+    return t
+
+
+def _act_dtype(t, name):
+    if t.dtype == torch.float32:
+        return F32
+    if t.dtype == torch.bfloat16:
+        return BF16
+    raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+
+
+def qcache_append(cache, k, v, timestamps, tok_offsets, rows, pos, *, stream=None):
+    """hstu_qcache_append: quantise new tokens' keys and values [T, H, d] into
+    the cache; sequence b's tokens tok_offsets[b]..tok_offsets[b + 1] go to rows
+    rows[b].. at positions pos[b]..."""
+    off = _host_i64(tok_offsets)
+    B = len(off) - 1
+    rows, pos = _host_vec(rows, B, np.int64, "rows"), _host_vec(pos, B, np.int32, "pos")
+    dt = _act_dtype(k, "k")
+    if v.dtype != k.dtype:
+        raise ValueError(f"v dtype {v.dtype} != k dtype {k.dtype}")
+    T = int(off[-1]) if B else 0
+    if k.shape[0] < T or v.shape[0] < T or timestamps.shape[0] < T:
+        raise ValueError(f"k, v and timestamps need {T} tokens")
+    k_rs = _row_stride(k, cache.num_heads, cache.d_qk, "k")
+    v_rs = _row_stride(v, cache.num_heads, cache.d_v, "v")
+    _typed(timestamps, torch.int64, "timestamps")
+    with _Launch(cache.device, stream, k, v, timestamps) as st:
+        _check(LIB.hstu_qcache_append(ctypes.byref(cache._c), dt, B, off.ctypes.data,
+                                      rows.ctypes.data, pos.ctypes.data, _ptr(k), k_rs, _ptr(v),
+                                      v_rs, _ptr(timestamps), st), "hstu_qcache_append")
+
+
+def qcache_read(cache, rows, lens, *, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """hstu_qcache_read: (k, v) [sum lens, H, d], the values that rows stand for."""
+    lens = _host_i64(lens)
+    rows = _host_vec(rows, len(lens), np.int64, "rows")
+    T = int(lens.sum())
+    with _Launch(cache.device, stream, k, v) as st:
+        if k is None:
+            k = torch.empty((T, cache.num_heads, cache.d_qk), dtype=dtype, device=cache.device)
+        if v is None:
+            v = torch.empty((T, cache.num_heads, cache.d_v), dtype=dtype, device=cache.device)
+        if k.dtype != v.dtype or k.shape[0] < T or v.shape[0] < T:
+            raise ValueError(f"k and v must share a dtype and hold {T} tokens")
+        k_rs = _row_stride(k, cache.num_heads, cache.d_qk, "k")
+        v_rs = _row_stride(v, cache.num_heads, cache.d_v, "v")
+        _check(LIB.hstu_qcache_read(ctypes.byref(cache._c), _act_dtype(k, "k"), len(lens),
+                                    rows.ctypes.data, lens.ctypes.data, _ptr(k), k_rs, _ptr(v),
+                                    v_rs, st), "hstu_qcache_read")
+    return k, v
+
+
+def qcache_evict(cache, rows, lens, budgets, keep_pos, *, dst=None, dst_rows=None,
+                 workspace=None, stream=None):
+    """hstu_qcache_evict: keep each sequence's budgets[b] most used rows, in
+    place or (dst, dst_rows) in another cache.  Returns the new lengths."""
+    lens = _host_i64(lens)
+    B = len(lens)
+    rows = _host_vec(rows, B, np.int64, "rows")
+    budgets = _host_vec(budgets, B, np.int64, "budgets")
+    keep_pos = _host_vec(keep_pos, B, np.int32, "keep_pos")
+    if (dst is None) != (dst_rows is None):
+        raise ValueError("dst and dst_rows go together")
+    if cache.weight is None or (dst is not None and dst.weight is None):
+        raise ValueError("evicting needs caches with weights")
+    if dst is not None and dst.device != cache.device:
+        raise ValueError(f"caches on {cache.device} and {dst.device}")
+    to = cache if dst is None else dst
+    to_rows = rows if dst is None else _host_vec(dst_rows, B, np.int64, "dst_rows")
+    n = ctypes.c_size_t(0)
+    _check(LIB.hstu_qcache_evict_workspace_size(B, lens.ctypes.data, budgets.ctypes.data,
+                                                ctypes.byref(n)),
+           "hstu_qcache_evict_workspace_size")
+    with _Launch(cache.device, stream, workspace) as st:
+        ws = _workspace(int(n.value), cache.device, workspace)
+        _check(LIB.hstu_qcache_evict(
+            ctypes.byref(cache._c), ctypes.byref(to._c), B, rows.ctypes.data, lens.ctypes.data,
+            budgets.ctypes.data, keep_pos.ctypes.data, to_rows.ctypes.data, _ptr(ws),
+            ws.numel() * ws.element_size(), st), "hstu_qcache_evict")
+    return np.minimum(lens, budgets)
+
+
+def _check_cache_heads(cache, H, d_qk, d_v):
+    if (cache.num_heads, cache.d_qk, cache.d_v) != (H, d_qk, d_v):
+        raise ValueError(f"the cache holds {cache.num_heads} heads of {cache.d_qk} / "
+                         f"{cache.d_v}, the call {H} of {d_qk} / {d_v}")
+
+
+def attn_fwd_candidates_qcache(q, k, v, cache, cache_rows, cache_lens, cand_offsets, cand_pos,
+                               cand_timestamps, rab_pos, rab_time, *, max_seq_len,
+                               time_bucket_sub_bits, alpha=None, silu_scale=None,
+                               rab_per_head=False, weight_decay=None, impl="auto", out=None,
+                               workspace=None, stream=None):
+    """hstu_attn_fwd_candidates_qcache: out[Tc, H, d_v] for candidates against
+    the 4-bit cache.  weight_decay: None leaves cache.weight alone; a number
+    updates it (weight <- weight_decay weight + this call's weights)."""
+    Tc, H = q.shape[0], q.shape[1]
+    d_v = v.shape[-1] if v.dim() == 3 else v.shape[1] // H
+    coff = _host_i64(cand_offsets)
+    B = len(coff) - 1
+    rows = _host_vec(cache_rows, B, np.int64, "cache_rows")
+    lens = _host_vec(cache_lens, B, np.int64, "cache_lens")
+    pos = _host_vec(cand_pos, B, np.int32, "cand_pos")
+    _check_cache_heads(cache, H, q.shape[2], d_v)
+    n_c = int(coff[-1]) if B else 0
+    if min(Tc, k.shape[0], v.shape[0], cand_timestamps.shape[0]) < n_c:
+        raise ValueError(f"q, k, v and cand_timestamps need {n_c} candidates")
+    if weight_decay is not None and cache.weight is None:
+        raise ValueError("weight_decay needs a cache with weights")
+    _typed(cand_timestamps, torch.int64, "cand_timestamps")
+    for t, name in ((rab_pos, "rab_pos"), (rab_time, "rab_time")):
+        _typed(t, torch.float32, name)
+        if tuple(t.shape[:-1]) != ((H,) if rab_per_head else ()):
+            raise ValueError(f"{name}: unexpected shape {list(t.shape)}")
+    with _Launch(cache.device, stream, q, k, v, cand_timestamps, rab_pos, rab_time, out,
+                 workspace) as st:
+        if out is None:
+            out = torch.empty((Tc, H, d_v), dtype=q.dtype, device=q.device)
+        if out.shape[0] < n_c or out.dtype != q.dtype:
+            raise ValueError(f"out must hold {n_c} candidates of {q.dtype}")
+        p = make_params(q, k, v, coff, max_seq_len=max_seq_len,
+                        num_pos_buckets=rab_pos.shape[-1], num_time_buckets=rab_time.shape[-1],
+                        time_bucket_sub_bits=time_bucket_sub_bits, alpha=alpha,
+                        silu_scale=silu_scale, rab_per_head=rab_per_head, impl=impl, out=out)
+        upd, decay = int(weight_decay is not None), float(weight_decay or 0.0)
+        n = ctypes.c_size_t(0)
+        _check(LIB.hstu_attn_candidates_qcache_workspace_size(
+            ctypes.byref(p), lens.ctypes.data, coff.ctypes.data, upd, ctypes.byref(n)),
+            "hstu_attn_candidates_qcache_workspace_size")
+        ws = _workspace(int(n.value), q.device, workspace)
+        _check(LIB.hstu_attn_fwd_candidates_qcache(
+            ctypes.byref(p), ctypes.byref(cache._c), rows.ctypes.data, lens.ctypes.data,
+            coff.ctypes.data, pos.ctypes.data, _ptr(cand_timestamps), _ptr(q), _ptr(k), _ptr(v),
+            _ptr(rab_pos), _ptr(rab_time), upd, decay, _ptr(out), _ptr(ws),
+            ws.numel() * ws.element_size(), st), "hstu_attn_fwd_candidates_qcache")
+    return out
+
+
+def layer_fwd_candidates_qcache(x_cand, w1, b1, ln_gamma, ln_beta, w2, b2, rab_pos, rab_time,
+                                cache, cache_rows, cache_lens, cand_offsets, cand_pos,
+                                cand_timestamps, *, num_heads, d_qk, d_v, max_seq_len,
+                                time_bucket_sub_bits, alpha=None, silu_scale=None, ln_eps=1e-5,
+                                residual=True, weight_decay=None, out=None, proj_out=None,
+                                workspace=None, stream=None):
+    """hstu_layer_fwd_candidates_qcache: one layer on candidates against the
+    4-bit cache of its history.  proj_out [Tc, N1] bf16 (optional) receives the
+    candidates' projection [U|V|Q|K]."""
+    Tc, D = x_cand.shape
+    H, F = num_heads, num_heads * d_v
+    n1 = 2 * (F + H * d_qk)
+    coff = _host_i64(cand_offsets)
+    B = len(coff) - 1
+    rows = _host_vec(cache_rows, B, np.int64, "cache_rows")
+    lens = _host_vec(cache_lens, B, np.int64, "cache_lens")
+    pos = _host_vec(cand_pos, B, np.int32, "cand_pos")
+    _check_cache_heads(cache, H, d_qk, d_v)
+    n_c = int(coff[-1]) if B else 0
+    bf, f32 = torch.bfloat16, torch.float32
+    want = [("x_cand", x_cand, bf, (Tc, D)), ("w1", w1, bf, (n1, D)), ("b1", b1, f32, (n1,)),
+            ("ln_gamma", ln_gamma, f32, (F,)), ("ln_beta", ln_beta, f32, (F,)),
+            ("w2", w2, bf, (D, F)), ("b2", b2, f32, (D,)),
+            ("rab_pos", rab_pos, f32, tuple(rab_pos.shape[-1:])),
+            ("rab_time", rab_time, f32, tuple(rab_time.shape[-1:])), ("out", out, bf, (Tc, D)),
+            ("proj_out", proj_out, bf, (Tc, n1))]
+    for name, t, dt, shape in want:
+        if t is not None and (t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected contiguous {dt} {list(shape)}, got {t.dtype} "
+                             f"{list(t.shape)}")
+    if min(Tc, cand_timestamps.shape[0]) < n_c:
+        raise ValueError(f"x_cand and cand_timestamps need {n_c} candidates")
+    if weight_decay is not None and cache.weight is None:
+        raise ValueError("weight_decay needs a cache with weights")
+    _typed(cand_timestamps, torch.int64, "cand_timestamps")
+    with _Launch(cache.device, stream, x_cand, w1, b1, ln_gamma, ln_beta, w2, b2, rab_pos,
+                 rab_time, cand_timestamps, out, proj_out, workspace) as st:
+        if out is None:
+            out = torch.empty((Tc, D), dtype=bf, device=x_cand.device)
+        lp, _, _ = _layer_params(x_cand, rab_pos, rab_time, coff, None, num_heads=H, d_qk=d_qk,
+                                 d_v=d_v, max_seq_len=max_seq_len,
+                                 time_bucket_sub_bits=time_bucket_sub_bits, alpha=alpha,
+                                 silu_scale=silu_scale, ln_eps=ln_eps, residual=residual)
+        upd, decay = int(weight_decay is not None), float(weight_decay or 0.0)
+        n = ctypes.c_size_t(0)
+        _check(LIB.hstu_layer_candidates_qcache_workspace_size(
+            ctypes.byref(lp), lens.ctypes.data, coff.ctypes.data, upd, ctypes.byref(n)),
+            "hstu_layer_candidates_qcache_workspace_size")
+        ws = _workspace(int(n.value), x_cand.device, workspace)
+        _check(LIB.hstu_layer_fwd_candidates_qcache(
+            ctypes.byref(lp), ctypes.byref(cache._c), rows.ctypes.data, lens.ctypes.data,
+            coff.ctypes.data, pos.ctypes.data, _ptr(cand_timestamps), _ptr(x_cand), _ptr(w1),
+            _ptr(b1), _ptr(ln_gamma), _ptr(ln_beta), _ptr(w2), _ptr(b2), _ptr(rab_pos),
+            _ptr(rab_time), upd, decay, _ptr(out), _ptr(proj_out), _ptr(ws),
+            ws.numel() * ws.element_size(), st), "hstu_layer_fwd_candidates_qcache")
     return out
 
 

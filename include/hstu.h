@@ -260,6 +260,157 @@ hstu_status_t hstu_layer_fwd_candidates(
     const float *rab_pos, const float *rab_time, const void *hist_proj, void *y_cand,
     void *workspace, size_t workspace_bytes, void *stream);
 
+/* A cache of history keys and values held in 4 bits, with the attention, the
+ * layer and the trimming that work on it.
+ *
+ * The cached history of hstu_attn_fwd_candidates is the bf16 projection of the
+ * history pass, 2 bytes per value, and what bounds how many users one GPU
+ * serves.  Here a row (one history token) keeps only its keys and values, at
+ * 4.5 bits per value, together with its time, its position in the user's
+ * history, and the attention weight it has received, so that a user's rows can
+ * be trimmed to the ones that matter (hstu_qcache_evict) while every remaining
+ * row keeps its exact position and time distance.
+ *
+ * Format: groups of 32 values along a head's row share a scale s and a zero
+ * point z; a value is s (q - z), q in 0..15.  With lo = min(0, min x) and
+ * hi = max(0, max x) over the group: s is the smallest float with 4 significant
+ * bits, s >= 2^-126, 15 s >= hi - lo; z = rne(-lo / s);
+ * q = clamp(rne(x / s) + z, 0, 15), exact quotients, ties to even.  So zero is
+ * kept exactly, |error| <= s / 2 (s at the one code that the clamp can cut),
+ * and every stored value is exact in bf16.  A group of zeros has s = z = q = 0.
+ * NaN is stored as 0, magnitudes are held to 2^126.
+ *   codes   [H][rows][d / 2] bytes: 32-bit words of 8 codes, nibble i of a word
+ *           is element 2 i, nibble i + 4 element 2 i + 1 (i = 0..3).
+ *   scales  [H][rows][d / 32] 16-bit: the upper 12 bits of s as a bfloat16,
+ *           z in the low 4 bits.
+ * All buffers are the caller's (device memory).  Rows are addressed per
+ * sequence by host arrays: sequence b owns rows [rows_host[b], + its length);
+ * their order within the region carries no meaning.  Alignment: codes 16
+ * bytes, the others their element.  weight may be NULL where no call updates
+ * or reads it. */
+typedef struct {
+  int64_t rows;                  /* capacity, 0..2^40 */
+  int32_t num_heads;             /* H, 1..4096 */
+  int32_t d_qk, d_v;             /* 32..256, multiples of 32 */
+  int32_t reserved;
+  void *k_codes;                 /* [H][rows][d_qk / 2] bytes */
+  uint16_t *k_scales;            /* [H][rows][d_qk / 32] */
+  void *v_codes;                 /* [H][rows][d_v / 2] bytes */
+  uint16_t *v_scales;            /* [H][rows][d_v / 32] */
+  int64_t *times;                /* [rows] seconds */
+  int32_t *pos;                  /* [rows] position in the user's history */
+  float *weight;                 /* [rows] accumulated attention weight */
+} hstu_qcache_t;
+
+/* Stores new tokens: quantises their keys and values into the cache and sets
+ * time, position and a weight of 0.
+ *  dtype             hstu_dtype_t of k and v.
+ *  tok_offsets_host  [batch + 1]: tokens of sequence b are rows
+ *                    [tok_offsets[b], tok_offsets[b+1]) of k, v, timestamps.
+ *  rows_host         [batch]: first cache row of sequence b's tokens; the
+ *                    regions written must not overlap.
+ *  pos_host          [batch]: position of its first token (then + 1 each).
+ *  k, v              [T][row_stride] as for hstu_attn_fwd (any alignment of
+ *                    the element; 16 bytes and strides in 16-byte steps are
+ *                    read faster).  timestamps_dev [T] int64.
+ * No workspace.  Errors: HSTU_ERR_INVALID_ARG, HSTU_ERR_UNSUPPORTED (2^31
+ * tokens or more), HSTU_ERR_CUDA. */
+hstu_status_t hstu_qcache_append(const hstu_qcache_t *cache, int32_t dtype, int32_t batch,
+                                 const int64_t *tok_offsets_host, const int64_t *rows_host,
+                                 const int32_t *pos_host, const void *k, int64_t k_row_stride,
+                                 const void *v, int64_t v_row_stride,
+                                 const int64_t *timestamps_dev, void *stream);
+
+/* The values that rows stand for: sequence b's lens_host[b] rows from
+ * rows_host[b] on, all sequences one behind the other, into k and v
+ * [sum lens][row_stride] of `dtype` (exact in both).  Errors as
+ * hstu_qcache_append. */
+hstu_status_t hstu_qcache_read(const hstu_qcache_t *cache, int32_t dtype, int32_t batch,
+                               const int64_t *rows_host, const int64_t *lens_host, void *k,
+                               int64_t k_row_stride, void *v, int64_t v_row_stride, void *stream);
+
+/* hstu_attn_fwd_candidates over the 4-bit cache.  Each of sequence b's
+ * candidates i (or its one new event: the form for single tokens) sees the
+ * sequence's cached rows j and itself, from position P_b = cand_pos_host[b]:
+ *   x_ij = alpha <q_i, k_j> + rab_pos[min(nb_p - 1, max(0, P_b - pos_j))]
+ *                           + rab_time[min(nb_t - 1, tb(t_i - t_j))]
+ *   out_i = silu_scale (sum_j SiLU(x_ij) v_j + SiLU(x_ii) v_i)
+ * with the candidate's own pair at distance 0.  With update_weight != 0 the
+ * rows of every sequence of the call (also one without candidates) get
+ *   weight_j <- weight_decay weight_j + silu_scale sum_{i, heads} |SiLU(x_ij)|
+ * (weight_decay 0: the old weight is not read); sums run in float32 in a fixed
+ * order, so equal calls give equal bits.  A table entry of -inf (or below
+ * -1e30) hides its bucket.  k_j, v_j are exactly the stored values; the
+ * arithmetic is float32.
+ *  params            as hstu_attn_fwd_candidates (mask is ignored); num_heads,
+ *                    d_qk, d_v those of the cache; max_seq_len bounds the
+ *                    cached rows plus candidates of a sequence.
+ *  cache_rows_host, cache_lens_host  [B]: the sequence's rows (regions may
+ *                    overlap unless update_weight).
+ *  cand_offsets_host [B + 1], cand_timestamps_dev, q, k, v, out: the
+ *                    candidates, any element alignment; every candidate row
+ *                    of out is written, no other.
+ *  workspace         >= hstu_attn_candidates_qcache_workspace_size bytes,
+ *                    256-byte aligned, one per stream. */
+hstu_status_t hstu_attn_candidates_qcache_workspace_size(const hstu_attn_params_t *params,
+                                                         const int64_t *cache_lens_host,
+                                                         const int64_t *cand_offsets_host,
+                                                         int32_t update_weight, size_t *bytes);
+
+hstu_status_t hstu_attn_fwd_candidates_qcache(
+    const hstu_attn_params_t *params, const hstu_qcache_t *cache, const int64_t *cache_rows_host,
+    const int64_t *cache_lens_host, const int64_t *cand_offsets_host,
+    const int32_t *cand_pos_host, const int64_t *cand_timestamps_dev, const void *q,
+    const void *k, const void *v, const float *rab_pos, const float *rab_time,
+    int32_t update_weight, float weight_decay, void *out, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/* Trims every sequence to its budgets_host[b] most used rows (all of them when
+ * it has no more).  Rows with pos >= keep_pos_host[b] count as if their weight
+ * were +inf, NaN as -inf; of rows with equal weight those with the lower index
+ * are kept.  With n = min(length, budget): a kept row below n stays at its
+ * index, the kept rows at n and behind fill the holes below n, both in
+ * ascending order, so the result is determined and only as many rows move as
+ * leave the front.  Codes, scales, time, position and weight move together.
+ *  dst               src itself (every pointer, and dst_rows_host equal to
+ *                    rows_host): in place, rows behind n are left as they
+ *                    were.  Or another cache that shares no memory with src:
+ *                    the n rows go to [dst_rows_host[b], + n) there.
+ *  workspace         >= hstu_qcache_evict_workspace_size bytes, 256-aligned.
+ * Regions (in place: of the sequences; else: the ones written) must not
+ * overlap. */
+hstu_status_t hstu_qcache_evict_workspace_size(int32_t batch, const int64_t *lens_host,
+                                               const int64_t *budgets_host, size_t *bytes);
+
+hstu_status_t hstu_qcache_evict(const hstu_qcache_t *src, const hstu_qcache_t *dst,
+                                int32_t batch, const int64_t *rows_host,
+                                const int64_t *lens_host, const int64_t *budgets_host,
+                                const int32_t *keep_pos_host, const int64_t *dst_rows_host,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* hstu_layer_fwd_candidates over the 4-bit cache of that layer's history:
+ *   [U|V|Q|K]_c = SiLU(x_cand W1^T + b1)
+ *   A_c = hstu_attn_fwd_candidates_qcache(Q_c, K_c, V_c)
+ *   y_cand = x_cand + (LayerNorm(A_c) (.) U_c) W2^T + b2   (residual as flagged)
+ *  proj_out  may be NULL; else [Tc][N1] bf16, 16-byte aligned, receives the
+ *            projection, whose K and V columns hstu_qcache_append stores once
+ *            a candidate has become an event.
+ *  Other arguments as hstu_layer_fwd_candidates and
+ *  hstu_attn_fwd_candidates_qcache; d_qk, d_v multiples of 32. */
+hstu_status_t hstu_layer_candidates_qcache_workspace_size(const hstu_layer_params_t *params,
+                                                          const int64_t *cache_lens_host,
+                                                          const int64_t *cand_offsets_host,
+                                                          int32_t update_weight, size_t *bytes);
+
+hstu_status_t hstu_layer_fwd_candidates_qcache(
+    const hstu_layer_params_t *params, const hstu_qcache_t *cache,
+    const int64_t *cache_rows_host, const int64_t *cache_lens_host,
+    const int64_t *cand_offsets_host, const int32_t *cand_pos_host,
+    const int64_t *cand_timestamps_dev, const void *x_cand, const void *w1, const float *b1,
+    const float *ln_gamma, const float *ln_beta, const void *w2, const float *b2,
+    const float *rab_pos, const float *rab_time, int32_t update_weight, float weight_decay,
+    void *y_cand, void *proj_out, void *workspace, size_t workspace_bytes, void *stream);
+
 /* One HSTU layer backward (training): the gradients of hstu_layer_fwd's y
  * with respect to its input and every parameter, given dy = dL/dy.  By the
  * chain rule through the layer's steps in reverse:
