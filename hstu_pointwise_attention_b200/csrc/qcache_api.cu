@@ -176,6 +176,7 @@ hstu_status_t check_attn(const AttnArgs &a, bool have_cache) {
 // One launch's share of the call: sequences [b0, b0 + n_seqs), their key
 // ranges and their places in the scratch buffers.
 struct Share {
+  bool tc;                   // tensor cores
   int nq, plane;             // candidates per CTA; candidates per weight partial
   int64_t acc_rows, wp;      // rows of `acc` (d_v floats each) and floats of `wpart` it uses
 };
@@ -239,9 +240,19 @@ void make_share(const AttnArgs &a, int32_t b0, int64_t acc_row, int64_t wp, QcAt
   const hstu_attn_params_t &ap = *a.p;
   const int64_t H = ap.num_heads;
   p.n_seqs = std::min(kQcMaxSeqs, ap.batch - b0);
-  s.nq = kQcSimtQueries;
-  s.plane = kQcSimtQueries;
-  p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148 * 4, 1);
+  s.tc = ap.dtype == HSTU_BF16 && ap.impl == HSTU_IMPL_AUTO && ap.d_qk == ap.d_v &&
+         (ap.d_qk == 64 || ap.d_qk == 128);
+  if (s.tc) {
+    // 64 candidates per CTA while no sequence has more
+    int64_t most = 0;
+    for (int32_t b = b0; b < b0 + p.n_seqs; ++b) most = std::max(most, a.coff[b + 1] - a.coff[b]);
+    s.nq = most <= 64 ? 64 : 128;
+    s.plane = s.nq / 2;
+    p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148, 3);
+  } else {
+    s.nq = s.plane = kQcSimtQueries;
+    p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148 * 4, 1);
+  }
   s.acc_rows = s.wp = 0;
   int64_t items = 0, fin = 0, wrow = 0;
   for (int32_t i = 0; i < p.n_seqs; ++i) {
@@ -338,7 +349,9 @@ hstu_status_t run_attn(const AttnArgs &a, const int64_t *cand_ts, const void *q,
     rows += s.acc_rows;
     wp += s.wp;
     if (p.items > 0) {
-      if (launch_qcache_attn_simt(p, bf16, st) != cudaSuccess) return HSTU_ERR_CUDA;
+      const cudaError_t e = s.tc ? launch_qcache_attn_tc(p, s.nq, st)
+                                 : launch_qcache_attn_simt(p, bf16, st);
+      if (e != cudaSuccess) return HSTU_ERR_CUDA;
       p.clear_err = false;
     }
     if (launch_qcache_finish(p, bf16, s.plane, st) != cudaSuccess) return HSTU_ERR_CUDA;

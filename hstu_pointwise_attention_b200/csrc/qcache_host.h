@@ -80,6 +80,8 @@ cudaError_t launch_qcache_append(const QcRowsParams &p, bool bf16, cudaStream_t 
 cudaError_t launch_qcache_read(const QcRowsParams &p, bool bf16, cudaStream_t st);
 cudaError_t launch_qcache_evict(const QcEvictParams &p, int32_t max_len, int64_t move_blocks,
                                 cudaStream_t st);
+// Tensor cores: bf16, d_qk = d_v in {64, 128}; nq = 64 or 128 candidates per CTA.
+cudaError_t launch_qcache_attn_tc(const QcAttnParams &p, int nq, cudaStream_t st);
 cudaError_t launch_qcache_attn_simt(const QcAttnParams &p, bool bf16, cudaStream_t st);
 // Sums the partial outputs of split sequences and the weight partials
 // (planes of `plane` candidates each).

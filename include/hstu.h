@@ -341,7 +341,8 @@ hstu_status_t hstu_qcache_read(const hstu_qcache_t *cache, int32_t dtype, int32_
  * (weight_decay 0: the old weight is not read); sums run in float32 in a fixed
  * order, so equal calls give equal bits.  A table entry of -inf (or below
  * -1e30) hides its bucket.  k_j, v_j are exactly the stored values; the
- * arithmetic is float32.
+ * arithmetic is float32, on the tensor cores with P = SiLU(x) rounded to bf16
+ * ahead of its product with v, as in hstu_attn_fwd.
  *  params            as hstu_attn_fwd_candidates (mask is ignored); num_heads,
  *                    d_qk, d_v those of the cache; max_seq_len bounds the
  *                    cached rows plus candidates of a sequence.
@@ -351,7 +352,9 @@ hstu_status_t hstu_qcache_read(const hstu_qcache_t *cache, int32_t dtype, int32_
  *                    candidates, any element alignment; every candidate row
  *                    of out is written, no other.
  *  workspace         >= hstu_attn_candidates_qcache_workspace_size bytes,
- *                    256-byte aligned, one per stream. */
+ *                    256-byte aligned, one per stream.
+ * bf16 with d_qk = d_v in {64, 128} runs on the tensor cores (unless params
+ * ask for HSTU_IMPL_SIMT), everything else on the CUDA cores. */
 hstu_status_t hstu_attn_candidates_qcache_workspace_size(const hstu_attn_params_t *params,
                                                          const int64_t *cache_lens_host,
                                                          const int64_t *cand_offsets_host,
