@@ -18,10 +18,12 @@
 //                decode them exactly to bf16 and write K and V tiles in the
 //                128-byte swizzle.
 //   warp 0       issues the MMAs: S^T of the next tile ahead of O^T of this one.
-//   warps 4-11   read S^T (thread = key; each warpgroup half of the
-//                candidates), make P = SiLU(x), write P^T (bf16) to shared
-//                memory, add up the weights; at the end write O.
-//   warps 1-3    the candidates' own pairs <q_i, k_i> meanwhile.
+//   warps 4-11   two warpgroups, taking tiles by turns: read S^T (thread = key),
+//                make P = SiLU(x), write P^T (bf16) to shared memory, add up the
+//                weights.  Before that the candidates' own pairs <q_i, k_i>, at
+//                the end each warpgroup writes half of O.
+//   warps 1-3    a tile per warp, up to four tiles ahead: what each key brings
+//                along (KeyBias).
 // Tensor memory: S^T in [0, NQ) and [NQ, 2 NQ) by turns, O^T in [2 NQ, 3 NQ).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -50,6 +52,19 @@ struct Cfg {
   static constexpr uint32_t kTmemCols = NQ == 128 ? 512 : 256;
 };
 
+// How the time bias of a tile's keys is found.  kTimeOne: the same for all
+// candidates, part of c.  kTimeTwo: each key meets one or two neighbouring
+// buckets, c below and c2 from candidate time t on (relative to the earliest).
+// kTimeFloat: by the float-exponent table, t = earliest candidate - key.
+// kTimeInt: bucket by bucket in 64 bits.
+enum : int { kTimeOne = 0, kTimeTwo = 1, kTimeFloat = 2, kTimeInt = 3 };
+constexpr int kBias = 4;              // tiles of KeyBias in flight
+struct KeyBias {
+  float c[kTile], c2[kTile], t[kTile];
+  int64_t tk[kTile];
+  int mode;
+};
+
 template <int D, int NQ>
 struct Smem {
   using C = Cfg<D, NQ>;
@@ -57,6 +72,7 @@ struct Smem {
   alignas(1024) uint8_t k[C::kK][C::kTileBytes];
   alignas(1024) uint8_t v[C::kV][C::kTileBytes];
   alignas(1024) uint8_t p[C::kP][C::kPBytes];   // behind v: see the D = 64 note at issue_o
+  KeyBias bias[kBias];
   alignas(16) int64_t tq[NQ];     // candidates' times
   alignas(16) float tqd[NQ];      // and relative to the earliest of them
   float p_self[NQ];
@@ -64,7 +80,8 @@ struct Smem {
   int64_t tq_min, tq_max;
   uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
   uint64_t s_full[2], p_full[C::kP], p_empty[C::kP];
-  uint64_t self_full, o_full, drain;
+  uint64_t bias_full[kBias], bias_empty[kBias];
+  uint64_t o_full, drain;
   uint32_t tmem_base;
   uint32_t abort;                 // a wait of this CTA ran out
 };
@@ -100,6 +117,28 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
                : "l"(p));
   return v;
 }
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+// 8 values of a bf16 row.
+__device__ __forceinline__ uint4 load_row8(const __nv_bfloat16 *src, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4 *>(src);
+  uint32_t e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = reinterpret_cast<const uint16_t *>(src)[i];
+  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float s) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+    s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
+  }
+  return s;
+}
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -111,45 +150,56 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// SiLU of the logit x.  With weights (which are returned in float32) the
-// quotient form, good to a few 2^-22; else h (1 + tanh h), h = x / 2, half the
-// special-function work, its error below P's rounding to bf16.
-template <bool WEIGHTS>
-__device__ __forceinline__ float silu_of(float x) {
-  if constexpr (WEIGHTS) {
-    return x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
-  } else {
-    return fmaf(x, tanh_approx(x), x);   // x already halved
-  }
-}
-
-// How a thread finds the time bias of its key against the candidates.
-enum : int { kTimeOne = 0, kTimeFloat = 1, kTimeInt = 2 };
-
-// 32 candidates of one key: P as bf16 pairs, and the sum of |P| over the first
-// `live` of them.
-template <int D, int NQ, bool WEIGHTS, int MODE>
-__device__ __forceinline__ void chunk32(const uint32_t (&s)[32], uint32_t (&pk)[16],
-                                        const Smem<D, NQ> &sm, int c0, float a, float c,
-                                        float base, int64_t tk, const float *rt, float half,
+// W candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum
+// of |P| over the first `live` of them.  With weights (returned in float32)
+// SiLU is x / (1 + 2^y), y = -x log2 e, good to a few 2^-22; else h (1 + tanh h)
+// with h = x / 2, half the special-function work, its error below P's rounding.
+template <int D, int NQ, bool WEIGHTS, int MODE, bool ALL, int W>
+__device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W / 2],
+                                        const Smem<D, NQ> &sm, int c0, float a, float c, float c2,
+                                        float t, int64_t tk, const float *rt, float half,
                                         int sub_bits, int nb_t, int live, float &wsum) {
   const int sh = 23 - sub_bits;
   const int32_t r0 = fast_r0(sub_bits);
+  constexpr float kL = -1.4426950408889634f;
+  const float ay = kL * a, cy = kL * c;
+  float tq[4];
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) {
+  for (int e = 0; e < W; e += 2) {
+    if constexpr (MODE == kTimeTwo || MODE == kTimeFloat) {
+      if ((e & 3) == 0) {
+        const float4 v = *reinterpret_cast<const float4 *>(&sm.tqd[c0 + e]);
+        tq[0] = v.x;
+        tq[1] = v.y;
+        tq[2] = v.z;
+        tq[3] = v.w;
+      }
+    }
     float pv[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      float x = fmaf(a, __uint_as_float(s[e + u]), c);
-      if constexpr (MODE == kTimeFloat) {
-        const int32_t rr = __float_as_int(base + sm.tqd[c0 + e + u]) >> sh;
-        x += sm.tbl_t[(rr > r0 ? rr : r0) - r0];
-      } else if constexpr (MODE == kTimeInt) {
-        x += half * qc_bias(rt[time_bucket_i64(sm.tq[c0 + e + u] - tk, sub_bits, nb_t)]);
+      const float sv = __uint_as_float(s[e + u]);
+      float x, y = 0.f;
+      if constexpr (MODE == kTimeOne) {
+        x = fmaf(a, sv, c);
+        if constexpr (WEIGHTS) y = fmaf(ay, sv, cy);
+      } else if constexpr (MODE == kTimeTwo) {
+        x = fmaf(a, sv, tq[(e & 3) + u] >= t ? c2 : c);
+        y = kL * x;
+      } else if constexpr (MODE == kTimeFloat) {
+        const int32_t rr = __float_as_int(t + tq[(e & 3) + u]) >> sh;
+        x = fmaf(a, sv, c) + sm.tbl_t[(rr > r0 ? rr : r0) - r0];
+        y = kL * x;
+      } else {
+        x = fmaf(a, sv, c) +
+            half * qc_bias(rt[time_bucket_i64(sm.tq[c0 + e + u] - tk, sub_bits, nb_t)]);
+        y = kL * x;
       }
-      pv[u] = silu_of<WEIGHTS>(x);
       if constexpr (WEIGHTS) {
-        if (live >= 32 || e + u < live) wsum += fabsf(pv[u]);
+        pv[u] = x * rcp_approx(1.0f + ex2_approx(y));
+        if (ALL || e + u < live) wsum += fabsf(pv[u]);
+      } else {
+        pv[u] = fmaf(x, tanh_approx(x), x);   // x already halved
       }
     }
     pk[e / 2] = pack_bf16x2(pv[0], pv[1]);
@@ -187,18 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = tid; x < kUnits; x += kThreads) {
       const int r = x / (D / 8), u = x % (D / 8);
       uint4 val = make_uint4(0, 0, 0, 0);
-      if (r < nq) {
-        const __nv_bfloat16 *src = q + r * p.q_rs + u * 8;
-        if (p.vec) {
-          val = *reinterpret_cast<const uint4 *>(src);
-        } else {
-          uint16_t e[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = reinterpret_cast<const uint16_t *>(src)[i];
-          val = make_uint4(e[0] | uint32_t(e[1]) << 16, e[2] | uint32_t(e[3]) << 16,
-                           e[4] | uint32_t(e[5]) << 16, e[6] | uint32_t(e[7]) << 16);
-        }
-      }
+      if (r < nq) val = load_row8(q + r * p.q_rs + u * 8, p.vec);
       *reinterpret_cast<uint4 *>(sm.q + (u >> 3) * kQHalf + r * 128 + (((u & 7) ^ (r & 7)) << 4)) =
           val;
     }
@@ -242,10 +281,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], kElemThreads);
+      mbar_init(&sm.p_full[i], kElemThreads / 2);
       mbar_init(&sm.p_empty[i], 1);
     }
-    mbar_init(&sm.self_full, 96);
+    for (int i = 0; i < kBias; ++i) {
+      mbar_init(&sm.bias_full[i], 32);
+      mbar_init(&sm.bias_empty[i], kElemThreads / 64);
+    }
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -313,193 +355,309 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp < 4) {
-    // ===================== the candidates' own pairs =====================
-    if (it.split == 0) {
-      const float bias = qc_bias(rp[0]) + qc_bias(rt[0]);
-      for (int i = warp - 1; i < nq; i += 3) {
-        const __nv_bfloat16 *qr =
-            static_cast<const __nv_bfloat16 *>(p.q) + (q_row + i) * p.q_rs + h * D;
-        const __nv_bfloat16 *kr =
-            static_cast<const __nv_bfloat16 *>(p.k) + (q_row + i) * p.k_rs + h * D;
-        float dot = 0.f;
+    // ===================== what each key brings along =====================
+    const int64_t t_lo = sm.tq_min, t_hi = sm.tq_max, lim = int64_t(1) << 24;
+    const int sh = 23 - p.sub_bits;
+    const int32_t r0 = fast_r0(p.sub_bits);
+    for (int n = warp - 1; n < n_tiles; n += 3) {
+      KeyBias &kb = sm.bias[n % kBias];
+      int64_t tk[4];
+      float c[4];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-          dot = fmaf(__bfloat162float(qr[e * 32 + lane]), __bfloat162float(kr[e * 32 + lane]), dot);
-#pragma unroll
-        for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-        if (lane == 0) sm.p_self[i] = silu_of<true>(fmaf(p.alpha, dot, bias));
+      for (int x = 0; x < 4; ++x) {
+        // keys behind the last take its values; their P is zeroed
+        const int32_t j = min((it.t0 + n) * kTile + x * 32 + lane, sq.len - 1);
+        tk[x] = cv.times[sq.row + j];
+        c[x] = __int_as_float(cv.pos[sq.row + j]);
       }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        c[x] = half * qc_bias(rp[pos_bucket(int64_t(sq.pos) - __float_as_int(c[x]), p.nb_p)]);
+      // float time differences are exact: every one, and its two parts, below 2^24
+      bool one = true, near = p.sub_bits <= 4 && t_hi - t_lo < lim;
+      int32_t b_lo[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        b_lo[x] = time_bucket_i64(t_lo - tk[x], p.sub_bits, p.nb_t);
+        if (t_hi != t_lo)
+          one = one && b_lo[x] == time_bucket_i64(t_hi - tk[x], p.sub_bits, p.nb_t);
+        near = near && t_hi - tk[x] < lim && t_lo - tk[x] > -lim;
+      }
+      one = __all_sync(0xffffffffu, one);
+      near = __all_sync(0xffffffffu, near);
+      if (n >= kBias &&
+          !wait_cta_warp(&sm.bias_empty[n % kBias], ((n / kBias) - 1) & 1, &sm.abort, p.wait))
+        break;
+      int mode = one ? kTimeOne : near ? kTimeFloat : kTimeInt;
+      if (one) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) c[x] += half * qc_bias(rt[b_lo[x]]);
+      } else if (near) {
+        // table entries of the earliest and the latest candidate
+        float base[4];
+        int32_t e_lo[4], e_hi[4];
+        bool two = true;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          base[x] = float(t_lo - tk[x]);
+          e_lo[x] = max(__float_as_int(base[x]) >> sh, r0) - r0;
+          e_hi[x] = max(__float_as_int(float(t_hi - tk[x])) >> sh, r0) - r0;
+          two = two && e_hi[x] - e_lo[x] <= 1;
+        }
+        if (__all_sync(0xffffffffu, two)) {
+          // The entry is e_lo + 1 exactly from the distance on whose bits are
+          // (e_lo + 1 + r0) << sh: an integer below 2^24 where both entries
+          // occur, so its difference to base is exact.
+          mode = kTimeTwo;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            kb.c2[x * 32 + lane] = c[x] + sm.tbl_t[e_hi[x]];
+            kb.t[x * 32 + lane] = __int_as_float((e_lo[x] + 1 + r0) << sh) - base[x];
+            c[x] += sm.tbl_t[e_lo[x]];
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) kb.t[x * 32 + lane] = base[x];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        kb.c[x * 32 + lane] = c[x];
+        kb.tk[x * 32 + lane] = tk[x];
+      }
+      if (lane == 0) kb.mode = mode;
+      mbar_arrive(&sm.bias_full[n % kBias]);
     }
-    mbar_arrive(&sm.self_full);
   } else if (warp < 12) {
     // ===================== elementwise =====================
     const int wg = (warp - 4) >> 2, quad = warp & 3;
     const int key = quad * 32 + lane;
     const uint32_t lanes = tmem + (uint32_t(quad * 32) << 16);
+    if (it.split == 0) {
+      // The candidates' own pairs, while the first tiles are decoded: 8 lanes
+      // per candidate, each NQ / 8 of them per warp; every load is issued ahead
+      // of the first sum.
+      constexpr int kPass = NQ / 32, kVec = D / 64;
+      const int sub = lane & 7;
+      uint4 qv[kPass][kVec], kv[kPass][kVec];
+#pragma unroll
+      for (int x = 0; x < kPass; ++x) {
+        const int i = (warp - 4) * (NQ / 8) + x * 4 + (lane >> 3);
+#pragma unroll
+        for (int y = 0; y < kVec; ++y) {
+          qv[x][y] = kv[x][y] = make_uint4(0, 0, 0, 0);
+          if (i < nq) {
+            const int64_t e = h * D + (y * 8 + sub) * 8;
+            qv[x][y] = load_row8(static_cast<const __nv_bfloat16 *>(p.q) + (q_row + i) * p.q_rs + e,
+                                 p.vec);
+            kv[x][y] = load_row8(static_cast<const __nv_bfloat16 *>(p.k) + (q_row + i) * p.k_rs + e,
+                                 p.vec);
+          }
+        }
+      }
+      const float bias = qc_bias(rp[0]) + qc_bias(rt[0]);
+#pragma unroll
+      for (int x = 0; x < kPass; ++x) {
+        float dot = 0.f;
+#pragma unroll
+        for (int y = 0; y < kVec; ++y) dot = dot8(qv[x][y], kv[x][y], dot);
+#pragma unroll
+        for (int m = 4; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+        const float xs = fmaf(p.alpha, dot, bias);
+        if (sub == 0)
+          sm.p_self[(warp - 4) * (NQ / 8) + x * 4 + (lane >> 3)] =
+              xs * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * xs));
+      }
+    }
     const float a = half * p.alpha;
-    const int64_t t_lo = sm.tq_min, t_hi = sm.tq_max;
-    constexpr int kCols = NQ / 2;
-    const int c_first = wg * kCols, c_end = min(c_first + kCols, nq);   // empty for small nq
     bool ok = true;
-    for (int n = 0; n < n_tiles; ++n) {
+    for (int n = wg; n < n_tiles; n += 2) {
       const int32_t j = (it.t0 + n) * kTile + key;
       const bool valid = j < sq.len;
-      // what this key brings along: position bias, and its time bias when it
-      // is the same for all candidates
-      int mode = kTimeOne;
-      float c = 0.f, base = 0.f, wsum = 0.f;
+      const KeyBias &kb = sm.bias[n % kBias];
+      ok = wait_cta_warp(&sm.bias_full[n % kBias], (n / kBias) & 1, &sm.abort, p.wait);
+      if (!ok) break;
+      const int mode = kb.mode;
+      const float c = kb.c[key];
+      float c2 = 0.f, t = 0.f, wsum = 0.f;
       int64_t tk = 0;
-      if (c_first < c_end) {
-        const int64_t row = sq.row + (valid ? j : 0);
-        tk = cv.times[row];
-        c = half * qc_bias(rp[pos_bucket(int64_t(sq.pos) - cv.pos[row], p.nb_p)]);
-        const int32_t b_lo = time_bucket_i64(t_lo - tk, p.sub_bits, p.nb_t);
-        const int32_t b_hi = t_hi == t_lo ? b_lo : time_bucket_i64(t_hi - tk, p.sub_bits, p.nb_t);
-        if (__all_sync(0xffffffffu, b_lo == b_hi || !valid)) {
-          c += half * qc_bias(rt[b_lo]);
-        } else {
-          const int64_t lim = int64_t(1) << 24;
-          const bool near = t_hi - tk < lim && t_lo - tk > -lim;   // float differences are exact
-          mode = __all_sync(0xffffffffu, p.sub_bits <= 4 && (near || !valid)) ? kTimeFloat
-                                                                              : kTimeInt;
-          base = float(t_lo - tk);
-        }
+      if (mode != kTimeOne) {
+        c2 = kb.c2[key];
+        t = kb.t[key];
+        tk = kb.tk[key];
       }
-      ok = wait_cta_warp(&sm.s_full[n & 1], (n >> 1) & 1, &sm.abort, p.wait);
-      if (ok && n >= C::kP)
-        ok = wait_cta_warp(&sm.p_empty[n % C::kP], ((n / C::kP) - 1) & 1, &sm.abort, p.wait);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.bias_empty[n % kBias]);
+      ok = wait_cta_warp(&sm.s_full[wg], (n >> 1) & 1, &sm.abort, p.wait);
+      if (ok && n >= C::kP)   // the product of the tile two back has read P
+        ok = wait_cta_warp(&sm.p_empty[wg], ((n >> 1) - 1) & 1, &sm.abort, p.wait);
       if (!ok) break;
       tc_fence_after();
-      uint8_t *pt = sm.p[n % C::kP] + key * 128;
-#pragma unroll 1
-      for (int c0 = c_first; c0 < c_end; c0 += 32) {
-        uint32_t r[32], pk[16];
-        tmem_ld32(lanes + (n & 1) * NQ + c0, r);
+      uint8_t *pt = sm.p[wg] + key * 128;
+#define HSTU_QC_CHUNK(M_, A_, W_)                                                                \
+  chunk<D, NQ, WEIGHTS, M_, A_, W_>(r, pk, sm, c0, a, c, c2, t, tk, rt, half, p.sub_bits, p.nb_t, \
+                                    nq - c0, wsum)
+      if (nq <= 16 && mode == kTimeOne) {   // few candidates: half a chunk
+        constexpr int c0 = 0;
+        uint32_t r[16], pk[8];
+        tmem_ld16(lanes + wg * NQ, r);
         tmem_wait_ld(r);
-        const int live = c_end - c0;
-        if (mode == kTimeOne)
-          chunk32<D, NQ, WEIGHTS, kTimeOne>(r, pk, sm, c0, a, c, base, tk, rt, half, p.sub_bits,
-                                            p.nb_t, live, wsum);
-        else if (mode == kTimeFloat)
-          chunk32<D, NQ, WEIGHTS, kTimeFloat>(r, pk, sm, c0, a, c, base, tk, rt, half, p.sub_bits,
-                                              p.nb_t, live, wsum);
-        else
-          chunk32<D, NQ, WEIGHTS, kTimeInt>(r, pk, sm, c0, a, c, base, tk, rt, half, p.sub_bits,
-                                            p.nb_t, live, wsum);
-        if (!valid) {
+        HSTU_QC_CHUNK(kTimeOne, !WEIGHTS, 16);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0;
-        }
-        uint8_t *box = pt + (c0 >> 6) * kBoxBytes;
+        for (int e = 0; e < 8; ++e) pk[e] = valid ? pk[e] : 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4 *>(box + (((((c0 & 63) >> 3) + e) ^ (key & 7)) << 4)) =
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint4 *>(pt + ((e ^ (key & 7)) << 4)) =
               make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+      } else {
+#pragma unroll 1
+        for (int c0 = 0; c0 < nq; c0 += 32) {
+          uint32_t r[32], pk[16];
+          tmem_ld32(lanes + wg * NQ + c0, r);
+          tmem_wait_ld(r);
+          if (mode == kTimeOne) {
+            if (!WEIGHTS || nq - c0 >= 32)
+              HSTU_QC_CHUNK(kTimeOne, true, 32);
+            else
+              HSTU_QC_CHUNK(kTimeOne, false, 32);
+          } else if (mode == kTimeTwo) {
+            HSTU_QC_CHUNK(kTimeTwo, !WEIGHTS, 32);
+          } else if (mode == kTimeFloat) {
+            HSTU_QC_CHUNK(kTimeFloat, !WEIGHTS, 32);
+          } else {
+            HSTU_QC_CHUNK(kTimeInt, !WEIGHTS, 32);
+          }
+          if (!valid) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0;
+          }
+          uint8_t *box = pt + (c0 >> 6) * kBoxBytes;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4 *>(box + (((((c0 & 63) >> 3) + e) ^ (key & 7)) << 4)) =
+                make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+        }
       }
+#undef HSTU_QC_CHUNK
       tc_fence_before();          // S^T has been read
       fence_proxy_async_smem();   // P^T is written
-      mbar_arrive(&sm.p_full[n % C::kP]);
+      mbar_arrive(&sm.p_full[wg]);
       if constexpr (WEIGHTS) {
-        if (valid && c_first < c_end)
-          p.wpart[sq.wp0 + (int64_t(it.qtile * 2 + wg) * H + h) * sq.len + j] = wsum;
+        if (valid) p.wpart[sq.wp0 + (int64_t(it.qtile) * H + h) * sq.len + j] = wsum;
       }
     }
     // ---- O^T (tensor memory: lane = feature) + own pair -> rows of out ----
-    if (ok) ok = wait_cta_warp(&sm.self_full, 0, &sm.abort, p.wait);
+    named_bar_sync(1, kElemThreads);   // p_self of all warps
+    constexpr int kCols = NQ / 2;
+    const int c_first = wg * kCols, c_end = min(c_first + kCols, nq);
     if (ok && n_tiles > 0) ok = wait_cta_warp(&sm.o_full, 0, &sm.abort, p.wait);
     tc_fence_after();
-    if (ok && key < D) {
+    if (ok && quad * 32 < D) {
       const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v) + q_row * p.v_rs + h * D + key;
       __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + q_row * p.o_rs + h * D + key;
       float *acc = p.acc + ((sq.acc0 + (int64_t(it.split) * sq.n + i0) * H + h) * D + key);
 #pragma unroll 1
-      for (int c0 = c_first; c0 < c_end; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(lanes + 2 * NQ + c0, r);
+      for (int c0 = c_first; c0 < c_end; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld16(lanes + 2 * NQ + c0, r);
         tmem_wait_ld(r);
+        float o[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < 16; ++e) {
+          o[e] = n_tiles > 0 ? __uint_as_float(r[e]) : 0.f;
+          if (it.split == 0 && c0 + e < c_end)
+            o[e] = fmaf(sm.p_self[c0 + e], __bfloat162float(v[(c0 + e) * p.v_rs]), o[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
           const int i = c0 + e;
           if (i < c_end) {
-            float o = n_tiles > 0 ? __uint_as_float(r[e]) : 0.f;
-            if (it.split == 0) o = fmaf(sm.p_self[i], __bfloat162float(v[i * p.v_rs]), o);
             if (sq.splits > 1)
-              acc[int64_t(i) * H * D] = o;
+              acc[int64_t(i) * H * D] = o[e];
             else
-              out[i * p.o_rs] = __float2bfloat16_rn(o * p.scale);
+              out[i * p.o_rs] = __float2bfloat16_rn(o[e] * p.scale);
           }
         }
       }
     }
   } else {
     // ===================== decoding K and V =====================
-    constexpr int G = D / 32, kPer = kTile * G / kDecThreads;   // groups per row / per thread
-    const int dt = tid - 384;
-    const uint4 *kc = reinterpret_cast<const uint4 *>(cv.k_codes);
-    const uint4 *vc = reinterpret_cast<const uint4 *>(cv.v_codes);
-    const int64_t g0 = (int64_t(h) * cv.rows + sq.row) * G;
+    // A warp takes 8 rows x 4 groups (16 x 2 at D = 64) of a tile, 512 bytes in
+    // one piece.  Eight lanes that store together hold 4 rows x 2 neighbouring
+    // groups, whose 16-byte chunks lie in eight different banks under the
+    // swizzle.
+    constexpr int G = D / 32;                      // groups per row
+    constexpr int kPer = kTile * G / kDecThreads;  // groups per thread and tile
+    constexpr int kStep = kDecThreads / G;         // rows between a thread's groups
+    const int dw = warp - 12;
+    const int row = G == 4 ? dw * 8 + ((lane >> 4) << 2) + ((lane >> 1) & 3)
+                           : dw * 16 + (lane >> 1);
+    const int g = G == 4 ? ((lane >> 3) & 1) * 2 + (lane & 1) : lane & 1;
+    const int64_t at = (int64_t(h) * cv.rows + sq.row + int64_t(it.t0) * kTile + row) * G + g;
+    const uint4 *kc = reinterpret_cast<const uint4 *>(cv.k_codes) + at;
+    const uint4 *vc = reinterpret_cast<const uint4 *>(cv.v_codes) + at;
+    const uint16_t *ks = cv.k_scales + at, *vs = cv.v_scales + at;
+    int32_t left = sq.len - it.t0 * kTile - row;   // rows of the sequence from this one on
+    uint32_t off[4];   // where the group's chunks go in a tile
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      off[e] = (g >> 1) * kBoxBytes + row * 128 + ((((g & 1) * 4 + e) ^ (row & 7)) << 4);
     struct Raw {
       uint4 k[kPer], v[kPer];
       uint32_t kp[kPer], vp[kPer];
     };
-    // rows behind the sequence's last decode to zeros: scale 0
-    auto fetch = [&](int n, Raw &r) {
+    auto fetch = [&](Raw &r) {
 #pragma unroll
       for (int x = 0; x < kPer; ++x) {
-        const int idx = dt + x * kDecThreads;
-        const int64_t j = int64_t(it.t0 + n) * kTile + idx / G;
-        r.k[x] = r.v[x] = make_uint4(0, 0, 0, 0);
-        r.kp[x] = r.vp[x] = 0;
-        if (n < n_tiles && j < sq.len) {
-          const int64_t at = g0 + int64_t(it.t0 + n) * kTile * G + idx;
-          r.k[x] = ld_stream(kc + at);
-          r.v[x] = ld_stream(vc + at);
-          r.kp[x] = cv.k_scales[at];
-          r.vp[x] = cv.v_scales[at];
+        if (x * kStep < left) {
+          r.k[x] = ld_stream(kc + x * kDecThreads);
+          r.v[x] = ld_stream(vc + x * kDecThreads);
+          r.kp[x] = ks[x * kDecThreads];
+          r.vp[x] = vs[x * kDecThreads];
+        } else {   // behind the last row: zeros
+          r.k[x] = r.v[x] = make_uint4(0, 0, 0, 0);
+          r.kp[x] = r.vp[x] = 0;
         }
       }
+      kc += kTile * G;
+      vc += kTile * G;
+      ks += kTile * G;
+      vs += kTile * G;
+      left -= kTile;
     };
-    auto store = [&](uint8_t *tile, const uint4 (&code)[kPer], const uint32_t (&par)[kPer]) {
+    auto store = [&](uint32_t tile, const uint4 (&code)[kPer], const uint32_t (&par)[kPer]) {
 #pragma unroll
       for (int x = 0; x < kPer; ++x) {
-        const int idx = dt + x * kDecThreads, row = idx / G, g = idx % G;
         uint32_t zz, ss;
         q4_group(par[x], zz, ss);
-        // A warp's eight 16-byte stores of a phase hold 2 rows x 4 groups at
-        // D = 128; groups 2 and 3 (the other box, same banks) go in another
-        // chunk order so that the phase touches every bank once.
-        const bool swap = G == 4 && (g & 2);
-        const uint32_t w[4] = {swap ? code[x].z : code[x].x, swap ? code[x].w : code[x].y,
-                               swap ? code[x].x : code[x].z, swap ? code[x].y : code[x].w};
-        uint8_t *dst = tile + (g >> 1) * kBoxBytes + row * 128;
-        const int first = (g & 1) * 4, flip = swap ? 2 : 0;
+        const uint32_t w[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t o[4];
           q4_decode_bf16(w[e], zz, ss, o);
-          *reinterpret_cast<uint4 *>(dst + (((first + (e ^ flip)) ^ (row & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+          st_shared_v4(tile + off[e] + x * kStep * 128, o);
         }
       }
     };
+    const uint32_t k0 = smem_u32(sm.k[0]), v0 = smem_u32(sm.v[0]);
     Raw raw[2];
-    fetch(0, raw[0]);
-    fetch(1, raw[1]);
+    fetch(raw[0]);
+    fetch(raw[1]);
     bool ok = true;
     auto step = [&](int n, Raw &r) {
       if (n >= C::kK)
         ok = wait_cta_warp(&sm.k_empty[n % C::kK], ((n / C::kK) - 1) & 1, &sm.abort, p.wait);
       if (!ok) return;
-      store(sm.k[n % C::kK], r.k, r.kp);
+      store(k0 + (n % C::kK) * C::kTileBytes, r.k, r.kp);
       fence_proxy_async_smem();
       mbar_arrive(&sm.k_full[n % C::kK]);
       if (n >= C::kV)
         ok = wait_cta_warp(&sm.v_empty[n % C::kV], ((n / C::kV) - 1) & 1, &sm.abort, p.wait);
       if (!ok) return;
-      store(sm.v[n % C::kV], r.v, r.vp);
+      store(v0 + (n % C::kV) * C::kTileBytes, r.v, r.vp);
       fence_proxy_async_smem();
       mbar_arrive(&sm.v_full[n % C::kV]);
-      fetch(n + 2, r);
+      fetch(r);
     };
     for (int n = 0; n < n_tiles && ok; n += 2) {
       step(n, raw[0]);
