@@ -30,8 +30,8 @@ hstu_status_t check_cache(const hstu_qcache_t *c, bool weight) {
   if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || !c->times || !c->pos ||
       (weight && !c->weight))
     return HSTU_ERR_INVALID_ARG;
-  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 2) ||
-      !aligned(c->v_scales, 2) || !aligned(c->times, 8) || !aligned(c->pos, 4) ||
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 16) ||
+      !aligned(c->v_scales, 16) || !aligned(c->times, 8) || !aligned(c->pos, 4) ||
       !aligned(c->weight, 4))
     return HSTU_ERR_INVALID_ARG;
   return HSTU_OK;

@@ -14,17 +14,19 @@
 // and its weight sum over the candidates stays in a register.  It also keeps
 // the tile 128 keys high for a single candidate (NQ only pads the N side).
 //
-//   warps 12-19  read codes (16 bytes = one group per load, two tiles ahead),
-//                decode them exactly to bf16 and write K and V tiles in the
-//                128-byte swizzle.
-//   warp 0       issues the MMAs: S^T of the next tile ahead of O^T of this one.
+//   warps 12-19  keys: bring codes to shared memory (cp.async, ahead), decode
+//                them exactly to bf16, write K tiles in the 128-byte swizzle.
+//   warps 20-27  the same for values.
+//   warp 0       issues the MMAs, whichever has its operands: O^T of a tile
+//                first, else S^T up to two tiles ahead.
 //   warps 4-11   two warpgroups, taking tiles by turns: read S^T (thread = key),
 //                make P = SiLU(x), write P^T (bf16) to shared memory, add up the
-//                weights.  Before that the candidates' own pairs <q_i, k_i>, at
-//                the end each warpgroup writes half of O.
-//   warps 1-3    a tile per warp, up to four tiles ahead: what each key brings
+//                weights; at the end each warpgroup writes half of O.
+//   warps 1-3    a tile per warp, up to six tiles ahead: what each key brings
 //                along (KeyBias).
-// Tensor memory: S^T in [0, NQ) and [NQ, 2 NQ) by turns, O^T in [2 NQ, 3 NQ).
+// The candidates' own pairs are one more tile, the first of the range that has
+// them: its keys are the candidates and only P's diagonal is kept.
+// Tensor memory: S^T of tile n in [(n % 3) NQ, + NQ), O^T in [3 NQ, 4 NQ).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,21 +37,31 @@ namespace hstu {
 namespace qc_tc {
 
 constexpr int kTile = kQcKeyTile;
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr int kElemThreads = 256;     // warps 4-11
-constexpr int kDecThreads = 256;      // warps 12-19
+constexpr int kDecThreads = 256;      // warps 12-19, and 20-27
+// Registers: 72 x 896 at launch; the control and decoding warpgroups give up
+// some for the two elementwise ones (56 + 2 x 96 + 4 x 64 = 7 x 72).
+constexpr int kRegsAll = 72, kRegsCtlW = 56, kRegsElem = 96, kRegsDec = 64;
+static_assert(kRegsCtlW + 2 * kRegsElem + 4 * kRegsDec <= 7 * kRegsAll, "register split");
 constexpr int kTblT = 385;            // float-exponent table of the time bias, sub_bits <= 4
 constexpr uint32_t kBoxBytes = kTile * 128;   // 128 rows of 64 bf16
 
 template <int D, int NQ>
 struct Cfg {
   static constexpr int kTileBytes = kTile * D * 2;
-  // The K tile is free again as soon as S^T is done, well before P is; one
-  // buffer does where two would not fit.
-  static constexpr int kK = D == 128 && NQ == 128 ? 1 : 2;
-  static constexpr int kV = 2, kP = 2;
+  // One K tile: it is free again as soon as S^T is done.  A V tile lives until
+  // its P is there: two of them.
+  static constexpr int kV = 2;
   static constexpr int kPBytes = NQ / 64 * int(kBoxBytes);
-  static constexpr uint32_t kTmemCols = NQ == 128 ? 512 : 256;
+  // Tiles of codes on their way: with few candidates the cache's bandwidth is
+  // the limit, and bytes in flight per SM = bandwidth x latency, about 36 KB at
+  // full HBM rate; with many a tile's time covers the latency.
+  static constexpr int kStages = D == 128 ? (NQ == 128 ? 1 : 3) : 4;
+  static constexpr int kCodeBytes = kTile * D / 2;       // of one tile of K (or V)
+  static constexpr int kScaleBytes = kTile * D / 16;
+  static constexpr uint32_t kTmemCols = 4 * NQ;
+  static constexpr uint32_t kO = 3 * NQ;                 // first column of O^T
 };
 
 // How the time bias of a tile's keys is found.  kTimeOne: the same for all
@@ -58,10 +70,13 @@ struct Cfg {
 // kTimeFloat: by the float-exponent table, t = earliest candidate - key.
 // kTimeInt: bucket by bucket in 64 bits.
 enum : int { kTimeOne = 0, kTimeTwo = 1, kTimeFloat = 2, kTimeInt = 3 };
-constexpr int kBias = 4;              // tiles of KeyBias in flight
+// Tiles of KeyBias in flight: a multiple of the 3 warps that fill them and of
+// the 2 warpgroups that take them, so a slot always has the same two parties and
+// none of them can be a whole round of its barriers ahead of the other (a parity
+// wait cannot tell two rounds apart).
+constexpr int kBias = 6;
 struct KeyBias {
   float c[kTile], c2[kTile], t[kTile];
-  int64_t tk[kTile];
   int mode;
 };
 
@@ -69,21 +84,27 @@ template <int D, int NQ>
 struct Smem {
   using C = Cfg<D, NQ>;
   alignas(1024) uint8_t q[NQ * D * 2];
-  alignas(1024) uint8_t k[C::kK][C::kTileBytes];
+  alignas(1024) uint8_t k[C::kTileBytes];
   alignas(1024) uint8_t v[C::kV][C::kTileBytes];
-  alignas(1024) uint8_t p[C::kP][C::kPBytes];   // behind v: see the D = 64 note at issue_o
+  alignas(1024) uint8_t p[2][C::kPBytes];       // behind v: see the D = 64 note at issue_o
+  alignas(16) uint8_t k_codes[C::kStages][C::kCodeBytes];
+  alignas(16) uint8_t v_codes[C::kStages][C::kCodeBytes];
+  alignas(16) uint8_t k_scales[C::kStages][C::kScaleBytes];
+  alignas(16) uint8_t v_scales[C::kStages][C::kScaleBytes];
   KeyBias bias[kBias];
   alignas(16) int64_t tq[NQ];     // candidates' times
   alignas(16) float tqd[NQ];      // and relative to the earliest of them
-  float p_self[NQ];
   float tbl_t[kTblT];
   int64_t tq_min, tq_max;
-  uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
-  uint64_t s_full[2], p_full[C::kP], p_empty[C::kP];
+  uint64_t k_full, k_empty, v_full[C::kV], v_empty[C::kV];
+  uint64_t s_full[3];             // a warpgroup takes every other round of a slot: the commits
+                                  // are in order, so the round between is over by then
+  uint64_t p_full[2], p_empty[2];
   uint64_t bias_full[kBias], bias_empty[kBias];
-  uint64_t o_full, drain;
+  uint64_t q_full, o_full, drain;
   uint32_t tmem_base;
   uint32_t abort;                 // a wait of this CTA ran out
+  static_assert(sizeof(p) >= NQ * D * sizeof(float), "O goes through the P tiles at the end");
 };
 
 // Bounded wait.  The CTA's own flag, not the error word of the workspace, tells
@@ -110,12 +131,24 @@ __device__ __forceinline__ bool wait_cta_warp(uint64_t *bar, uint32_t parity, ui
   return __all_sync(0xffffffffu, wait_cta(bar, parity, abort, w));
 }
 
-__device__ __forceinline__ uint4 ld_stream(const void *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// N bytes global -> shared, zeros when !ok (src is then not read).
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool ok) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? N : 0), "n"(N)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
@@ -154,6 +187,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // of |P| over the first `live` of them.  With weights (returned in float32)
 // SiLU is x / (1 + 2^y), y = -x log2 e, good to a few 2^-22; else h (1 + tanh h)
 // with h = x / 2, half the special-function work, its error below P's rounding.
+// The special-function unit (16 results a cycle and SM) is what bounds this
+// loop with weights; every other pair of quotients shares a reciprocal, which
+// trades one of its results for three multiplications and balances the two.
 template <int D, int NQ, bool WEIGHTS, int MODE, bool ALL, int W>
 __device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W / 2],
                                         const Smem<D, NQ> &sm, int c0, float a, float c, float c2,
@@ -175,32 +211,46 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W /
         tq[3] = v.w;
       }
     }
-    float pv[2];
+    float x[2], y[2], pv[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const float sv = __uint_as_float(s[e + u]);
-      float x, y = 0.f;
       if constexpr (MODE == kTimeOne) {
-        x = fmaf(a, sv, c);
-        if constexpr (WEIGHTS) y = fmaf(ay, sv, cy);
+        x[u] = fmaf(a, sv, c);
+        y[u] = fmaf(ay, sv, cy);
       } else if constexpr (MODE == kTimeTwo) {
-        x = fmaf(a, sv, tq[(e & 3) + u] >= t ? c2 : c);
-        y = kL * x;
+        x[u] = fmaf(a, sv, tq[(e & 3) + u] >= t ? c2 : c);
+        y[u] = kL * x[u];
       } else if constexpr (MODE == kTimeFloat) {
         const int32_t rr = __float_as_int(t + tq[(e & 3) + u]) >> sh;
-        x = fmaf(a, sv, c) + sm.tbl_t[(rr > r0 ? rr : r0) - r0];
-        y = kL * x;
+        x[u] = fmaf(a, sv, c) + sm.tbl_t[(rr > r0 ? rr : r0) - r0];
+        y[u] = kL * x[u];
       } else {
-        x = fmaf(a, sv, c) +
-            half * qc_bias(rt[time_bucket_i64(sm.tq[c0 + e + u] - tk, sub_bits, nb_t)]);
-        y = kL * x;
+        x[u] = fmaf(a, sv, c) +
+               half * qc_bias(rt[time_bucket_i64(sm.tq[c0 + e + u] - tk, sub_bits, nb_t)]);
+        y[u] = kL * x[u];
       }
-      if constexpr (WEIGHTS) {
-        pv[u] = x * rcp_approx(1.0f + ex2_approx(y));
+    }
+    if constexpr (WEIGHTS) {
+      if (MODE == kTimeOne && (e & 2) == 0) {
+        // one reciprocal for two quotients; logits are held at -42.9, where SiLU
+        // is -1e-17, so that the product of the two stays finite
+        x[0] = fmaxf(x[0], -42.9f);
+        x[1] = fmaxf(x[1], -42.9f);
+        const float d0 = 1.0f + ex2_approx(kL * x[0]), d1 = 1.0f + ex2_approx(kL * x[1]);
+        const float r = rcp_approx(d0 * d1);
+        pv[0] = x[0] * (r * d1);
+        pv[1] = x[1] * (r * d0);
+      } else {
+        pv[0] = x[0] * rcp_approx(1.0f + ex2_approx(y[0]));
+        pv[1] = x[1] * rcp_approx(1.0f + ex2_approx(y[1]));
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
         if (ALL || e + u < live) wsum += fabsf(pv[u]);
-      } else {
-        pv[u] = fmaf(x, tanh_approx(x), x);   // x already halved
-      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) pv[u] = fmaf(x[u], tanh_approx(x[u]), x[u]);   // x halved
     }
     pk[e / 2] = pack_bf16x2(pv[0], pv[1]);
   }
@@ -230,57 +280,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float half = WEIGHTS ? 1.0f : 0.5f;     // the tanh form works on x / 2
   constexpr uint32_t kQHalf = NQ * 128;         // bytes of one 64-column box of Q
 
-  // ---- start-up: queries in the K-major 128-byte swizzle, tables, barriers ----
-  {
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + q_row * p.q_rs + h * D;
-    constexpr int kUnits = NQ * (D / 8);
-    for (int x = tid; x < kUnits; x += kThreads) {
-      const int r = x / (D / 8), u = x % (D / 8);
-      uint4 val = make_uint4(0, 0, 0, 0);
-      if (r < nq) val = load_row8(q + r * p.q_rs + u * 8, p.vec);
-      *reinterpret_cast<uint4 *>(sm.q + (u >> 3) * kQHalf + r * 128 + (((u & 7) ^ (r & 7)) << 4)) =
-          val;
-    }
-    if (p.sub_bits <= 4) {
-      const int n = fast_table_size(p.sub_bits);
-      for (int x = tid; x < n; x += kThreads)
-        sm.tbl_t[x] = half * qc_bias(rt[fast_table_bucket(x, p.sub_bits, p.nb_t)]);
-    }
-  }
-  if (warp == 1) {
-    // candidates' times, their range, and their distances to the earliest;
-    // a padding candidate takes the first one's
-    int64_t lo = INT64_MAX, hi = INT64_MIN;
-    for (int i = lane; i < NQ; i += 32) {
-      const int64_t t = p.cand_ts[q_row + (i < nq ? i : 0)];
-      sm.tq[i] = t;
-      lo = t < lo ? t : lo;
-      hi = t > hi ? t : hi;
-    }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) {
-      const int64_t a = __shfl_xor_sync(0xffffffffu, lo, m), b = __shfl_xor_sync(0xffffffffu, hi, m);
-      lo = a < lo ? a : lo;
-      hi = b > hi ? b : hi;
-    }
-    __syncwarp();
-    for (int i = lane; i < NQ; i += 32) sm.tqd[i] = float(sm.tq[i] - lo);
-    if (lane == 0) {
-      sm.tq_min = lo;
-      sm.tq_max = hi;
-    }
-  }
-  if (tid == 0) {
-    for (int i = 0; i < C::kK; ++i) {
-      mbar_init(&sm.k_full[i], kDecThreads);
-      mbar_init(&sm.k_empty[i], 1);
-    }
+  constexpr int G = D / 32;                      // groups per row
+  constexpr int kPer = kTile * G / kDecThreads;  // groups per thread and tile
+  constexpr int kStep = kDecThreads / G;         // rows between a thread's groups
+  const int self = it.split == 0 ? 1 : 0;        // tile 0 is the candidates' own
+  const int n_all = n_tiles + self;
+
+  if (tid == 64) {
+    mbar_init(&sm.q_full, kElemThreads);
+    mbar_init(&sm.k_full, kDecThreads);
+    mbar_init(&sm.k_empty, 1);
     for (int i = 0; i < C::kV; ++i) {
       mbar_init(&sm.v_full[i], kDecThreads);
       mbar_init(&sm.v_empty[i], 1);
     }
+    for (int i = 0; i < 3; ++i) mbar_init(&sm.s_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], kElemThreads / 2);
       mbar_init(&sm.p_empty[i], 1);
     }
@@ -294,213 +309,265 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0) {
-    __syncwarp();
     tmem_alloc(&sm.tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
-  fence_proxy_async_smem();   // the queries, ahead of the MMAs that read them
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  if (warp == 0) {
-    // ===================== MMA issuer =====================
-    if (elect_one() && n_tiles > 0) {
-      constexpr uint32_t idesc_s = idesc_bf16(kTile, NQ, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16(128, NQ, true, true);
-      const uint64_t dq = sdesc_sw128(smem_u32(sm.q), 16, 1024);
-      auto issue_s = [&](int n) {
-        const uint64_t dk = sdesc_sw128(smem_u32(sm.k[n % C::kK]), 16, 1024);
+  if (warp < 4) {
+    regs_release_ctl<kRegsCtlW>();
+    if (warp == 0) {
+      // ===================== MMA issuer =====================
+      if (elect_one()) {
+        constexpr uint32_t idesc_s = idesc_bf16(kTile, NQ, false, false);
+        constexpr uint32_t idesc_o = idesc_bf16(128, NQ, true, true);
+        const uint64_t dq = sdesc_sw128(smem_u32(sm.q), 16, 1024);
+        const uint64_t dk = sdesc_sw128(smem_u32(sm.k), 16, 1024);
+        bool ok = wait_cta(&sm.q_full, 0, &sm.abort, p.wait);
+        int ns = 0, no = 0, s_slot = 0;   // next S^T, next O^T; ns % 3
+        uint32_t idle = 0;
+        uint64_t t0 = 0;
+        while (ok && no < n_all) {
+          if (no < ns && mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1) &&
+              mbar_test_wait(&sm.v_full[no & 1], (no >> 1) & 1)) {
+            // D = 64: the instruction is 128 rows high all the same; rows 64-127
+            // read whatever lies one box behind the V tile (the next V tile or P,
+            // inside this struct) and fill tensor-memory lanes that nobody reads.
+            tc_fence_after();
+            const uint64_t dv = sdesc_sw128(smem_u32(sm.v[no & 1]), kBoxBytes, 1024);
+            const uint64_t dp = sdesc_sw128(smem_u32(sm.p[no & 1]), kBoxBytes, 1024);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(tmem + (n & 1) * NQ, dk + (((kk / 4) * kBoxBytes + (kk % 4) * 32) >> 4),
-                  dq + (((kk / 4) * kQHalf + (kk % 4) * 32) >> 4), idesc_s, kk > 0);
-        umma_commit(&sm.s_full[n & 1]);
-        umma_commit(&sm.k_empty[n % C::kK]);
-      };
-      // D = 64: the instruction is 128 rows high all the same; rows 64-127 read
-      // whatever lies one box behind the V tile (the next V tile or P, inside
-      // this struct) and fill tensor-memory lanes that nobody reads.
-      auto issue_o = [&](int n) {
-        const uint64_t dv = sdesc_sw128(smem_u32(sm.v[n % C::kV]), kBoxBytes, 1024);
-        const uint64_t dp = sdesc_sw128(smem_u32(sm.p[n % C::kP]), kBoxBytes, 1024);
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_ss(tmem + C::kO, dv + ((kk * 16 * 128) >> 4), dp + ((kk * 16 * 128) >> 4),
+                      idesc_o, (no > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&sm.v_empty[no & 1]);
+            umma_commit(&sm.p_empty[no & 1]);
+            ++no;
+            idle = 0;
+          } else if (ns < n_all && ns < no + 3 && mbar_test_wait(&sm.k_full, ns & 1)) {
+            // the columns of S^T are free: P of tile ns - 3 is there
+            tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_ss(tmem + 2 * NQ, dv + ((kk * 16 * 128) >> 4), dp + ((kk * 16 * 128) >> 4),
-                  idesc_o, (n > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&sm.v_empty[n % C::kV]);
-        umma_commit(&sm.p_empty[n % C::kP]);
-      };
-      bool ok = wait_cta(&sm.k_full[0], 0, &sm.abort, p.wait);
-      tc_fence_after();
-      if (ok) issue_s(0);
-      for (int n = 0; n < n_tiles && ok; ++n) {
-        if (n + 1 < n_tiles) {
-          // its S^T columns are free: P of tile n - 1 was waited for below
-          ok = wait_cta(&sm.k_full[(n + 1) % C::kK], ((n + 1) / C::kK) & 1, &sm.abort, p.wait);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(n + 1);
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(tmem + s_slot * NQ, dk + (((kk / 4) * kBoxBytes + (kk % 4) * 32) >> 4),
+                      dq + (((kk / 4) * kQHalf + (kk % 4) * 32) >> 4), idesc_s, kk > 0);
+            umma_commit(&sm.s_full[s_slot]);
+            umma_commit(&sm.k_empty);
+            s_slot = s_slot == 2 ? 0 : s_slot + 1;
+            ++ns;
+            idle = 0;
+          } else if ((++idle & 63) == 0) {   // bounded, like wait_cta
+            if (idle == 64) t0 = globaltimer_ns();
+            if (*reinterpret_cast<volatile uint32_t *>(&sm.abort) != 0) ok = false;
+            if (ok && globaltimer_ns() - t0 > p.wait.limit_ns) {
+              *reinterpret_cast<volatile uint32_t *>(&sm.abort) = 1;
+              record_error(p.wait.err, kDevErrTimeout);
+              ok = false;
+            }
+          }
         }
-        ok = wait_cta(&sm.v_full[n % C::kV], (n / C::kV) & 1, &sm.abort, p.wait) &&
-             wait_cta(&sm.p_full[n % C::kP], (n / C::kP) & 1, &sm.abort, p.wait);
-        if (!ok) break;
-        tc_fence_after();
-        issue_o(n);
+        umma_commit(&sm.o_full);
+        umma_commit(&sm.drain);
+        drain_bar(&sm.drain, 0, p.wait.err, 4000000000ull);
       }
-      umma_commit(&sm.o_full);
-      umma_commit(&sm.drain);
-      drain_bar(&sm.drain, 0, p.wait.err, 4000000000ull);
-    }
-    __syncwarp();
-  } else if (warp < 4) {
-    // ===================== what each key brings along =====================
-    const int64_t t_lo = sm.tq_min, t_hi = sm.tq_max, lim = int64_t(1) << 24;
-    const int sh = 23 - p.sub_bits;
-    const int32_t r0 = fast_r0(p.sub_bits);
-    for (int n = warp - 1; n < n_tiles; n += 3) {
-      KeyBias &kb = sm.bias[n % kBias];
-      int64_t tk[4];
-      float c[4];
+      __syncwarp();
+    } else {
+      // ===================== what each key brings along =====================
+      if (warp == 1) {
+        // candidates' times, their range, and their distances to the earliest;
+        // a padding candidate takes the first one's
+        int64_t lo = INT64_MAX, hi = INT64_MIN;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        // keys behind the last take its values; their P is zeroed
-        const int32_t j = min((it.t0 + n) * kTile + x * 32 + lane, sq.len - 1);
-        tk[x] = cv.times[sq.row + j];
-        c[x] = __int_as_float(cv.pos[sq.row + j]);
+        for (int i = lane; i < NQ; i += 32) {
+          const int64_t t = p.cand_ts[q_row + (i < nq ? i : 0)];
+          sm.tq[i] = t;
+          lo = t < lo ? t : lo;
+          hi = t > hi ? t : hi;
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) {
+          const int64_t a = __shfl_xor_sync(0xffffffffu, lo, m);
+          const int64_t b = __shfl_xor_sync(0xffffffffu, hi, m);
+          lo = a < lo ? a : lo;
+          hi = b > hi ? b : hi;
+        }
+        __syncwarp();
+        for (int i = lane; i < NQ; i += 32) sm.tqd[i] = float(sm.tq[i] - lo);
+        if (lane == 0) {
+          sm.tq_min = lo;
+          sm.tq_max = hi;
+        }
       }
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        c[x] = half * qc_bias(rp[pos_bucket(int64_t(sq.pos) - __float_as_int(c[x]), p.nb_p)]);
-      // float time differences are exact: every one, and its two parts, below 2^24
-      bool one = true, near = p.sub_bits <= 4 && t_hi - t_lo < lim;
-      int32_t b_lo[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        b_lo[x] = time_bucket_i64(t_lo - tk[x], p.sub_bits, p.nb_t);
-        if (t_hi != t_lo)
-          one = one && b_lo[x] == time_bucket_i64(t_hi - tk[x], p.sub_bits, p.nb_t);
-        near = near && t_hi - tk[x] < lim && t_lo - tk[x] > -lim;
+      named_bar_sync(2, 96);
+      const int64_t t_lo = sm.tq_min, t_hi = sm.tq_max, lim = int64_t(1) << 24;
+      const int sh = 23 - p.sub_bits;
+      const int32_t r0 = fast_r0(p.sub_bits);
+      if (t_lo != t_hi && p.sub_bits <= 4) {   // candidates of several times: the exponent table
+        const int n = fast_table_size(p.sub_bits);
+        for (int x = tid - 32; x < n; x += 96)
+          sm.tbl_t[x] = half * qc_bias(rt[fast_table_bucket(x, p.sub_bits, p.nb_t)]);
+        named_bar_sync(2, 96);
       }
-      one = __all_sync(0xffffffffu, one);
-      near = __all_sync(0xffffffffu, near);
-      if (n >= kBias &&
-          !wait_cta_warp(&sm.bias_empty[n % kBias], ((n / kBias) - 1) & 1, &sm.abort, p.wait))
-        break;
-      int mode = one ? kTimeOne : near ? kTimeFloat : kTimeInt;
-      if (one) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) c[x] += half * qc_bias(rt[b_lo[x]]);
-      } else if (near) {
-        // table entries of the earliest and the latest candidate
-        float base[4];
-        int32_t e_lo[4], e_hi[4];
-        bool two = true;
+#pragma unroll 1
+      for (int n = warp - 1; n < n_tiles; n += 3) {
+        KeyBias &kb = sm.bias[n % kBias];
+        int64_t tk[4];
+        float c[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          base[x] = float(t_lo - tk[x]);
-          e_lo[x] = max(__float_as_int(base[x]) >> sh, r0) - r0;
-          e_hi[x] = max(__float_as_int(float(t_hi - tk[x])) >> sh, r0) - r0;
-          two = two && e_hi[x] - e_lo[x] <= 1;
+          // keys behind the last take its values; their P is zeroed
+          const int32_t j = min((it.t0 + n) * kTile + x * 32 + lane, sq.len - 1);
+          tk[x] = cv.times[sq.row + j];
+          c[x] = __int_as_float(cv.pos[sq.row + j]);
         }
-        if (__all_sync(0xffffffffu, two)) {
-          // The entry is e_lo + 1 exactly from the distance on whose bits are
-          // (e_lo + 1 + r0) << sh: an integer below 2^24 where both entries
-          // occur, so its difference to base is exact.
-          mode = kTimeTwo;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          c[x] = half * qc_bias(rp[pos_bucket(int64_t(sq.pos) - __float_as_int(c[x]), p.nb_p)]);
+        // float time differences are exact: every one, and its two parts, below 2^24
+        bool one = true, near = p.sub_bits <= 4 && t_hi - t_lo < lim;
+        int32_t b_lo[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          b_lo[x] = time_bucket_i64(t_lo - tk[x], p.sub_bits, p.nb_t);
+          if (t_hi != t_lo)
+            one = one && b_lo[x] == time_bucket_i64(t_hi - tk[x], p.sub_bits, p.nb_t);
+          near = near && t_hi - tk[x] < lim && t_lo - tk[x] > -lim;
+        }
+        one = __all_sync(0xffffffffu, one);
+        near = __all_sync(0xffffffffu, near);
+        if (n >= kBias &&
+            !wait_cta_warp(&sm.bias_empty[n % kBias], ((n / kBias) - 1) & 1, &sm.abort, p.wait))
+          break;
+        int mode = one ? kTimeOne : near ? kTimeFloat : kTimeInt;
+        if (one) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) c[x] += half * qc_bias(rt[b_lo[x]]);
+        } else if (near) {
+          // table entries of the earliest and the latest candidate
+          float base[4];
+          int32_t e_lo[4], e_hi[4];
+          bool two = true;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            kb.c2[x * 32 + lane] = c[x] + sm.tbl_t[e_hi[x]];
-            kb.t[x * 32 + lane] = __int_as_float((e_lo[x] + 1 + r0) << sh) - base[x];
-            c[x] += sm.tbl_t[e_lo[x]];
+            base[x] = float(t_lo - tk[x]);
+            e_lo[x] = max(__float_as_int(base[x]) >> sh, r0) - r0;
+            e_hi[x] = max(__float_as_int(float(t_hi - tk[x])) >> sh, r0) - r0;
+            two = two && e_hi[x] - e_lo[x] <= 1;
           }
-        } else {
+          if (__all_sync(0xffffffffu, two)) {
+            // The entry is e_lo + 1 exactly from the distance on whose bits are
+            // (e_lo + 1 + r0) << sh: an integer below 2^24 where both entries
+            // occur, so its difference to base is exact.
+            mode = kTimeTwo;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) kb.t[x * 32 + lane] = base[x];
+            for (int x = 0; x < 4; ++x) {
+              kb.c2[x * 32 + lane] = c[x] + sm.tbl_t[e_hi[x]];
+              kb.t[x * 32 + lane] = __int_as_float((e_lo[x] + 1 + r0) << sh) - base[x];
+              c[x] += sm.tbl_t[e_lo[x]];
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) kb.t[x * 32 + lane] = base[x];
+          }
         }
-      }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        kb.c[x * 32 + lane] = c[x];
-        kb.tk[x * 32 + lane] = tk[x];
+        for (int x = 0; x < 4; ++x) kb.c[x * 32 + lane] = c[x];
+        if (lane == 0) kb.mode = mode;
+        mbar_arrive(&sm.bias_full[n % kBias]);
       }
-      if (lane == 0) kb.mode = mode;
-      mbar_arrive(&sm.bias_full[n % kBias]);
     }
   } else if (warp < 12) {
     // ===================== elementwise =====================
+    regs_grow_ew<kRegsElem>();
     const int wg = (warp - 4) >> 2, quad = warp & 3;
     const int key = quad * 32 + lane;
     const uint32_t lanes = tmem + (uint32_t(quad * 32) << 16);
-    if (it.split == 0) {
-      // The candidates' own pairs, while the first tiles are decoded: 8 lanes
-      // per candidate, each NQ / 8 of them per warp; every load is issued ahead
-      // of the first sum.
-      constexpr int kPass = NQ / 32, kVec = D / 64;
-      const int sub = lane & 7;
-      uint4 qv[kPass][kVec], kv[kPass][kVec];
-#pragma unroll
-      for (int x = 0; x < kPass; ++x) {
-        const int i = (warp - 4) * (NQ / 8) + x * 4 + (lane >> 3);
-#pragma unroll
-        for (int y = 0; y < kVec; ++y) {
-          qv[x][y] = kv[x][y] = make_uint4(0, 0, 0, 0);
-          if (i < nq) {
-            const int64_t e = h * D + (y * 8 + sub) * 8;
-            qv[x][y] = load_row8(static_cast<const __nv_bfloat16 *>(p.q) + (q_row + i) * p.q_rs + e,
-                                 p.vec);
-            kv[x][y] = load_row8(static_cast<const __nv_bfloat16 *>(p.k) + (q_row + i) * p.k_rs + e,
-                                 p.vec);
-          }
-        }
+    {
+      // the queries, K-major in the 128-byte swizzle; rows behind the last are zero
+      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + q_row * p.q_rs + h * D;
+#pragma unroll 4
+      for (int x = tid - 128; x < NQ * (D / 8); x += kElemThreads) {
+        const int r = x / (D / 8), u = x % (D / 8);
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (r < nq) val = load_row8(q + r * p.q_rs + u * 8, p.vec);
+        *reinterpret_cast<uint4 *>(sm.q + (u >> 3) * kQHalf + r * 128 +
+                                   (((u & 7) ^ (r & 7)) << 4)) = val;
       }
-      const float bias = qc_bias(rp[0]) + qc_bias(rt[0]);
-#pragma unroll
-      for (int x = 0; x < kPass; ++x) {
-        float dot = 0.f;
-#pragma unroll
-        for (int y = 0; y < kVec; ++y) dot = dot8(qv[x][y], kv[x][y], dot);
-#pragma unroll
-        for (int m = 4; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-        const float xs = fmaf(p.alpha, dot, bias);
-        if (sub == 0)
-          sm.p_self[(warp - 4) * (NQ / 8) + x * 4 + (lane >> 3)] =
-              xs * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * xs));
-      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sm.q_full);
     }
     const float a = half * p.alpha;
     bool ok = true;
-    for (int n = wg; n < n_tiles; n += 2) {
-      const int32_t j = (it.t0 + n) * kTile + key;
-      const bool valid = j < sq.len;
-      const KeyBias &kb = sm.bias[n % kBias];
-      ok = wait_cta_warp(&sm.bias_full[n % kBias], (n / kBias) & 1, &sm.abort, p.wait);
+    int slot = wg, round = 0;   // n % 3, n / 3
+#pragma unroll 1
+    for (int n = wg; n < n_all; n += 2, slot += 2, slot -= slot >= 3 ? (++round, 3) : 0) {
+      const uint32_t s_col = lanes + slot * NQ;
+      uint8_t *pt = sm.p[wg] + key * 128;
+      if (n < self) {
+        // the candidates' own pairs: bias of distance 0, P's diagonal
+        ok = wait_cta_warp(&sm.s_full[0], 0, &sm.abort, p.wait);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t bits = 0;
+        if (quad * 32 < nq) {
+          uint32_t r[32];
+          tmem_ld32(s_col + quad * 32, r);
+          tmem_wait_ld(r);
+          uint32_t sv = 0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sv = lane == e ? r[e] : sv;
+          const float x = fmaf(p.alpha, __uint_as_float(sv), qc_bias(rp[0]) + qc_bias(rt[0]));
+          const float ps = x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
+          bits = key < nq ? pack_bf16x2(ps, 0.f) : 0u;
+        }
+        bits = key & 1 ? bits << 16 : bits;
+#pragma unroll
+        for (int u = 0; u < NQ / 8; ++u) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = (key >> 1) == u * 4 + e ? bits : 0u;
+          *reinterpret_cast<uint4 *>(pt + (u >> 3) * kBoxBytes + (((u & 7) ^ (key & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.p_full[0]);
+        continue;
+      }
+      const int m = n - self;                       // tile of the cache
+      const int32_t j = (it.t0 + m) * kTile + key;
+      const int bs = m % kBias;
+      const KeyBias &kb = sm.bias[bs];
+      ok = wait_cta_warp(&sm.bias_full[bs], (m / kBias) & 1, &sm.abort, p.wait);
       if (!ok) break;
       const int mode = kb.mode;
       const float c = kb.c[key];
+      // a key behind the last, or in a hidden bucket, adds exactly nothing
+      const bool valid = j < sq.len && !(mode == kTimeOne && c <= 0.5f * kQcBiasFloor);
       float c2 = 0.f, t = 0.f, wsum = 0.f;
       int64_t tk = 0;
       if (mode != kTimeOne) {
         c2 = kb.c2[key];
         t = kb.t[key];
-        tk = kb.tk[key];
+        if (mode == kTimeInt) tk = cv.times[sq.row + min(j, sq.len - 1)];
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.bias_empty[n % kBias]);
-      ok = wait_cta_warp(&sm.s_full[wg], (n >> 1) & 1, &sm.abort, p.wait);
-      if (ok && n >= C::kP)   // the product of the tile two back has read P
+      if (lane == 0) mbar_arrive(&sm.bias_empty[bs]);
+      ok = wait_cta_warp(&sm.s_full[slot], round & 1, &sm.abort, p.wait);
+      if (ok && n >= 2)   // the product of the tile two back has read P
         ok = wait_cta_warp(&sm.p_empty[wg], ((n >> 1) - 1) & 1, &sm.abort, p.wait);
       if (!ok) break;
       tc_fence_after();
-      uint8_t *pt = sm.p[wg] + key * 128;
 #define HSTU_QC_CHUNK(M_, A_, W_)                                                                \
   chunk<D, NQ, WEIGHTS, M_, A_, W_>(r, pk, sm, c0, a, c, c2, t, tk, rt, half, p.sub_bits, p.nb_t, \
                                     nq - c0, wsum)
       if (nq <= 16 && mode == kTimeOne) {   // few candidates: half a chunk
         constexpr int c0 = 0;
         uint32_t r[16], pk[8];
-        tmem_ld16(lanes + wg * NQ, r);
+        tmem_ld16(s_col, r);
         tmem_wait_ld(r);
         HSTU_QC_CHUNK(kTimeOne, !WEIGHTS, 16);
 #pragma unroll
@@ -513,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c0 = 0; c0 < nq; c0 += 32) {
           uint32_t r[32], pk[16];
-          tmem_ld32(lanes + wg * NQ + c0, r);
+          tmem_ld32(s_col + c0, r);
           tmem_wait_ld(r);
           if (mode == kTimeOne) {
             if (!WEIGHTS || nq - c0 >= 32)
@@ -543,126 +610,164 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();   // P^T is written
       mbar_arrive(&sm.p_full[wg]);
       if constexpr (WEIGHTS) {
-        if (valid) p.wpart[sq.wp0 + (int64_t(it.qtile) * H + h) * sq.len + j] = wsum;
+        if (j < sq.len)
+          p.wpart[sq.wp0 + (int64_t(it.qtile) * H + h) * sq.len + j] = valid ? wsum : 0.f;
       }
     }
-    // ---- O^T (tensor memory: lane = feature) + own pair -> rows of out ----
-    named_bar_sync(1, kElemThreads);   // p_self of all warps
+    // ---- O^T (lane = feature) through the P tiles' memory to rows of out ----
+    // each warpgroup its half of the candidates
     constexpr int kCols = NQ / 2;
     const int c_first = wg * kCols, c_end = min(c_first + kCols, nq);
-    if (ok && n_tiles > 0) ok = wait_cta_warp(&sm.o_full, 0, &sm.abort, p.wait);
+    if (ok) ok = wait_cta_warp(&sm.o_full, 0, &sm.abort, p.wait);
     tc_fence_after();
+    float *stage = reinterpret_cast<float *>(&sm.p[0][0]);   // [NQ][D]
     if (ok && quad * 32 < D) {
-      const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v) + q_row * p.v_rs + h * D + key;
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + q_row * p.o_rs + h * D + key;
-      float *acc = p.acc + ((sq.acc0 + (int64_t(it.split) * sq.n + i0) * H + h) * D + key);
 #pragma unroll 1
       for (int c0 = c_first; c0 < c_end; c0 += 16) {
         uint32_t r[16];
-        tmem_ld16(lanes + 2 * NQ + c0, r);
+        tmem_ld16(lanes + C::kO + c0, r);
         tmem_wait_ld(r);
-        float o[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          o[e] = n_tiles > 0 ? __uint_as_float(r[e]) : 0.f;
-          if (it.split == 0 && c0 + e < c_end)
-            o[e] = fmaf(sm.p_self[c0 + e], __bfloat162float(v[(c0 + e) * p.v_rs]), o[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int i = c0 + e;
-          if (i < c_end) {
-            if (sq.splits > 1)
-              acc[int64_t(i) * H * D] = o[e];
-            else
-              out[i * p.o_rs] = __float2bfloat16_rn(o[e] * p.scale);
+        for (int e = 0; e < 16; ++e) stage[(c0 + e) * D + key] = __uint_as_float(r[e]);
+      }
+    }
+    named_bar_sync(3 + wg, kElemThreads / 2);
+    if (ok) {
+      constexpr int kRowLanes = D / 4, kRows = 128 / kRowLanes;   // 4 features per lane
+      const int wt = (tid - 128) & 127, e = (wt % kRowLanes) * 4;
+#pragma unroll 2
+      for (int i = c_first + wt / kRowLanes; i < c_end; i += kRows) {
+        const float4 o = *reinterpret_cast<const float4 *>(stage + i * D + e);
+        if (sq.splits > 1) {
+          *reinterpret_cast<float4 *>(
+              p.acc + ((sq.acc0 + (int64_t(it.split) * sq.n + i0 + i) * H + h) * D + e)) = o;
+        } else {
+          __nv_bfloat16 *dst =
+              static_cast<__nv_bfloat16 *>(p.out) + (q_row + i) * p.o_rs + h * D + e;
+          const uint2 w = make_uint2(pack_bf16x2(o.x * p.scale, o.y * p.scale),
+                                     pack_bf16x2(o.z * p.scale, o.w * p.scale));
+          if (p.vec) {
+            *reinterpret_cast<uint2 *>(dst) = w;
+          } else {
+            reinterpret_cast<uint16_t *>(dst)[0] = uint16_t(w.x);
+            reinterpret_cast<uint16_t *>(dst)[1] = uint16_t(w.x >> 16);
+            reinterpret_cast<uint16_t *>(dst)[2] = uint16_t(w.y);
+            reinterpret_cast<uint16_t *>(dst)[3] = uint16_t(w.y >> 16);
           }
         }
       }
     }
   } else {
-    // ===================== decoding K and V =====================
+    // ===================== decoding K (warps 12-19) and V (20-27) =====================
     // A warp takes 8 rows x 4 groups (16 x 2 at D = 64) of a tile, 512 bytes in
     // one piece.  Eight lanes that store together hold 4 rows x 2 neighbouring
     // groups, whose 16-byte chunks lie in eight different banks under the
     // swizzle.
-    constexpr int G = D / 32;                      // groups per row
-    constexpr int kPer = kTile * G / kDecThreads;  // groups per thread and tile
-    constexpr int kStep = kDecThreads / G;         // rows between a thread's groups
-    const int dw = warp - 12;
+    regs_release_ctl<kRegsDec>();
+    const bool is_v = warp >= 20;
+    const int dw = is_v ? warp - 20 : warp - 12, dt = dw * 32 + lane;
     const int row = G == 4 ? dw * 8 + ((lane >> 4) << 2) + ((lane >> 1) & 3)
                            : dw * 16 + (lane >> 1);
     const int g = G == 4 ? ((lane >> 3) & 1) * 2 + (lane & 1) : lane & 1;
-    const int64_t at = (int64_t(h) * cv.rows + sq.row + int64_t(it.t0) * kTile + row) * G + g;
-    const uint4 *kc = reinterpret_cast<const uint4 *>(cv.k_codes) + at;
-    const uint4 *vc = reinterpret_cast<const uint4 *>(cv.v_codes) + at;
-    const uint16_t *ks = cv.k_scales + at, *vs = cv.v_scales + at;
-    int32_t left = sq.len - it.t0 * kTile - row;   // rows of the sequence from this one on
     uint32_t off[4];   // where the group's chunks go in a tile
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       off[e] = (g >> 1) * kBoxBytes + row * 128 + ((((g & 1) * 4 + e) ^ (row & 7)) << 4);
-    struct Raw {
-      uint4 k[kPer], v[kPer];
-      uint32_t kp[kPer], vp[kPer];
-    };
-    auto fetch = [&](Raw &r) {
+    // codes: a thread copies what it decodes itself; a row's parameters come
+    // through the lane of its first group
+    const int64_t at = (int64_t(h) * cv.rows + sq.row + int64_t(it.t0) * kTile + row) * G + g;
+    const uint8_t *src = reinterpret_cast<const uint8_t *>(is_v ? cv.v_codes : cv.k_codes);
+    const uint8_t *psrc = reinterpret_cast<const uint8_t *>(is_v ? cv.v_scales : cv.k_scales);
+    const uint8_t *const src0 = src, *const psrc0 = psrc;
+    src += at * 16;
+    psrc += at * 2;
+    int32_t left = sq.len - it.t0 * kTile - row;   // the sequence's rows from this one on
+    uint8_t *const codes = is_v ? sm.v_codes[0] : sm.k_codes[0];
+    uint8_t *const scales = is_v ? sm.v_scales[0] : sm.k_scales[0];
+    const uint32_t code_dst = smem_u32(codes) + dt * 16;
+    const uint32_t scale_dst = smem_u32(scales) + row * 2 * G;
+    auto copy = [&](int st) {   // the next tile of the cache into stage st
 #pragma unroll
       for (int x = 0; x < kPer; ++x) {
-        if (x * kStep < left) {
-          r.k[x] = ld_stream(kc + x * kDecThreads);
-          r.v[x] = ld_stream(vc + x * kDecThreads);
-          r.kp[x] = ks[x * kDecThreads];
-          r.vp[x] = vs[x * kDecThreads];
-        } else {   // behind the last row: zeros
-          r.k[x] = r.v[x] = make_uint4(0, 0, 0, 0);
-          r.kp[x] = r.vp[x] = 0;
-        }
+        const bool ok = x * kStep < left;
+        cp_async<16>(code_dst + st * C::kCodeBytes + x * kDecThreads * 16,
+                     ok ? src + x * kDecThreads * 16 : src0, ok);
+        if (g == 0)
+          cp_async<2 * G>(scale_dst + st * C::kScaleBytes + x * kStep * 2 * G,
+                          ok ? psrc + x * kDecThreads * 2 : psrc0, ok);
       }
-      kc += kTile * G;
-      vc += kTile * G;
-      ks += kTile * G;
-      vs += kTile * G;
+      src += kTile * G * 16;
+      psrc += kTile * G * 2;
       left -= kTile;
     };
-    auto store = [&](uint32_t tile, const uint4 (&code)[kPer], const uint32_t (&par)[kPer]) {
+    int m_copy = 0;
+#pragma unroll 1
+    for (; m_copy < C::kStages; ++m_copy) {
+      if (m_copy < n_tiles) copy(m_copy);
+      cp_async_commit();
+    }
+    uint64_t *const full = is_v ? sm.v_full : &sm.k_full;
+    uint64_t *const empty = is_v ? sm.v_empty : &sm.k_empty;
+    const uint32_t tile0 = smem_u32(is_v ? sm.v[0] : sm.k);
+    const int two = is_v ? 1 : 0;   // V: two tiles in turn
+    bool ok = true;
+    int st = 0;
+#pragma unroll 1
+    for (int n = 0; n < n_all; ++n) {
+      const int buf = two ? n & 1 : 0, round = n >> two;
+      const uint32_t tile = tile0 + buf * C::kTileBytes;
+      if (n < self) {
+        // the candidates' own keys or values, bf16 already
+        const __nv_bfloat16 *own =
+            is_v ? static_cast<const __nv_bfloat16 *>(p.v) + q_row * p.v_rs + h * D + g * 32
+                 : static_cast<const __nv_bfloat16 *>(p.k) + q_row * p.k_rs + h * D + g * 32;
+        const int64_t rs = is_v ? p.v_rs : p.k_rs;
 #pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        uint32_t zz, ss;
-        q4_group(par[x], zz, ss);
-        const uint32_t w[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
+        for (int x = 0; x < kPer; ++x) {
+          const int i = row + x * kStep;
+          uint4 w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t o[4];
-          q4_decode_bf16(w[e], zz, ss, o);
-          st_shared_v4(tile + off[e] + x * kStep * 128, o);
+          for (int e = 0; e < 4; ++e)
+            w[e] = i < nq ? load_row8(own + i * rs + e * 8, p.vec) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t o[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+            st_shared_v4(tile + off[e] + x * kStep * 128, o);
+          }
+        }
+      } else {
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();   // the row's parameters came through another lane of this warp
+        if (round > 0) ok = wait_cta_warp(&empty[buf], (round - 1) & 1, &sm.abort, p.wait);
+        if (!ok) break;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          const uint4 code = *reinterpret_cast<const uint4 *>(codes + st * C::kCodeBytes +
+                                                              (x * kDecThreads + dt) * 16);
+          uint32_t zz, ss;
+          q4_group(*reinterpret_cast<const uint16_t *>(scales + st * C::kScaleBytes +
+                                                       ((row + x * kStep) * G + g) * 2),
+                   zz, ss);
+          const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t o[4];
+            q4_decode_bf16(w[e], zz, ss, o);
+            st_shared_v4(tile + off[e] + x * kStep * 128, o);
+          }
         }
       }
-    };
-    const uint32_t k0 = smem_u32(sm.k[0]), v0 = smem_u32(sm.v[0]);
-    Raw raw[2];
-    fetch(raw[0]);
-    fetch(raw[1]);
-    bool ok = true;
-    auto step = [&](int n, Raw &r) {
-      if (n >= C::kK)
-        ok = wait_cta_warp(&sm.k_empty[n % C::kK], ((n / C::kK) - 1) & 1, &sm.abort, p.wait);
-      if (!ok) return;
-      store(k0 + (n % C::kK) * C::kTileBytes, r.k, r.kp);
       fence_proxy_async_smem();
-      mbar_arrive(&sm.k_full[n % C::kK]);
-      if (n >= C::kV)
-        ok = wait_cta_warp(&sm.v_empty[n % C::kV], ((n / C::kV) - 1) & 1, &sm.abort, p.wait);
-      if (!ok) return;
-      store(v0 + (n % C::kV) * C::kTileBytes, r.v, r.vp);
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.v_full[n % C::kV]);
-      fetch(r);
-    };
-    for (int n = 0; n < n_tiles && ok; n += 2) {
-      step(n, raw[0]);
-      if (ok && n + 1 < n_tiles) step(n + 1, raw[1]);
+      mbar_arrive(&full[buf]);
+      if (n >= self) {
+        __syncwarp();   // the warp has read the stage
+        if (m_copy < n_tiles) copy(st);
+        cp_async_commit();
+        ++m_copy;
+        st = st == C::kStages - 1 ? 0 : st + 1;
+      }
     }
+    cp_async_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
@@ -677,7 +782,15 @@ cudaError_t launch_t(const QcAttnParams &p, cudaStream_t st) {
   constexpr size_t smem = sizeof(Smem<D, NQ>) + 1024;
   static_assert(smem <= 232448, "shared memory");
   static PerDeviceOnce attr;
-  cudaError_t e = set_smem_once(attr, attn_kernel<D, NQ, WEIGHTS>, smem);
+  cudaError_t e = attr.run([&](int) {
+    // the register split needs exactly what the kernel was launched with
+    cudaFuncAttributes fa;
+    const cudaError_t err = cudaFuncGetAttributes(&fa, attn_kernel<D, NQ, WEIGHTS>);
+    if (err != cudaSuccess) return err;
+    if (fa.numRegs != kRegsAll) return cudaErrorInvalidKernelImage;
+    return cudaFuncSetAttribute(attn_kernel<D, NQ, WEIGHTS>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  });
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(p.items) * unsigned(p.cache.heads);
   attn_kernel<D, NQ, WEIGHTS><<<grid, kThreads, smem, st>>>(p);

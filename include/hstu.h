@@ -285,8 +285,8 @@ hstu_status_t hstu_layer_fwd_candidates(
  *           z in the low 4 bits.
  * All buffers are the caller's (device memory).  Rows are addressed per
  * sequence by host arrays: sequence b owns rows [rows_host[b], + its length);
- * their order within the region carries no meaning.  Alignment: codes 16
- * bytes, the others their element.  weight may be NULL where no call updates
+ * their order within the region carries no meaning.  Alignment: codes and
+ * scales 16 bytes, the others their element.  weight may be NULL where no call updates
  * or reads it. */
 typedef struct {
   int64_t rows;                  /* capacity, 0..2^40 */
