@@ -15,8 +15,9 @@
 // the tile 128 keys high for a single candidate (NQ only pads the N side).
 //
 //   warps 12-19  keys: bring codes to shared memory (cp.async, ahead), decode
-//                them exactly to bf16, write K tiles in the 128-byte swizzle.
-//   warps 20-27  the same for values.
+//                them exactly to bf16 and write K to tensor memory (lane = key),
+//                from where the MMA takes it.
+//   warps 20-27  values the same way, V to shared memory in the 128-byte swizzle.
 //   warp 0       issues the MMAs, whichever has its operands: O^T of a tile
 //                first, else S^T up to two tiles ahead.
 //   warps 4-11   two warpgroups, taking tiles by turns: read S^T (thread = key),
@@ -26,7 +27,11 @@
 //                along (KeyBias).
 // The candidates' own pairs are one more tile, the first of the range that has
 // them: its keys are the candidates and only P's diagonal is kept.
-// Tensor memory: S^T of tile n in [(n % 3) NQ, + NQ), O^T in [3 NQ, 4 NQ).
+// Shared-memory traffic is what bounds the loop once the decoding keeps up (an
+// MMA with both operands there and N = 128 takes all of its 128 bytes a cycle):
+// keeping K out of it saves 32 KB written and 32 KB read of about 260 KB per tile
+// at D = 128, NQ = 128.
+// Tensor memory: S^T slots, then O^T, then two K tiles (Cfg).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,6 +40,7 @@
 
 namespace hstu {
 namespace qc_tc {
+
 
 constexpr int kTile = kQcKeyTile;
 constexpr int kThreads = 896;
@@ -50,8 +56,6 @@ constexpr uint32_t kBoxBytes = kTile * 128;   // 128 rows of 64 bf16
 template <int D, int NQ>
 struct Cfg {
   static constexpr int kTileBytes = kTile * D * 2;
-  // One K tile: it is free again as soon as S^T is done.  A V tile lives until
-  // its P is there: two of them.
   static constexpr int kV = 2;
   static constexpr int kPBytes = NQ / 64 * int(kBoxBytes);
   // Tiles of codes on their way: with few candidates the cache's bandwidth is
@@ -59,9 +63,11 @@ struct Cfg {
   // full HBM rate; with many a tile's time covers the latency.
   static constexpr int kStages = D == 128 ? (NQ == 128 ? 1 : 3) : 4;
   static constexpr int kCodeBytes = kTile * D / 2;       // of one tile of K (or V)
-  static constexpr int kScaleBytes = kTile * D / 16;
-  static constexpr uint32_t kTmemCols = 4 * NQ;
-  static constexpr uint32_t kO = 3 * NQ;                 // first column of O^T
+  static constexpr int kScaleBytes = kTile * 8;          // 8 bytes per row (4 used at D = 64)
+  // Tensor memory columns: kS slots of S^T, O^T, two K tiles.
+  static constexpr int kS = NQ == 128 ? 2 : 3;
+  static constexpr uint32_t kO = kS * NQ, kK = kO + NQ;
+  static_assert(kK + 2 * (D / 2) <= 512, "tensor memory");
 };
 
 // How the time bias of a tile's keys is found.  kTimeOne: the same for all
@@ -84,7 +90,6 @@ template <int D, int NQ>
 struct Smem {
   using C = Cfg<D, NQ>;
   alignas(1024) uint8_t q[NQ * D * 2];
-  alignas(1024) uint8_t k[C::kTileBytes];
   alignas(1024) uint8_t v[C::kV][C::kTileBytes];
   alignas(1024) uint8_t p[2][C::kPBytes];       // behind v: see the D = 64 note at issue_o
   alignas(16) uint8_t k_codes[C::kStages][C::kCodeBytes];
@@ -96,9 +101,9 @@ struct Smem {
   alignas(16) float tqd[NQ];      // and relative to the earliest of them
   float tbl_t[kTblT];
   int64_t tq_min, tq_max;
-  uint64_t k_full, k_empty, v_full[C::kV], v_empty[C::kV];
-  uint64_t s_full[3];             // a warpgroup takes every other round of a slot: the commits
-                                  // are in order, so the round between is over by then
+  uint64_t k_full[2], k_empty[2], v_full[C::kV], v_empty[C::kV];
+  uint64_t s_full[3];             // with three slots a warpgroup takes every other round of one:
+                                  // the commits are in order, so the round between is over by then
   uint64_t p_full[2], p_empty[2];
   uint64_t bias_full[kBias], bias_empty[kBias];
   uint64_t q_full, o_full, drain;
@@ -150,7 +155,7 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t *v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3])
                : "memory");
@@ -288,9 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 64) {
     mbar_init(&sm.q_full, kElemThreads);
-    mbar_init(&sm.k_full, kDecThreads);
-    mbar_init(&sm.k_empty, 1);
-    for (int i = 0; i < C::kV; ++i) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.k_full[i], kDecThreads);
+      mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], kDecThreads);
       mbar_init(&sm.v_empty[i], 1);
     }
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(&sm.tmem_base, C::kTmemCols);
+    tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -325,14 +330,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc_s = idesc_bf16(kTile, NQ, false, false);
         constexpr uint32_t idesc_o = idesc_bf16(128, NQ, true, true);
         const uint64_t dq = sdesc_sw128(smem_u32(sm.q), 16, 1024);
-        const uint64_t dk = sdesc_sw128(smem_u32(sm.k), 16, 1024);
         bool ok = wait_cta(&sm.q_full, 0, &sm.abort, p.wait);
-        int ns = 0, no = 0, s_slot = 0;   // next S^T, next O^T; ns % 3
+        int ns = 0, no = 0, s_slot = 0;   // next S^T, next O^T; ns % kS
         uint32_t idle = 0;
         uint64_t t0 = 0;
         while (ok && no < n_all) {
-          if (no < ns && mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1) &&
-              mbar_test_wait(&sm.v_full[no & 1], (no >> 1) & 1)) {
+          // S^T first: the warpgroup that takes it may be waiting, and its columns
+          // are free once P of the tile that had them is there
+          if (ns < n_all && ns <= no + C::kS &&
+              mbar_test_wait(&sm.k_full[ns & 1], (ns >> 1) & 1) &&
+              (ns < no + C::kS || mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1))) {
+            tc_fence_after();
+            const uint32_t k = tmem + C::kK + (ns & 1) * (D / 2);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ts(tmem + s_slot * NQ, k + kk * 8, dq + (((kk / 4) * kQHalf + (kk % 4) * 32) >> 4),
+                      idesc_s, kk > 0);
+            umma_commit(&sm.s_full[s_slot]);
+            umma_commit(&sm.k_empty[ns & 1]);
+            s_slot = s_slot == C::kS - 1 ? 0 : s_slot + 1;
+            ++ns;
+            idle = 0;
+          } else if (no < ns && mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1) &&
+                     mbar_test_wait(&sm.v_full[no & 1], (no >> 1) & 1)) {
             // D = 64: the instruction is 128 rows high all the same; rows 64-127
             // read whatever lies one box behind the V tile (the next V tile or P,
             // inside this struct) and fill tensor-memory lanes that nobody reads.
@@ -346,18 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(&sm.v_empty[no & 1]);
             umma_commit(&sm.p_empty[no & 1]);
             ++no;
-            idle = 0;
-          } else if (ns < n_all && ns < no + 3 && mbar_test_wait(&sm.k_full, ns & 1)) {
-            // the columns of S^T are free: P of tile ns - 3 is there
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(tmem + s_slot * NQ, dk + (((kk / 4) * kBoxBytes + (kk % 4) * 32) >> 4),
-                      dq + (((kk / 4) * kQHalf + (kk % 4) * 32) >> 4), idesc_s, kk > 0);
-            umma_commit(&sm.s_full[s_slot]);
-            umma_commit(&sm.k_empty);
-            s_slot = s_slot == 2 ? 0 : s_slot + 1;
-            ++ns;
             idle = 0;
           } else if ((++idle & 63) == 0) {   // bounded, like wait_cta
             if (idle == 64) t0 = globaltimer_ns();
@@ -501,9 +509,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const float a = half * p.alpha;
     bool ok = true;
-    int slot = wg, round = 0;   // n % 3, n / 3
+    int slot = wg, round = 0;   // n % kS, n / kS
 #pragma unroll 1
-    for (int n = wg; n < n_all; n += 2, slot += 2, slot -= slot >= 3 ? (++round, 3) : 0) {
+    for (int n = wg; n < n_all; n += 2, slot += 2, slot -= slot >= C::kS ? (++round, C::kS) : 0) {
       const uint32_t s_col = lanes + slot * NQ;
       uint8_t *pt = sm.p[wg] + key * 128;
       if (n < self) {
@@ -658,44 +666,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ===================== decoding K (warps 12-19) and V (20-27) =====================
-    // A warp takes 8 rows x 4 groups (16 x 2 at D = 64) of a tile, 512 bytes in
-    // one piece.  Eight lanes that store together hold 4 rows x 2 neighbouring
-    // groups, whose 16-byte chunks lie in eight different banks under the
-    // swizzle.
+    // ===================== decoding =====================
+    // K (warps 12-19): thread = key and half of the row, since a warp writes its
+    // own 32 lanes of tensor memory.  V (warps 20-27): a warp takes 8 rows x 4
+    // groups (16 x 2 at D = 64), 512 bytes in one piece; eight lanes that store
+    // together hold 4 rows x 2 neighbouring groups, whose 16-byte chunks lie in
+    // eight different banks under the swizzle.
     regs_release_ctl<kRegsDec>();
     const bool is_v = warp >= 20;
-    const int dw = is_v ? warp - 20 : warp - 12, dt = dw * 32 + lane;
-    const int row = G == 4 ? dw * 8 + ((lane >> 4) << 2) + ((lane >> 1) & 3)
-                           : dw * 16 + (lane >> 1);
-    const int g = G == 4 ? ((lane >> 3) & 1) * 2 + (lane & 1) : lane & 1;
-    uint32_t off[4];   // where the group's chunks go in a tile
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      off[e] = (g >> 1) * kBoxBytes + row * 128 + ((((g & 1) * 4 + e) ^ (row & 7)) << 4);
-    // codes: a thread copies what it decodes itself; a row's parameters come
-    // through the lane of its first group
+    const int dw = is_v ? warp - 20 : warp - 12, dt = dw * 32 + lane, hx = dw >> 2;
+    const int row = !is_v    ? (dw & 3) * 32 + lane
+                    : G == 4 ? dw * 8 + ((lane >> 4) << 2) + ((lane >> 1) & 3)
+                             : dw * 16 + (lane >> 1);
+    // first group of the thread; its next is one group (K) or kStep rows (V) on
+    const int g = !is_v    ? hx * kPer
+                  : G == 4 ? ((lane >> 3) & 1) * 2 + (lane & 1)
+                           : lane & 1;
     const int64_t at = (int64_t(h) * cv.rows + sq.row + int64_t(it.t0) * kTile + row) * G + g;
     const uint8_t *src = reinterpret_cast<const uint8_t *>(is_v ? cv.v_codes : cv.k_codes);
     const uint8_t *psrc = reinterpret_cast<const uint8_t *>(is_v ? cv.v_scales : cv.k_scales);
     const uint8_t *const src0 = src, *const psrc0 = psrc;
     src += at * 16;
-    psrc += at * 2;
+    // parameters travel 4 bytes and more at a time: K both groups of the thread
+    // (at D = 64 of the row), V a whole row through the lane of its first group
+    psrc += (at - (!is_v && G == 2 ? g : 0)) * 2;
     int32_t left = sq.len - it.t0 * kTile - row;   // the sequence's rows from this one on
     uint8_t *const codes = is_v ? sm.v_codes[0] : sm.k_codes[0];
     uint8_t *const scales = is_v ? sm.v_scales[0] : sm.k_scales[0];
-    const uint32_t code_dst = smem_u32(codes) + dt * 16;
-    const uint32_t scale_dst = smem_u32(scales) + row * 2 * G;
+    // where the thread's codes lie in a stage; for K a row's chunks are permuted
+    // so that 8 lanes (rows) that read together touch every bank once
+    uint32_t code_at[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x)
+      code_at[x] = is_v ? (x * kDecThreads + dt) * 16
+                   : G == 4 ? row * 64 + (((g + x) ^ ((row >> 1) & 3)) << 4)
+                            : row * 32 + ((g ^ ((row >> 2) & 1)) << 4);
+    const uint32_t scale_at = is_v ? row * 2 * G : hx * (kTile * 4) + row * 4;
+    const uint32_t code_dst = smem_u32(codes), scale_dst = smem_u32(scales) + scale_at;
     auto copy = [&](int st) {   // the next tile of the cache into stage st
 #pragma unroll
       for (int x = 0; x < kPer; ++x) {
-        const bool ok = x * kStep < left;
-        cp_async<16>(code_dst + st * C::kCodeBytes + x * kDecThreads * 16,
-                     ok ? src + x * kDecThreads * 16 : src0, ok);
-        if (g == 0)
+        const bool ok = (is_v ? x * kStep : 0) < left;
+        cp_async<16>(code_dst + st * C::kCodeBytes + code_at[x],
+                     ok ? src + (is_v ? x * kDecThreads : x) * 16 : src0, ok);
+        if (is_v && g == 0)
           cp_async<2 * G>(scale_dst + st * C::kScaleBytes + x * kStep * 2 * G,
                           ok ? psrc + x * kDecThreads * 2 : psrc0, ok);
       }
+      if (!is_v)
+        cp_async<4>(scale_dst + st * C::kScaleBytes, 0 < left ? psrc : psrc0, 0 < left);
       src += kTile * G * 16;
       psrc += kTile * G * 2;
       left -= kTile;
@@ -706,58 +725,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (m_copy < n_tiles) copy(m_copy);
       cp_async_commit();
     }
-    uint64_t *const full = is_v ? sm.v_full : &sm.k_full;
-    uint64_t *const empty = is_v ? sm.v_empty : &sm.k_empty;
-    const uint32_t tile0 = smem_u32(is_v ? sm.v[0] : sm.k);
-    const int two = is_v ? 1 : 0;   // V: two tiles in turn
+    uint64_t *const full = is_v ? sm.v_full : sm.k_full;
+    uint64_t *const empty = is_v ? sm.v_empty : sm.k_empty;
+    // V: where the group's chunks go in a tile.  K: its columns.
+    uint32_t off[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      off[e] = (g >> 1) * kBoxBytes + row * 128 + ((((g & 1) * 4 + e) ^ (row & 7)) << 4);
+    const uint32_t v_tile = smem_u32(sm.v[0]);
+    const uint32_t k_tile = tmem + (uint32_t((dw & 3) * 32) << 16) + C::kK + hx * (kPer * 16);
+    const __nv_bfloat16 *own =   // the candidates' own keys or values
+        is_v ? static_cast<const __nv_bfloat16 *>(p.v) + q_row * p.v_rs + h * D + g * 32
+             : static_cast<const __nv_bfloat16 *>(p.k) + q_row * p.k_rs + h * D + g * 32;
+    const int64_t rs = is_v ? p.v_rs : p.k_rs;
     bool ok = true;
     int st = 0;
 #pragma unroll 1
     for (int n = 0; n < n_all; ++n) {
-      const int buf = two ? n & 1 : 0, round = n >> two;
-      const uint32_t tile = tile0 + buf * C::kTileBytes;
-      if (n < self) {
-        // the candidates' own keys or values, bf16 already
-        const __nv_bfloat16 *own =
-            is_v ? static_cast<const __nv_bfloat16 *>(p.v) + q_row * p.v_rs + h * D + g * 32
-                 : static_cast<const __nv_bfloat16 *>(p.k) + q_row * p.k_rs + h * D + g * 32;
-        const int64_t rs = is_v ? p.v_rs : p.k_rs;
+      const int buf = n & 1, round = n >> 1;
+      if (n >= self) {
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();   // V: the row's parameters came through another lane of this warp
+      }
+      if (round > 0) ok = wait_cta_warp(&empty[buf], (round - 1) & 1, &sm.abort, p.wait);
+      if (!ok) break;
+      if (!is_v) tc_fence_after();
 #pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-          const int i = row + x * kStep;
-          uint4 w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = i < nq ? load_row8(own + i * rs + e * 8, p.vec) : make_uint4(0, 0, 0, 0);
+      for (int x = 0; x < kPer; ++x) {
+        uint32_t o[16];
+        if (n < self) {
+          const int i = row + (is_v ? x * kStep : 0);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t o[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
-            st_shared_v4(tile + off[e] + x * kStep * 128, o);
+            const uint4 w = i < nq ? load_row8(own + i * rs + (is_v ? 0 : x * 32) + e * 8, p.vec)
+                                   : make_uint4(0, 0, 0, 0);
+            o[4 * e] = w.x;
+            o[4 * e + 1] = w.y;
+            o[4 * e + 2] = w.z;
+            o[4 * e + 3] = w.w;
           }
-        }
-      } else {
-        cp_async_wait<C::kStages - 1>();
-        __syncwarp();   // the row's parameters came through another lane of this warp
-        if (round > 0) ok = wait_cta_warp(&empty[buf], (round - 1) & 1, &sm.abort, p.wait);
-        if (!ok) break;
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-          const uint4 code = *reinterpret_cast<const uint4 *>(codes + st * C::kCodeBytes +
-                                                              (x * kDecThreads + dt) * 16);
+        } else {
+          const uint4 code =
+              *reinterpret_cast<const uint4 *>(codes + st * C::kCodeBytes + code_at[x]);
+          const uint32_t par = *reinterpret_cast<const uint16_t *>(
+              scales + st * C::kScaleBytes + scale_at +
+              (is_v ? x * kStep * 2 * G + g * 2 : G == 4 ? x * 2 : g * 2));
           uint32_t zz, ss;
-          q4_group(*reinterpret_cast<const uint16_t *>(scales + st * C::kScaleBytes +
-                                                       ((row + x * kStep) * G + g) * 2),
-                   zz, ss);
+          q4_group(par, zz, ss);
           const uint32_t w[4] = {code.x, code.y, code.z, code.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            uint32_t o[4];
-            q4_decode_bf16(w[e], zz, ss, o);
-            st_shared_v4(tile + off[e] + x * kStep * 128, o);
+            uint32_t v4[4];
+            q4_decode_bf16(w[e], zz, ss, v4);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[4 * e + u] = v4[u];
           }
         }
+        if (is_v) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            st_shared_v4(v_tile + buf * C::kTileBytes + off[e] + x * kStep * 128, &o[4 * e]);
+        } else {
+          tmem_st16(k_tile + buf * (D / 2) + x * 16, o);
+        }
       }
-      fence_proxy_async_smem();
+      if (is_v) {
+        fence_proxy_async_smem();
+      } else {
+        tmem_wait_st();
+        tc_fence_before();
+      }
       mbar_arrive(&full[buf]);
       if (n >= self) {
         __syncwarp();   // the warp has read the stage
@@ -773,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
