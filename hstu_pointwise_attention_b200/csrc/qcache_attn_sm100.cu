@@ -261,6 +261,160 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W /
   }
 }
 
+// The decoding warps of K (IS_V false) or V: tiles of codes from the cache into
+// stages (cp.async), from there to bf16, K to tensor memory, V to shared memory.
+//   K: thread = key and half of the row, since a warp writes its own 32 lanes of
+//   tensor memory; a row's chunks are permuted in the stage so that 8 lanes that
+//   read together touch every bank once.
+//   V: a warp takes 8 rows x 4 groups (16 x 2 at D = 64), 512 bytes in one piece;
+//   eight lanes that store together hold 4 rows x 2 neighbouring groups, whose
+//   16-byte chunks lie in eight different banks under the swizzle.
+template <int D, int NQ, bool IS_V>
+__device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> &sm,
+                                             const QcItem &it, const QcAttnSeq &sq, int h,
+                                             int64_t q_row, int nq, uint32_t tmem, int dw,
+                                             int lane) {
+  using C = Cfg<D, NQ>;
+  constexpr int G = D / 32;                      // groups per row
+  constexpr int kPer = kTile * G / kDecThreads;  // groups per thread and tile
+  constexpr int kStep = kDecThreads / G;         // V: rows between a thread's groups
+  const QCacheView &cv = p.cache;
+  const int dt = dw * 32 + lane, hx = dw >> 2;
+  const int n_tiles = it.t1 - it.t0, self = it.split == 0 ? 1 : 0, n_all = n_tiles + self;
+  const int row = !IS_V    ? (dw & 3) * 32 + lane
+                  : G == 4 ? dw * 8 + ((lane >> 4) << 2) + ((lane >> 1) & 3)
+                           : dw * 16 + (lane >> 1);
+  const int g = !IS_V ? hx * kPer : G == 4 ? ((lane >> 3) & 1) * 2 + (lane & 1) : lane & 1;
+  const int64_t at = (int64_t(h) * cv.rows + sq.row + int64_t(it.t0) * kTile + row) * G + g;
+  const uint8_t *const src0 = reinterpret_cast<const uint8_t *>(IS_V ? cv.v_codes : cv.k_codes);
+  const uint8_t *const psrc0 = reinterpret_cast<const uint8_t *>(IS_V ? cv.v_scales : cv.k_scales);
+  const uint8_t *src = src0 + at * 16;
+  // parameters travel 4 bytes and more at a time: K both groups of the thread
+  // (at D = 64 of the row), V a whole row through the lane of its first group
+  const uint8_t *psrc = psrc0 + (at - (!IS_V && G == 2 ? g : 0)) * 2;
+  int32_t left = sq.len - it.t0 * kTile - row;   // the sequence's rows from this one on
+  uint8_t *const codes = IS_V ? sm.v_codes[0] : sm.k_codes[0];
+  uint8_t *const scales = IS_V ? sm.v_scales[0] : sm.k_scales[0];
+  uint32_t code_at[kPer];   // where the thread's codes lie in a stage
+#pragma unroll
+  for (int x = 0; x < kPer; ++x)
+    code_at[x] = IS_V     ? (x * kDecThreads + dt) * 16
+                 : G == 4 ? row * 64 + (((g + x) ^ ((row >> 1) & 3)) << 4)
+                          : row * 32 + ((g ^ ((row >> 2) & 1)) << 4);
+  const uint32_t scale_at = IS_V ? row * 2 * G : hx * (kTile * 4) + row * 4;
+  const uint32_t code_dst = smem_u32(codes), scale_dst = smem_u32(scales) + scale_at;
+  auto copy = [&](int st) {   // the next tile of the cache into stage st
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const bool ok = (IS_V ? x * kStep : 0) < left;
+      cp_async<16>(code_dst + st * C::kCodeBytes + code_at[x],
+                   ok ? src + (IS_V ? x * kDecThreads : x) * 16 : src0, ok);
+      if (IS_V && g == 0)
+        cp_async<2 * G>(scale_dst + st * C::kScaleBytes + x * kStep * 2 * G,
+                        ok ? psrc + x * kDecThreads * 2 : psrc0, ok);
+    }
+    if (!IS_V) cp_async<4>(scale_dst + st * C::kScaleBytes, 0 < left ? psrc : psrc0, 0 < left);
+    src += kTile * G * 16;
+    psrc += kTile * G * 2;
+    left -= kTile;
+  };
+  int m_copy = 0;
+#pragma unroll 1
+  for (; m_copy < C::kStages; ++m_copy) {
+    if (m_copy < n_tiles) copy(m_copy);
+    cp_async_commit();
+  }
+  uint64_t *const full = IS_V ? sm.v_full : sm.k_full;
+  uint64_t *const empty = IS_V ? sm.v_empty : sm.k_empty;
+  uint32_t off[4];   // V: where the group's chunks go in a tile
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    off[e] = smem_u32(sm.v[0]) + (g >> 1) * kBoxBytes + row * 128 +
+             ((((g & 1) * 4 + e) ^ (row & 7)) << 4);
+  const uint32_t k_tile = tmem + (uint32_t((dw & 3) * 32) << 16) + C::kK + hx * (kPer * 16);
+  // 32 values of group x to their place in tile buffer `buf`
+  auto put = [&](int buf, int x, const uint32_t (&o)[16]) {
+    if constexpr (IS_V) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        st_shared_v4(off[e] + buf * C::kTileBytes + x * kStep * 128, &o[4 * e]);
+    } else {
+      tmem_st16(k_tile + buf * (D / 2) + x * 16, o);
+    }
+  };
+  auto done = [&](int buf) {
+    if constexpr (IS_V) {
+      fence_proxy_async_smem();
+    } else {
+      tmem_wait_st();
+      tc_fence_before();
+    }
+    mbar_arrive(&full[buf]);
+  };
+  if (self) {   // tile 0: the candidates' own keys or values, bf16 already
+    const __nv_bfloat16 *own = static_cast<const __nv_bfloat16 *>(IS_V ? p.v : p.k) +
+                               q_row * (IS_V ? p.v_rs : p.k_rs) + h * D + g * 32;
+#pragma unroll 1
+    for (int x = 0; x < kPer; ++x) {
+      const int i = row + (IS_V ? x * kStep : 0);
+      uint32_t o[16];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (i < nq)
+          w = load_row8(own + i * (IS_V ? p.v_rs : p.k_rs) + (IS_V ? 0 : x * 32) + e * 8, p.vec);
+        o[4 * e] = w.x;
+        o[4 * e + 1] = w.y;
+        o[4 * e + 2] = w.z;
+        o[4 * e + 3] = w.w;
+      }
+      put(0, x, o);
+    }
+    done(0);
+  }
+  int st = 0;
+#pragma unroll 1
+  for (int n = self; n < n_all; ++n) {
+    const int buf = n & 1;
+    cp_async_wait<C::kStages - 1>();
+    if (IS_V) __syncwarp();   // the row's parameters came through another lane of this warp
+    uint4 code[kPer];
+    uint32_t par[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      code[x] = *reinterpret_cast<const uint4 *>(codes + st * C::kCodeBytes + code_at[x]);
+      par[x] = *reinterpret_cast<const uint16_t *>(
+          scales + st * C::kScaleBytes + scale_at +
+          (IS_V ? x * kStep * 2 * G + g * 2 : G == 4 ? x * 2 : g * 2));
+    }
+    __syncwarp();   // the warp has read the stage
+    if (m_copy < n_tiles) copy(st);
+    cp_async_commit();
+    ++m_copy;
+    st = st == C::kStages - 1 ? 0 : st + 1;
+    if (n >= 2 &&
+        !wait_cta_warp(&empty[buf], ((n >> 1) - 1) & 1, &sm.abort, p.wait))
+      break;
+    if (!IS_V) tc_fence_after();
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      uint32_t zz, ss, o[16];
+      q4_group(par[x], zz, ss);
+      const uint32_t w[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t v4[4];
+        q4_decode_bf16(w[e], zz, ss, v4);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[4 * e + u] = v4[u];
+      }
+      put(buf, x, o);
+    }
+    done(buf);
+  }
+  cp_async_wait<0>();
+}
+
 template <int D, int NQ, bool WEIGHTS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ QcAttnParams p) {
@@ -285,9 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float half = WEIGHTS ? 1.0f : 0.5f;     // the tanh form works on x / 2
   constexpr uint32_t kQHalf = NQ * 128;         // bytes of one 64-column box of Q
 
-  constexpr int G = D / 32;                      // groups per row
-  constexpr int kPer = kTile * G / kDecThreads;  // groups per thread and tile
-  constexpr int kStep = kDecThreads / G;         // rows between a thread's groups
   const int self = it.split == 0 ? 1 : 0;        // tile 0 is the candidates' own
   const int n_all = n_tiles + self;
 
@@ -667,144 +818,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ===================== decoding =====================
-    // K (warps 12-19): thread = key and half of the row, since a warp writes its
-    // own 32 lanes of tensor memory.  V (warps 20-27): a warp takes 8 rows x 4
-    // groups (16 x 2 at D = 64), 512 bytes in one piece; eight lanes that store
-    // together hold 4 rows x 2 neighbouring groups, whose 16-byte chunks lie in
-    // eight different banks under the swizzle.
     regs_release_ctl<kRegsDec>();
-    const bool is_v = warp >= 20;
-    const int dw = is_v ? warp - 20 : warp - 12, dt = dw * 32 + lane, hx = dw >> 2;
-    const int row = !is_v    ? (dw & 3) * 32 + lane
-                    : G == 4 ? dw * 8 + ((lane >> 4) << 2) + ((lane >> 1) & 3)
-                             : dw * 16 + (lane >> 1);
-    // first group of the thread; its next is one group (K) or kStep rows (V) on
-    const int g = !is_v    ? hx * kPer
-                  : G == 4 ? ((lane >> 3) & 1) * 2 + (lane & 1)
-                           : lane & 1;
-    const int64_t at = (int64_t(h) * cv.rows + sq.row + int64_t(it.t0) * kTile + row) * G + g;
-    const uint8_t *src = reinterpret_cast<const uint8_t *>(is_v ? cv.v_codes : cv.k_codes);
-    const uint8_t *psrc = reinterpret_cast<const uint8_t *>(is_v ? cv.v_scales : cv.k_scales);
-    const uint8_t *const src0 = src, *const psrc0 = psrc;
-    src += at * 16;
-    // parameters travel 4 bytes and more at a time: K both groups of the thread
-    // (at D = 64 of the row), V a whole row through the lane of its first group
-    psrc += (at - (!is_v && G == 2 ? g : 0)) * 2;
-    int32_t left = sq.len - it.t0 * kTile - row;   // the sequence's rows from this one on
-    uint8_t *const codes = is_v ? sm.v_codes[0] : sm.k_codes[0];
-    uint8_t *const scales = is_v ? sm.v_scales[0] : sm.k_scales[0];
-    // where the thread's codes lie in a stage; for K a row's chunks are permuted
-    // so that 8 lanes (rows) that read together touch every bank once
-    uint32_t code_at[kPer];
-#pragma unroll
-    for (int x = 0; x < kPer; ++x)
-      code_at[x] = is_v ? (x * kDecThreads + dt) * 16
-                   : G == 4 ? row * 64 + (((g + x) ^ ((row >> 1) & 3)) << 4)
-                            : row * 32 + ((g ^ ((row >> 2) & 1)) << 4);
-    const uint32_t scale_at = is_v ? row * 2 * G : hx * (kTile * 4) + row * 4;
-    const uint32_t code_dst = smem_u32(codes), scale_dst = smem_u32(scales) + scale_at;
-    auto copy = [&](int st) {   // the next tile of the cache into stage st
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        const bool ok = (is_v ? x * kStep : 0) < left;
-        cp_async<16>(code_dst + st * C::kCodeBytes + code_at[x],
-                     ok ? src + (is_v ? x * kDecThreads : x) * 16 : src0, ok);
-        if (is_v && g == 0)
-          cp_async<2 * G>(scale_dst + st * C::kScaleBytes + x * kStep * 2 * G,
-                          ok ? psrc + x * kDecThreads * 2 : psrc0, ok);
-      }
-      if (!is_v)
-        cp_async<4>(scale_dst + st * C::kScaleBytes, 0 < left ? psrc : psrc0, 0 < left);
-      src += kTile * G * 16;
-      psrc += kTile * G * 2;
-      left -= kTile;
-    };
-    int m_copy = 0;
-#pragma unroll 1
-    for (; m_copy < C::kStages; ++m_copy) {
-      if (m_copy < n_tiles) copy(m_copy);
-      cp_async_commit();
-    }
-    uint64_t *const full = is_v ? sm.v_full : sm.k_full;
-    uint64_t *const empty = is_v ? sm.v_empty : sm.k_empty;
-    // V: where the group's chunks go in a tile.  K: its columns.
-    uint32_t off[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      off[e] = (g >> 1) * kBoxBytes + row * 128 + ((((g & 1) * 4 + e) ^ (row & 7)) << 4);
-    const uint32_t v_tile = smem_u32(sm.v[0]);
-    const uint32_t k_tile = tmem + (uint32_t((dw & 3) * 32) << 16) + C::kK + hx * (kPer * 16);
-    const __nv_bfloat16 *own =   // the candidates' own keys or values
-        is_v ? static_cast<const __nv_bfloat16 *>(p.v) + q_row * p.v_rs + h * D + g * 32
-             : static_cast<const __nv_bfloat16 *>(p.k) + q_row * p.k_rs + h * D + g * 32;
-    const int64_t rs = is_v ? p.v_rs : p.k_rs;
-    bool ok = true;
-    int st = 0;
-#pragma unroll 1
-    for (int n = 0; n < n_all; ++n) {
-      const int buf = n & 1, round = n >> 1;
-      if (n >= self) {
-        cp_async_wait<C::kStages - 1>();
-        __syncwarp();   // V: the row's parameters came through another lane of this warp
-      }
-      if (round > 0) ok = wait_cta_warp(&empty[buf], (round - 1) & 1, &sm.abort, p.wait);
-      if (!ok) break;
-      if (!is_v) tc_fence_after();
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        uint32_t o[16];
-        if (n < self) {
-          const int i = row + (is_v ? x * kStep : 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 w = i < nq ? load_row8(own + i * rs + (is_v ? 0 : x * 32) + e * 8, p.vec)
-                                   : make_uint4(0, 0, 0, 0);
-            o[4 * e] = w.x;
-            o[4 * e + 1] = w.y;
-            o[4 * e + 2] = w.z;
-            o[4 * e + 3] = w.w;
-          }
-        } else {
-          const uint4 code =
-              *reinterpret_cast<const uint4 *>(codes + st * C::kCodeBytes + code_at[x]);
-          const uint32_t par = *reinterpret_cast<const uint16_t *>(
-              scales + st * C::kScaleBytes + scale_at +
-              (is_v ? x * kStep * 2 * G + g * 2 : G == 4 ? x * 2 : g * 2));
-          uint32_t zz, ss;
-          q4_group(par, zz, ss);
-          const uint32_t w[4] = {code.x, code.y, code.z, code.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t v4[4];
-            q4_decode_bf16(w[e], zz, ss, v4);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) o[4 * e + u] = v4[u];
-          }
-        }
-        if (is_v) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            st_shared_v4(v_tile + buf * C::kTileBytes + off[e] + x * kStep * 128, &o[4 * e]);
-        } else {
-          tmem_st16(k_tile + buf * (D / 2) + x * 16, o);
-        }
-      }
-      if (is_v) {
-        fence_proxy_async_smem();
-      } else {
-        tmem_wait_st();
-        tc_fence_before();
-      }
-      mbar_arrive(&full[buf]);
-      if (n >= self) {
-        __syncwarp();   // the warp has read the stage
-        if (m_copy < n_tiles) copy(st);
-        cp_async_commit();
-        ++m_copy;
-        st = st == C::kStages - 1 ? 0 : st + 1;
-      }
-    }
-    cp_async_wait<0>();
+    if (warp < 20)
+      decode_tiles<D, NQ, false>(p, sm, it, sq, h, q_row, nq, tmem, warp - 12, lane);
+    else
+      decode_tiles<D, NQ, true>(p, sm, it, sq, h, q_row, nq, tmem, warp - 20, lane);
   }
   tc_fence_before();
   __syncthreads();
