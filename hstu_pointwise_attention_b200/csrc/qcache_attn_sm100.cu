@@ -14,17 +14,18 @@
 // and its weight sum over the candidates stays in a register.  It also keeps
 // the tile 128 keys high for a single candidate (NQ only pads the N side).
 //
-//   warps 12-19  keys: bring codes to shared memory (cp.async, ahead), decode
-//                them exactly to bf16 and write K to tensor memory (lane = key),
-//                from where the MMA takes it.
-//   warps 20-27  values the same way, V to shared memory in the 128-byte swizzle.
-//   warp 0       issues the MMAs, whichever has its operands: O^T of a tile
-//                first, else S^T up to two tiles ahead.
-//   warps 4-11   two warpgroups, taking tiles by turns: read S^T (thread = key),
-//                make P = SiLU(x), write P^T (bf16) to shared memory, add up the
-//                weights; at the end each warpgroup writes half of O.
+//   warp 0       issues the MMAs as their operands arrive.
 //   warps 1-3    a tile per warp, up to six tiles ahead: what each key brings
 //                along (KeyBias).
+//   then 8 or 16 elementwise warps: one or two warpgroups take a tile, the next
+//                ones the next: read S^T (thread = key, 64 candidates), make
+//                P = SiLU(x), write P^T (bf16) to shared memory, add up the
+//                weights; at the end each warpgroup writes 32 candidates of O.
+//   then 8 or 4 warps for keys: bring codes to shared memory (cp.async, ahead),
+//                decode them exactly to bf16 and write K to tensor memory
+//                (lane = key), from where the MMA takes it;
+//   and as many for values the same way, V to shared memory in the 128-byte
+//                swizzle.
 // The candidates' own pairs are one more tile, the first of the range that has
 // them: its keys are the candidates and only P's diagonal is kept.
 // Shared-memory traffic is what bounds the loop once the decoding keeps up (an
@@ -43,18 +44,22 @@ namespace qc_tc {
 
 
 constexpr int kTile = kQcKeyTile;
-constexpr int kThreads = 896;
-constexpr int kElemThreads = 256;     // warps 4-11
-constexpr int kDecThreads = 256;      // warps 12-19, and 20-27
-// Registers: 72 x 896 at launch; the control and decoding warpgroups give up
-// some for the two elementwise ones (56 + 2 x 96 + 4 x 64 = 7 x 72).
-constexpr int kRegsAll = 72, kRegsCtlW = 56, kRegsElem = 96, kRegsDec = 64;
-static_assert(kRegsCtlW + 2 * kRegsElem + 4 * kRegsDec <= 7 * kRegsAll, "register split");
+constexpr int kThreads = 896;         // 4 control, 24 elementwise and decoding warps
 constexpr int kTblT = 385;            // float-exponent table of the time bias, sub_bits <= 4
 constexpr uint32_t kBoxBytes = kTile * 128;   // 128 rows of 64 bf16
 
 template <int D, int NQ>
 struct Cfg {
+  // With up to 64 candidates the decoding is most of the work, with up to 128 the
+  // elementwise pass: 64 candidates of a tile per elementwise warpgroup, two tiles
+  // in work, and the other warps decode, half of them K, half V.
+  static constexpr int kHalves = NQ / 64;                   // warpgroups per tile
+  static constexpr int kElemWarps = 8 * kHalves;
+  static constexpr int kDecWarps = (24 - kElemWarps) / 2;   // per operand: 8 or 4
+  static constexpr int kDecThreads = 32 * kDecWarps;
+  static constexpr int kG = D / 32;                         // groups per row
+  static constexpr int kPer = kTile * kG / kDecThreads;     // groups per thread and tile
+  static constexpr int kParBytes = kPer == 1 ? 4 : 2 * kPer;   // K: parameters copied per thread
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kV = 2;
   static constexpr int kPBytes = NQ / 64 * int(kBoxBytes);
@@ -63,7 +68,7 @@ struct Cfg {
   // full HBM rate; with many a tile's time covers the latency.
   static constexpr int kStages = D == 128 ? (NQ == 128 ? 1 : 3) : 4;
   static constexpr int kCodeBytes = kTile * D / 2;       // of one tile of K (or V)
-  static constexpr int kScaleBytes = kTile * 8;          // 8 bytes per row (4 used at D = 64)
+  static constexpr int kScaleBytes = kTile * 8;          // 8 bytes per row (V at D = 64: 4 of them)
   // Tensor memory columns: kS slots of S^T, O^T, two K tiles.
   static constexpr int kS = NQ == 128 ? 2 : 3;
   static constexpr uint32_t kO = kS * NQ, kK = kO + NQ;
@@ -263,7 +268,7 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W /
 
 // The decoding warps of K (IS_V false) or V: tiles of codes from the cache into
 // stages (cp.async), from there to bf16, K to tensor memory, V to shared memory.
-//   K: thread = key and half of the row, since a warp writes its own 32 lanes of
+//   K: thread = key and half of the row (or all of it), since a warp writes its own 32 lanes of
 //   tensor memory; a row's chunks are permuted in the stage so that 8 lanes that
 //   read together touch every bank once.
 //   V: a warp takes 8 rows x 4 groups (16 x 2 at D = 64), 512 bytes in one piece;
@@ -275,8 +280,7 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
                                              int64_t q_row, int nq, uint32_t tmem, int dw,
                                              int lane) {
   using C = Cfg<D, NQ>;
-  constexpr int G = D / 32;                      // groups per row
-  constexpr int kPer = kTile * G / kDecThreads;  // groups per thread and tile
+  constexpr int G = C::kG, kPer = C::kPer, kDecThreads = C::kDecThreads;
   constexpr int kStep = kDecThreads / G;         // V: rows between a thread's groups
   const QCacheView &cv = p.cache;
   const int dt = dw * 32 + lane, hx = dw >> 2;
@@ -289,9 +293,9 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
   const uint8_t *const src0 = reinterpret_cast<const uint8_t *>(IS_V ? cv.v_codes : cv.k_codes);
   const uint8_t *const psrc0 = reinterpret_cast<const uint8_t *>(IS_V ? cv.v_scales : cv.k_scales);
   const uint8_t *src = src0 + at * 16;
-  // parameters travel 4 bytes and more at a time: K both groups of the thread
-  // (at D = 64 of the row), V a whole row through the lane of its first group
-  const uint8_t *psrc = psrc0 + (at - (!IS_V && G == 2 ? g : 0)) * 2;
+  // parameters travel 4 bytes and more at a time: K the thread's groups (a single
+  // one with its neighbour), V a whole row through the lane of its first group
+  const uint8_t *psrc = psrc0 + (at - (!IS_V && kPer == 1 ? (g & 1) : 0)) * 2;
   int32_t left = sq.len - it.t0 * kTile - row;   // the sequence's rows from this one on
   uint8_t *const codes = IS_V ? sm.v_codes[0] : sm.k_codes[0];
   uint8_t *const scales = IS_V ? sm.v_scales[0] : sm.k_scales[0];
@@ -300,8 +304,8 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
   for (int x = 0; x < kPer; ++x)
     code_at[x] = IS_V     ? (x * kDecThreads + dt) * 16
                  : G == 4 ? row * 64 + (((g + x) ^ ((row >> 1) & 3)) << 4)
-                          : row * 32 + ((g ^ ((row >> 2) & 1)) << 4);
-  const uint32_t scale_at = IS_V ? row * 2 * G : hx * (kTile * 4) + row * 4;
+                          : row * 32 + (((g + x) ^ ((row >> 2) & 1)) << 4);
+  const uint32_t scale_at = IS_V ? row * 2 * G : (hx * kTile + row) * C::kParBytes;
   const uint32_t code_dst = smem_u32(codes), scale_dst = smem_u32(scales) + scale_at;
   auto copy = [&](int st) {   // the next tile of the cache into stage st
 #pragma unroll
@@ -313,7 +317,8 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
         cp_async<2 * G>(scale_dst + st * C::kScaleBytes + x * kStep * 2 * G,
                         ok ? psrc + x * kDecThreads * 2 : psrc0, ok);
     }
-    if (!IS_V) cp_async<4>(scale_dst + st * C::kScaleBytes, 0 < left ? psrc : psrc0, 0 < left);
+    if (!IS_V)
+      cp_async<C::kParBytes>(scale_dst + st * C::kScaleBytes, 0 < left ? psrc : psrc0, 0 < left);
     src += kTile * G * 16;
     psrc += kTile * G * 2;
     left -= kTile;
@@ -385,7 +390,7 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
       code[x] = *reinterpret_cast<const uint4 *>(codes + st * C::kCodeBytes + code_at[x]);
       par[x] = *reinterpret_cast<const uint16_t *>(
           scales + st * C::kScaleBytes + scale_at +
-          (IS_V ? x * kStep * 2 * G + g * 2 : G == 4 ? x * 2 : g * 2));
+          (IS_V ? x * kStep * 2 * G + g * 2 : kPer == 1 ? (g & 1) * 2 : x * 2));
     }
     __syncwarp();   // the warp has read the stage
     if (m_copy < n_tiles) copy(st);
@@ -443,21 +448,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_all = n_tiles + self;
 
   if (tid == 64) {
-    mbar_init(&sm.q_full, kElemThreads);
+    mbar_init(&sm.q_full, 32 * C::kElemWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.k_full[i], kDecThreads);
+      mbar_init(&sm.k_full[i], C::kDecThreads);
       mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], kDecThreads);
+      mbar_init(&sm.v_full[i], C::kDecThreads);
       mbar_init(&sm.v_empty[i], 1);
     }
     for (int i = 0; i < 3; ++i) mbar_init(&sm.s_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.p_full[i], kElemThreads / 2);
+      mbar_init(&sm.p_full[i], 128 * C::kHalves);
       mbar_init(&sm.p_empty[i], 1);
     }
     for (int i = 0; i < kBias; ++i) {
       mbar_init(&sm.bias_full[i], 32);
-      mbar_init(&sm.bias_empty[i], kElemThreads / 64);
+      mbar_init(&sm.bias_empty[i], 4 * C::kHalves);
     }
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.drain, 1);
@@ -474,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem_base;
 
   if (warp < 4) {
-    regs_release_ctl<kRegsCtlW>();
     if (warp == 0) {
       // ===================== MMA issuer =====================
       if (elect_one()) {
@@ -638,17 +642,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sm.bias_full[n % kBias]);
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < 4 + C::kElemWarps) {
     // ===================== elementwise =====================
-    regs_grow_ew<kRegsElem>();
-    const int wg = (warp - 4) >> 2, quad = warp & 3;
+    // warpgroup w takes tiles of parity `par` and candidates [64 hf, 64 hf + 64)
+    const int w = (warp - 4) >> 2, par = w / C::kHalves, hf = w % C::kHalves, quad = warp & 3;
     const int key = quad * 32 + lane;
     const uint32_t lanes = tmem + (uint32_t(quad * 32) << 16);
     {
       // the queries, K-major in the 128-byte swizzle; rows behind the last are zero
       const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + q_row * p.q_rs + h * D;
 #pragma unroll 4
-      for (int x = tid - 128; x < NQ * (D / 8); x += kElemThreads) {
+      for (int x = tid - 128; x < NQ * (D / 8); x += 32 * C::kElemWarps) {
         const int r = x / (D / 8), u = x % (D / 8);
         uint4 val = make_uint4(0, 0, 0, 0);
         if (r < nq) val = load_row8(q + r * p.q_rs + u * 8, p.vec);
@@ -660,36 +664,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const float a = half * p.alpha;
     bool ok = true;
-    int slot = wg, round = 0;   // n % kS, n / kS
+    int slot = par, round = 0;   // n % kS, n / kS
 #pragma unroll 1
-    for (int n = wg; n < n_all; n += 2, slot += 2, slot -= slot >= C::kS ? (++round, C::kS) : 0) {
+    for (int n = par; n < n_all; n += 2, slot += 2, slot -= slot >= C::kS ? (++round, C::kS) : 0) {
       const uint32_t s_col = lanes + slot * NQ;
-      uint8_t *pt = sm.p[wg] + key * 128;
+      uint8_t *pt = sm.p[par] + hf * kBoxBytes + key * 128;
       if (n < self) {
         // the candidates' own pairs: bias of distance 0, P's diagonal
         ok = wait_cta_warp(&sm.s_full[0], 0, &sm.abort, p.wait);
         if (!ok) break;
         tc_fence_after();
         uint32_t bits = 0;
-        if (quad * 32 < nq) {
-          uint32_t r[32];
-          tmem_ld32(s_col + quad * 32, r);
-          tmem_wait_ld(r);
+        // (candidates of this warpgroup's half: its diagonal lies in quads 2 hf, 2 hf + 1)
+        if (quad >> 1 == hf && quad * 32 < nq) {
           uint32_t sv = 0;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sv = lane == e ? r[e] : sv;
+          for (int e0 = 0; e0 < 32; e0 += 16) {
+            uint32_t r[16];
+            tmem_ld16(s_col + quad * 32 + e0, r);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sv = lane == e0 + e ? r[e] : sv;
+          }
           const float x = fmaf(p.alpha, __uint_as_float(sv), qc_bias(rp[0]) + qc_bias(rt[0]));
           const float ps = x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
           bits = key < nq ? pack_bf16x2(ps, 0.f) : 0u;
         }
         bits = key & 1 ? bits << 16 : bits;
+        const int at = key - hf * 64;   // its column in this half (other quads: bits are 0)
 #pragma unroll
-        for (int u = 0; u < NQ / 8; ++u) {
-          uint32_t w[4];
+        for (int u = 0; u < 8; ++u) {
+          uint32_t v4[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = (key >> 1) == u * 4 + e ? bits : 0u;
-          *reinterpret_cast<uint4 *>(pt + (u >> 3) * kBoxBytes + (((u & 7) ^ (key & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 4; ++e) v4[e] = (at >> 1) == u * 4 + e ? bits : 0u;
+          *reinterpret_cast<uint4 *>(pt + ((u ^ (key & 7)) << 4)) =
+              make_uint4(v4[0], v4[1], v4[2], v4[3]);
         }
         tc_fence_before();
         fence_proxy_async_smem();
@@ -717,66 +726,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.bias_empty[bs]);
       ok = wait_cta_warp(&sm.s_full[slot], round & 1, &sm.abort, p.wait);
       if (ok && n >= 2)   // the product of the tile two back has read P
-        ok = wait_cta_warp(&sm.p_empty[wg], ((n >> 1) - 1) & 1, &sm.abort, p.wait);
+        ok = wait_cta_warp(&sm.p_empty[par], ((n >> 1) - 1) & 1, &sm.abort, p.wait);
       if (!ok) break;
       tc_fence_after();
-#define HSTU_QC_CHUNK(M_, A_, W_)                                                                \
-  chunk<D, NQ, WEIGHTS, M_, A_, W_>(r, pk, sm, c0, a, c, c2, t, tk, rt, half, p.sub_bits, p.nb_t, \
+#define HSTU_QC_CHUNK(M_, A_)                                                                   \
+  chunk<D, NQ, WEIGHTS, M_, A_, 16>(r, pk, sm, c0, a, c, c2, t, tk, rt, half, p.sub_bits, p.nb_t, \
                                     nq - c0, wsum)
-      if (nq <= 16 && mode == kTimeOne) {   // few candidates: half a chunk
-        constexpr int c0 = 0;
+#pragma unroll 1
+      for (int c0 = hf * 64; c0 < min(hf * 64 + 64, nq); c0 += 16) {
         uint32_t r[16], pk[8];
-        tmem_ld16(s_col, r);
+        tmem_ld16(s_col + c0, r);
         tmem_wait_ld(r);
-        HSTU_QC_CHUNK(kTimeOne, !WEIGHTS, 16);
+        if (mode == kTimeOne) {
+          if (!WEIGHTS || nq - c0 >= 16)
+            HSTU_QC_CHUNK(kTimeOne, true);
+          else
+            HSTU_QC_CHUNK(kTimeOne, false);
+        } else if (mode == kTimeTwo) {
+          HSTU_QC_CHUNK(kTimeTwo, !WEIGHTS);
+        } else if (mode == kTimeFloat) {
+          HSTU_QC_CHUNK(kTimeFloat, !WEIGHTS);
+        } else {
+          HSTU_QC_CHUNK(kTimeInt, !WEIGHTS);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) pk[e] = valid ? pk[e] : 0;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<uint4 *>(pt + ((e ^ (key & 7)) << 4)) =
+          *reinterpret_cast<uint4 *>(pt + (((((c0 & 63) >> 3) + e) ^ (key & 7)) << 4)) =
               make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
-      } else {
-#pragma unroll 1
-        for (int c0 = 0; c0 < nq; c0 += 32) {
-          uint32_t r[32], pk[16];
-          tmem_ld32(s_col + c0, r);
-          tmem_wait_ld(r);
-          if (mode == kTimeOne) {
-            if (!WEIGHTS || nq - c0 >= 32)
-              HSTU_QC_CHUNK(kTimeOne, true, 32);
-            else
-              HSTU_QC_CHUNK(kTimeOne, false, 32);
-          } else if (mode == kTimeTwo) {
-            HSTU_QC_CHUNK(kTimeTwo, !WEIGHTS, 32);
-          } else if (mode == kTimeFloat) {
-            HSTU_QC_CHUNK(kTimeFloat, !WEIGHTS, 32);
-          } else {
-            HSTU_QC_CHUNK(kTimeInt, !WEIGHTS, 32);
-          }
-          if (!valid) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = 0;
-          }
-          uint8_t *box = pt + (c0 >> 6) * kBoxBytes;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4 *>(box + (((((c0 & 63) >> 3) + e) ^ (key & 7)) << 4)) =
-                make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
-        }
       }
 #undef HSTU_QC_CHUNK
       tc_fence_before();          // S^T has been read
       fence_proxy_async_smem();   // P^T is written
-      mbar_arrive(&sm.p_full[wg]);
+      mbar_arrive(&sm.p_full[par]);
       if constexpr (WEIGHTS) {
-        if (j < sq.len)
-          p.wpart[sq.wp0 + (int64_t(it.qtile) * H + h) * sq.len + j] = valid ? wsum : 0.f;
+        if (j < sq.len && hf * 64 < nq)
+          p.wpart[sq.wp0 + (int64_t(it.qtile * C::kHalves + hf) * H + h) * sq.len + j] =
+              valid ? wsum : 0.f;
       }
     }
     // ---- O^T (lane = feature) through the P tiles' memory to rows of out ----
-    // each warpgroup its half of the candidates
-    constexpr int kCols = NQ / 2;
-    const int c_first = wg * kCols, c_end = min(c_first + kCols, nq);
+    const int c_first = w * 32, c_end = min(c_first + 32, nq);
     if (ok) ok = wait_cta_warp(&sm.o_full, 0, &sm.abort, p.wait);
     tc_fence_after();
     float *stage = reinterpret_cast<float *>(&sm.p[0][0]);   // [NQ][D]
@@ -790,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 16; ++e) stage[(c0 + e) * D + key] = __uint_as_float(r[e]);
       }
     }
-    named_bar_sync(3 + wg, kElemThreads / 2);
+    named_bar_sync(3 + w, 128);
     if (ok) {
       constexpr int kRowLanes = D / 4, kRows = 128 / kRowLanes;   // 4 features per lane
       const int wt = (tid - 128) & 127, e = (wt % kRowLanes) * 4;
@@ -818,11 +809,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ===================== decoding =====================
-    regs_release_ctl<kRegsDec>();
-    if (warp < 20)
-      decode_tiles<D, NQ, false>(p, sm, it, sq, h, q_row, nq, tmem, warp - 12, lane);
+    const int dw = warp - 4 - C::kElemWarps;
+    if (dw < C::kDecWarps)
+      decode_tiles<D, NQ, false>(p, sm, it, sq, h, q_row, nq, tmem, dw, lane);
     else
-      decode_tiles<D, NQ, true>(p, sm, it, sq, h, q_row, nq, tmem, warp - 20, lane);
+      decode_tiles<D, NQ, true>(p, sm, it, sq, h, q_row, nq, tmem, dw - C::kDecWarps, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -837,15 +828,7 @@ cudaError_t launch_t(const QcAttnParams &p, cudaStream_t st) {
   constexpr size_t smem = sizeof(Smem<D, NQ>) + 1024;
   static_assert(smem <= 232448, "shared memory");
   static PerDeviceOnce attr;
-  cudaError_t e = attr.run([&](int) {
-    // the register split needs exactly what the kernel was launched with
-    cudaFuncAttributes fa;
-    const cudaError_t err = cudaFuncGetAttributes(&fa, attn_kernel<D, NQ, WEIGHTS>);
-    if (err != cudaSuccess) return err;
-    if (fa.numRegs != kRegsAll) return cudaErrorInvalidKernelImage;
-    return cudaFuncSetAttribute(attn_kernel<D, NQ, WEIGHTS>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  });
+  cudaError_t e = set_smem_once(attr, attn_kernel<D, NQ, WEIGHTS>, smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(p.items) * unsigned(p.cache.heads);
   attn_kernel<D, NQ, WEIGHTS><<<grid, kThreads, smem, st>>>(p);
