@@ -19,39 +19,7 @@ namespace qc {
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]);
-
-template <>
-__device__ __forceinline__ void load8<float>(const float *p, bool vec, float (&x)[8]) {
-  if (vec) {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = p[i];
-  }
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, bool vec,
-                                                      float (&x)[8]) {
-  if (vec) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(p[i]);
-  }
-}
-
-// rne(x / s) of the exact quotient, given inv ~ 1 / s: the product rounds to
+// rne(x / s) of the exact quotient, given inv = 1 / s: the product rounds to
 // within one of it, and the remainder x - y s (exact in one fma) settles it.
 __device__ __forceinline__ float rne_div(float x, float s, float inv) {
   float y = rintf(x * inv);
@@ -61,77 +29,195 @@ __device__ __forceinline__ float rne_div(float x, float s, float inv) {
   return y;
 }
 
-// One group: this lane's 8 values, the other 24 in the lanes of its quad.
-__device__ __forceinline__ void quantise8(float (&x)[8], uint32_t &word, uint32_t &param) {
-  const uint32_t quad = 0xFu << (threadIdx.x & 28);   // other quads may have left the loop
-  float lo = 0.f, hi = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -0x1p126f), 0x1p126f);
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-  }
-#pragma unroll
-  for (int m = 1; m < 4; m <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(quad, lo, m));
-    hi = fmaxf(hi, __shfl_xor_sync(quad, hi, m));
-  }
+// Scale and zero point of a group from its extremes, lo <= 0 <= hi.
+__device__ __forceinline__ void group_scale(float lo, float hi, float &s, float &inv, int &z) {
   // span = hi - lo exactly: rounded difference r plus its rounding error
   const float r = hi - lo, bb = r - hi, err = (hi - (r - bb)) + (-lo - bb);
   // the scale's 4 significant bits: truncate r / 15, one step up unless
   // 15 s (exact) already covers the span
-  float s = __uint_as_float(__float_as_uint(r / 15.0f) & 0xFFF00000u);
+  s = __uint_as_float(__float_as_uint(r / 15.0f) & 0xFFF00000u);
   const float p = 15.0f * s;
   if (p < r || (p == r && err > 0.f)) s = __uint_as_float(__float_as_uint(s) + 0x00100000u);
   s = fmaxf(s, 0x1p-126f);
-  word = 0;
-  param = 0;
-  if (hi > lo) {
-    const float inv = 1.0f / s;
-    const float z = rne_div(-lo, s, inv);
-    param = (__float_as_uint(s) >> 16) | uint32_t(z);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = fminf(fmaxf(rne_div(x[i], s, inv) + z, 0.f), 15.f);
-      word |= uint32_t(q) << (4 * (i >> 1) + 16 * (i & 1));
-    }
-  }
+  inv = 1.0f / s;
+  z = int(rne_div(-lo, s, inv));
 }
 
+__device__ __forceinline__ float held(float x) {   // NaN as 0, magnitudes to 2^126
+  return x != x ? 0.f : fminf(fmaxf(x, -0x1p126f), 0x1p126f);
+}
+
+// Eight values as they come from memory, and their quantisation together with
+// the 24 others of their group in the quad's other lanes.
 template <typename T>
+struct Eight;
+
+template <>
+struct Eight<float> {
+  float x[8];
+  __device__ __forceinline__ void load(const float *p, bool vec) {
+    if (vec) {
+      const float4 a = *reinterpret_cast<const float4 *>(p);
+      const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ void quantise(uint32_t quad, uint32_t &word, uint32_t &param) {
+    float lo = 0.f, hi = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = held(x[i]);
+      lo = fminf(lo, x[i]);
+      hi = fmaxf(hi, x[i]);
+    }
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(quad, lo, m));
+      hi = fmaxf(hi, __shfl_xor_sync(quad, hi, m));
+    }
+    word = param = 0;
+    if (hi > lo) {
+      float s, inv;
+      int z;
+      group_scale(lo, hi, s, inv, z);
+      param = (__float_as_uint(s) >> 16) | uint32_t(z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        word |= uint32_t(min(int(rne_div(x[i], s, inv)) + z, 15)) << (4 * (i >> 1) + 16 * (i & 1));
+    }
+  }
+};
+
+template <>
+struct Eight<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool vec) {
+    if (vec) {
+      const uint4 a = *reinterpret_cast<const uint4 *>(p);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = reinterpret_cast<const uint16_t *>(p)[2 * i] |
+               uint32_t(reinterpret_cast<const uint16_t *>(p)[2 * i + 1]) << 16;
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+  }
+  __device__ __forceinline__ void quantise(uint32_t quad, uint32_t &word, uint32_t &param) {
+    // extremes two at a time (NaN and infinities show in them), then over the quad
+    auto b2 = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); };
+    const __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(b2(w[0]), b2(w[1])),
+                                           __hmin2_nan(b2(w[2]), b2(w[3])));
+    const __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(b2(w[0]), b2(w[1])),
+                                           __hmax2_nan(b2(w[2]), b2(w[3])));
+    float lo = __bfloat162float(__hmin_nan(lo2.x, lo2.y));
+    float hi = __bfloat162float(__hmax_nan(hi2.x, hi2.y));
+    if (!(lo >= -0x1p126f && hi <= 0x1p126f)) {   // rare: bring the values into range
+      lo = hi = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = held(__uint_as_float(w[i] << 16));
+        const float b = held(__uint_as_float(w[i] & 0xFFFF0000u));
+        w[i] = (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
+        lo = fminf(lo, fminf(a, b));
+        hi = fmaxf(hi, fmaxf(a, b));
+      }
+    }
+    lo = fminf(lo, 0.f);
+    hi = fmaxf(hi, 0.f);
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(quad, lo, m));
+      hi = fmaxf(hi, __shfl_xor_sync(quad, hi, m));
+    }
+    word = param = 0;
+    if (hi > lo) {
+      float s, inv;
+      int z;
+      group_scale(lo, hi, s, inv, z);
+      param = (__float_as_uint(s) >> 16) | uint32_t(z);
+      // x has 8 significant bits and s 4, so x / s is a tie between two integers
+      // or at least 2^-13 of its size away from one: the quotient to float32
+      // (product and one correction) rounds to the integer that the exact one
+      // rounds to.  Adding 1.5 2^23 rounds to the nearest even integer.
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = at(i), q = x * inv, y = fmaf(fmaf(-q, s, x), inv, q) + 12582912.0f;
+        word |= uint32_t(min(int(__float_as_uint(y)) + (z - 0x4B400000), 15))
+                << (4 * (i >> 1) + 16 * (i & 1));
+      }
+    }
+  }
+};
+
+// A block takes tpb tokens side by side (or one in steps of the block), a thread
+// TPT of them one behind the other: with many tokens four, so that four loads
+// are in flight per thread; with few one, to have more blocks.
+struct RowPos {
+  int64_t tok, row, pos;
+};
+__device__ __forceinline__ RowPos row_pos(const QcRowsParams &p, int64_t tok) {
+  const int s = qc_find(p.seqs, p.n_seqs, tok, [](const QcRows &r) { return r.tok; });
+  const int64_t i = tok - p.seqs[s].tok;
+  return {tok, p.seqs[s].row + i, p.seqs[s].pos + i};
+}
+
+template <typename T, int TPT>
 __global__ void __launch_bounds__(kRowThreads)
     append_kernel(const __grid_constant__ QcRowsParams p) {
   const QCacheView &c = p.cache;
   const int kw = c.heads * (c.d_qk >> 3), units = kw + c.heads * (c.d_v >> 3);
-  // a block takes kRowThreads / units tokens side by side (units is a multiple
-  // of 4: a group's quad never straddles two tokens), or one token in steps
+  // units is a multiple of 4: a group's quad never straddles two tokens
   const int tpb = units < kRowThreads ? kRowThreads / units : 1;
   const int tl = tpb > 1 ? int(threadIdx.x) / units : 0;
   if (tl >= tpb) return;
   const int u0 = int(threadIdx.x) - tl * units;
-  const int64_t tok = p.tok0 + int64_t(blockIdx.x) * tpb + tl;
-  if (tok >= p.tok_end) return;
-  const int sq = qc_find(p.seqs, p.n_seqs, tok, [](const QcRows &s) { return s.tok; });
-  const QcRows seq = p.seqs[sq];
-  const int64_t i = tok - seq.tok, row = seq.row + i;
+  const uint32_t quad = 0xFu << (threadIdx.x & 28);   // other quads may have left the loops
+  const int64_t tok0 = p.tok0 + int64_t(blockIdx.x) * (tpb * TPT) + tl;
+  RowPos at[TPT];
+  int n = 0;   // this thread's tokens
+#pragma unroll
+  for (int k = 0; k < TPT; ++k)
+    if (tok0 + k * tpb < p.tok_end) {
+      at[k] = row_pos(p, tok0 + k * tpb);
+      n = k + 1;
+    }
   for (int u = u0; u < units; u += (tpb > 1 ? units : kRowThreads)) {
     const bool is_v = u >= kw;
     const int d = is_v ? c.d_v : c.d_qk, e = (is_v ? u - kw : u) * 8;   // element of the row
     const int h = e / d, ed = e - h * d;
-    const T *src = static_cast<const T *>(is_v ? p.v : p.k) + tok * (is_v ? p.v_rs : p.k_rs) + e;
-    float x[8];
-    load8<T>(src, p.vec, x);
-    uint32_t word, param;
-    quantise8(x, word, param);
-    const int64_t at = int64_t(h) * c.rows + row;
-    (is_v ? c.v_codes : c.k_codes)[at * (d >> 3) + (ed >> 3)] = word;
-    if ((ed & 31) == 0)
-      (is_v ? c.v_scales : c.k_scales)[at * (d >> 5) + (ed >> 5)] = uint16_t(param);
+    const T *src = static_cast<const T *>(is_v ? p.v : p.k) + e;
+    const int64_t rs = is_v ? p.v_rs : p.k_rs;
+    uint32_t *codes = (is_v ? c.v_codes : c.k_codes) + int64_t(h) * c.rows * (d >> 3) + (ed >> 3);
+    uint16_t *scales = (is_v ? c.v_scales : c.k_scales) + int64_t(h) * c.rows * (d >> 5) + (ed >> 5);
+    Eight<T> x[TPT];
+#pragma unroll
+    for (int k = 0; k < TPT; ++k)
+      if (k < n) x[k].load(src + at[k].tok * rs, p.vec);
+#pragma unroll
+    for (int k = 0; k < TPT; ++k) {
+      if (k < n) {
+        uint32_t word, param;
+        x[k].quantise(quad, word, param);
+        codes[at[k].row * (d >> 3)] = word;
+        if ((ed & 31) == 0) scales[at[k].row * (d >> 5)] = uint16_t(param);
+      }
+    }
   }
   if (u0 == 0) {
-    c.times[row] = p.ts[tok];
-    c.pos[row] = int32_t(seq.pos + i);
-    if (c.weight) c.weight[row] = 0.f;
+#pragma unroll
+    for (int k = 0; k < TPT; ++k)
+      if (k < n) {
+        c.times[at[k].row] = p.ts[at[k].tok];
+        c.pos[at[k].row] = int32_t(at[k].pos);
+        if (c.weight) c.weight[at[k].row] = 0.f;
+      }
   }
 }
 
@@ -139,6 +225,35 @@ __global__ void __launch_bounds__(kRowThreads)
 // Read: the values that rows stand for, 8 per lane.
 // ---------------------------------------------------------------------------
 template <typename T>
+__device__ __forceinline__ void store_values(T *dst, uint32_t w, uint32_t param, bool vec) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t zz, ss, o[4];
+    q4_group(param, zz, ss);
+    q4_decode_bf16(w, zz, ss, o);
+    if (vec) {
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        reinterpret_cast<uint16_t *>(dst)[i] = uint16_t(o[i >> 1] >> (16 * (i & 1)));
+    }
+  } else {
+    const float s = q4_scale(param);
+    const int z = int(param & 15u);
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = s * float(q4_code(w, i) - z);
+    if (vec) {
+      reinterpret_cast<float4 *>(dst)[0] = make_float4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<float4 *>(dst)[1] = make_float4(o[4], o[5], o[6], o[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dst[i] = o[i];
+    }
+  }
+}
+
+template <typename T, int TPT>
 __global__ void __launch_bounds__(kRowThreads)
     read_kernel(const __grid_constant__ QcRowsParams p) {
   const QCacheView &c = p.cache;
@@ -147,44 +262,35 @@ __global__ void __launch_bounds__(kRowThreads)
   const int tl = tpb > 1 ? int(threadIdx.x) / units : 0;
   if (tl >= tpb) return;
   const int u0 = int(threadIdx.x) - tl * units;
-  const int64_t tok = p.tok0 + int64_t(blockIdx.x) * tpb + tl;
-  if (tok >= p.tok_end) return;
-  const int sq = qc_find(p.seqs, p.n_seqs, tok, [](const QcRows &s) { return s.tok; });
-  const int64_t row = p.seqs[sq].row + (tok - p.seqs[sq].tok);
+  const int64_t tok0 = p.tok0 + int64_t(blockIdx.x) * (tpb * TPT) + tl;
+  RowPos at[TPT];
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < TPT; ++k)
+    if (tok0 + k * tpb < p.tok_end) {
+      at[k] = row_pos(p, tok0 + k * tpb);
+      n = k + 1;
+    }
   for (int u = u0; u < units; u += (tpb > 1 ? units : kRowThreads)) {
     const bool is_v = u >= kw;
     const int d = is_v ? c.d_v : c.d_qk, e = (is_v ? u - kw : u) * 8;
     const int h = e / d, ed = e - h * d;
-    const int64_t at = int64_t(h) * c.rows + row;
-    const uint32_t w = (is_v ? c.v_codes : c.k_codes)[at * (d >> 3) + (ed >> 3)];
-    const uint32_t param = (is_v ? c.v_scales : c.k_scales)[at * (d >> 5) + (ed >> 5)];
-    T *dst = static_cast<T *>(const_cast<void *>(is_v ? p.v : p.k)) +
-             tok * (is_v ? p.v_rs : p.k_rs) + e;
-    if constexpr (sizeof(T) == 2) {
-      uint32_t zz, ss, o[4];
-      q4_group(param, zz, ss);
-      q4_decode_bf16(w, zz, ss, o);
-      if (p.vec) {
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
+    const uint32_t *codes =
+        (is_v ? c.v_codes : c.k_codes) + int64_t(h) * c.rows * (d >> 3) + (ed >> 3);
+    const uint16_t *scales =
+        (is_v ? c.v_scales : c.k_scales) + int64_t(h) * c.rows * (d >> 5) + (ed >> 5);
+    T *dst = static_cast<T *>(const_cast<void *>(is_v ? p.v : p.k)) + e;
+    const int64_t rs = is_v ? p.v_rs : p.k_rs;
+    uint32_t w[TPT], par[TPT];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          reinterpret_cast<uint16_t *>(dst)[i] = uint16_t(o[i >> 1] >> (16 * (i & 1)));
+    for (int k = 0; k < TPT; ++k)
+      if (k < n) {
+        w[k] = codes[at[k].row * (d >> 3)];
+        par[k] = scales[at[k].row * (d >> 5)];
       }
-    } else {
-      const float s = q4_scale(param);
-      const int z = int(param & 15u);
-      float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = s * float(q4_code(w, i) - z);
-      if (p.vec) {
-        reinterpret_cast<float4 *>(dst)[0] = make_float4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<float4 *>(dst)[1] = make_float4(o[4], o[5], o[6], o[7]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = o[i];
-      }
-    }
+    for (int k = 0; k < TPT; ++k)
+      if (k < n) store_values<T>(dst + at[k].tok * rs, w[k], par[k], p.vec);
   }
 }
 
@@ -194,10 +300,19 @@ cudaError_t launch_rows_t(const QcRowsParams &p, cudaStream_t st) {
   const int tpb = units < kRowThreads ? kRowThreads / units : 1;
   const int64_t blocks = (p.tok_end - p.tok0 + tpb - 1) / tpb;
   if (blocks <= 0) return cudaSuccess;
-  if constexpr (APPEND)
-    append_kernel<T><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
-  else
-    read_kernel<T><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
+  // four tokens per thread once that still fills the SMs (8 blocks of 256 each)
+  if (blocks >= 4 * 8 * 148) {
+    const unsigned n = unsigned((blocks + 3) / 4);
+    if constexpr (APPEND)
+      append_kernel<T, 4><<<n, kRowThreads, 0, st>>>(p);
+    else
+      read_kernel<T, 4><<<n, kRowThreads, 0, st>>>(p);
+  } else {
+    if constexpr (APPEND)
+      append_kernel<T, 1><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
+    else
+      read_kernel<T, 1><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
+  }
   count_launch();
   return cudaGetLastError();
 }

@@ -181,7 +181,9 @@ def _row_stride(t: torch.Tensor, H: int, d: int, name: str) -> int:
     if t.shape[0] == 0 and tuple(t.shape[1:]) in ((H, d), (H * d,)):
         return H * d        # no rows: strides carry no meaning
     if t.dim() == 3:
-        if t.shape[1] != H or t.shape[2] != d or t.stride(2) != 1 or t.stride(1) != d:
+        if t.shape[1:] == (H, d) and t.is_contiguous():
+            return H * d
+        if t.shape[1:] != (H, d) or t.stride()[1:] != (d, 1):
             raise ValueError(f"{name}: expected [T, {H}, {d}] with contiguous heads")
     elif t.dim() == 2:
         if t.shape[1] != H * d or t.stride(1) != 1:
@@ -475,7 +477,7 @@ class QuantCache:
                                                                      v_scales)
         self.times, self.pos, self.weight = times, pos, weight
         self.rows, self.num_heads, self.d_qk, self.d_v = rows, H, 2 * half_k, 2 * half_v
-        self.device = k_codes.device
+        self.device, self._index = k_codes.device, k_codes.get_device()
         self._c = _QCacheStruct(rows, H, self.d_qk, self.d_v, 0, _ptr(k_codes), _ptr(k_scales),
                                 _ptr(v_codes), _ptr(v_scales), _ptr(times), _ptr(pos),
                                 _ptr(weight))
@@ -490,41 +492,66 @@ class QuantCache:
                    z((rows,), torch.int32), z((rows,), torch.float32))
 
 
+def _cuda_index(t, *others) -> int:
+    """Index of the CUDA device that t and the others (None aside) live on."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"expected CUDA tensors, got {t.device}")
+    for o in others:
+        if o is not None and o.get_device() != i:
+            raise ValueError(f"tensors on {o.device} and {t.device}")
+    return i
+
+
 class _Launch:
     """Makes the tensors' device current for a call, and the call's stream the
     one its own allocations belong to (a workspace is then reused only behind
-    the work that uses it)."""
+    the work that uses it).  Entering gives the raw stream."""
+    __slots__ = ("_ctx", "_index")
 
-    def __init__(self, device, stream, *tensors):
-        if device.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got {device}")
-        for t in tensors:
-            if t is not None and t.device != device:
-                raise ValueError(f"tensors on {t.device} and {device}")
-        self._ctx = []
-        if stream is not None and not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
+    def __init__(self, index, stream):
+        self._index = index
         if stream is not None:
-            self._ctx.append(torch.cuda.stream(stream))
-        elif device.index is not None and device.index != torch.cuda.current_device():
-            self._ctx.append(torch.cuda.device(device))
-        self._stream = stream
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream),
+                                                   device=torch.device("cuda", index))
+            self._ctx = torch.cuda.stream(stream)
+        else:
+            self._ctx = None if index == torch.cuda.current_device() else \
+                torch.cuda.device(index)
 
     def __enter__(self):
-        for c in self._ctx:
-            c.__enter__()
-        return _stream(self._stream)
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return torch.cuda.current_stream(self._index).cuda_stream
 
     def __exit__(self, *exc):
-        for c in reversed(self._ctx):
-            c.__exit__(*exc)
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
         return False
 
 
 def _host_vec(a, n, dtype, name):
-    a = _host_i64(a) if dtype is np.int64 else _host_i32(a)
+    if not (type(a) is np.ndarray and a.dtype == dtype and a.flags.c_contiguous):
+        a = _host_i64(a) if dtype is np.int64 else _host_i32(a)
     if a.shape != (n,):
         raise ValueError(f"{name}: expected {n} entries, got shape {a.shape}")
+    return a
+
+
+def _np_ptr(a) -> int:
+    """Address of a host array's data (ndarray.ctypes builds an object per use,
+    several microseconds for the arrays of one call)."""
+    try:
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))
+    except (TypeError, ValueError, BufferError):    # read-only or empty
+        return a.ctypes.data
+
+
+def _host_offsets(a):
+    a = _host_vec(a, len(a), np.int64, "offsets")
+    if len(a) < 1:
+        raise ValueError("offsets: expected batch + 1 entries")
     return a
 
 
@@ -546,7 +573,7 @@ def qcache_append(cache, k, v, timestamps, tok_offsets, rows, pos, *, stream=Non
     """hstu_qcache_append: quantise new tokens' keys and values [T, H, d] into
     the cache; sequence b's tokens tok_offsets[b]..tok_offsets[b + 1] go to rows
     rows[b].. at positions pos[b]..."""
-    off = _host_i64(tok_offsets)
+    off = _host_offsets(tok_offsets)
     B = len(off) - 1
     rows, pos = _host_vec(rows, B, np.int64, "rows"), _host_vec(pos, B, np.int32, "pos")
     dt = _act_dtype(k, "k")
@@ -558,9 +585,9 @@ def qcache_append(cache, k, v, timestamps, tok_offsets, rows, pos, *, stream=Non
     k_rs = _row_stride(k, cache.num_heads, cache.d_qk, "k")
     v_rs = _row_stride(v, cache.num_heads, cache.d_v, "v")
     _typed(timestamps, torch.int64, "timestamps")
-    with _Launch(cache.device, stream, k, v, timestamps) as st:
-        _check(LIB.hstu_qcache_append(ctypes.byref(cache._c), dt, B, off.ctypes.data,
-                                      rows.ctypes.data, pos.ctypes.data, _ptr(k), k_rs, _ptr(v),
+    with _Launch(_cuda_index(cache.k_codes, k, v, timestamps), stream) as st:
+        _check(LIB.hstu_qcache_append(ctypes.byref(cache._c), dt, B, _np_ptr(off),
+                                      _np_ptr(rows), _np_ptr(pos), _ptr(k), k_rs, _ptr(v),
                                       v_rs, _ptr(timestamps), st), "hstu_qcache_append")
 
 
@@ -569,7 +596,7 @@ def qcache_read(cache, rows, lens, *, dtype=torch.bfloat16, k=None, v=None, stre
     lens = _host_i64(lens)
     rows = _host_vec(rows, len(lens), np.int64, "rows")
     T = int(lens.sum())
-    with _Launch(cache.device, stream, k, v) as st:
+    with _Launch(_cuda_index(cache.k_codes, k, v), stream) as st:
         if k is None:
             k = torch.empty((T, cache.num_heads, cache.d_qk), dtype=dtype, device=cache.device)
         if v is None:
@@ -579,7 +606,7 @@ def qcache_read(cache, rows, lens, *, dtype=torch.bfloat16, k=None, v=None, stre
         k_rs = _row_stride(k, cache.num_heads, cache.d_qk, "k")
         v_rs = _row_stride(v, cache.num_heads, cache.d_v, "v")
         _check(LIB.hstu_qcache_read(ctypes.byref(cache._c), _act_dtype(k, "k"), len(lens),
-                                    rows.ctypes.data, lens.ctypes.data, _ptr(k), k_rs, _ptr(v),
+                                    _np_ptr(rows), _np_ptr(lens), _ptr(k), k_rs, _ptr(v),
                                     v_rs, st), "hstu_qcache_read")
     return k, v
 
@@ -602,14 +629,14 @@ def qcache_evict(cache, rows, lens, budgets, keep_pos, *, dst=None, dst_rows=Non
     to = cache if dst is None else dst
     to_rows = rows if dst is None else _host_vec(dst_rows, B, np.int64, "dst_rows")
     n = ctypes.c_size_t(0)
-    _check(LIB.hstu_qcache_evict_workspace_size(B, lens.ctypes.data, budgets.ctypes.data,
+    _check(LIB.hstu_qcache_evict_workspace_size(B, _np_ptr(lens), _np_ptr(budgets),
                                                 ctypes.byref(n)),
            "hstu_qcache_evict_workspace_size")
-    with _Launch(cache.device, stream, workspace) as st:
+    with _Launch(_cuda_index(cache.k_codes, workspace), stream) as st:
         ws = _workspace(int(n.value), cache.device, workspace)
         _check(LIB.hstu_qcache_evict(
-            ctypes.byref(cache._c), ctypes.byref(to._c), B, rows.ctypes.data, lens.ctypes.data,
-            budgets.ctypes.data, keep_pos.ctypes.data, to_rows.ctypes.data, _ptr(ws),
+            ctypes.byref(cache._c), ctypes.byref(to._c), B, _np_ptr(rows), _np_ptr(lens),
+            _np_ptr(budgets), _np_ptr(keep_pos), _np_ptr(to_rows), _ptr(ws),
             ws.numel() * ws.element_size(), st), "hstu_qcache_evict")
     return np.minimum(lens, budgets)
 
@@ -628,9 +655,14 @@ def attn_fwd_candidates_qcache(q, k, v, cache, cache_rows, cache_lens, cand_offs
     """hstu_attn_fwd_candidates_qcache: out[Tc, H, d_v] for candidates against
     the 4-bit cache.  weight_decay: None leaves cache.weight alone; a number
     updates it (weight <- weight_decay weight + this call's weights)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [Tc, H, d_qk]")
     Tc, H = q.shape[0], q.shape[1]
     d_v = v.shape[-1] if v.dim() == 3 else v.shape[1] // H
-    coff = _host_i64(cand_offsets)
+    dt = _act_dtype(q, "q")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError(f"q, k, v must share a dtype, got {q.dtype}, {k.dtype}, {v.dtype}")
+    coff = _host_offsets(cand_offsets)
     B = len(coff) - 1
     rows = _host_vec(cache_rows, B, np.int64, "cache_rows")
     lens = _host_vec(cache_lens, B, np.int64, "cache_lens")
@@ -646,25 +678,29 @@ def attn_fwd_candidates_qcache(q, k, v, cache, cache_rows, cache_lens, cand_offs
         _typed(t, torch.float32, name)
         if tuple(t.shape[:-1]) != ((H,) if rab_per_head else ()):
             raise ValueError(f"{name}: unexpected shape {list(t.shape)}")
-    with _Launch(cache.device, stream, q, k, v, cand_timestamps, rab_pos, rab_time, out,
-                 workspace) as st:
+    with _Launch(_cuda_index(cache.k_codes, q, k, v, cand_timestamps, rab_pos, rab_time, out,
+                             workspace), stream) as st:
         if out is None:
             out = torch.empty((Tc, H, d_v), dtype=q.dtype, device=q.device)
         if out.shape[0] < n_c or out.dtype != q.dtype:
             raise ValueError(f"out must hold {n_c} candidates of {q.dtype}")
-        p = make_params(q, k, v, coff, max_seq_len=max_seq_len,
-                        num_pos_buckets=rab_pos.shape[-1], num_time_buckets=rab_time.shape[-1],
-                        time_bucket_sub_bits=time_bucket_sub_bits, alpha=alpha,
-                        silu_scale=silu_scale, rab_per_head=rab_per_head, impl=impl, out=out)
+        d_qk, msl = q.shape[2], int(max_seq_len)
+        p = AttnParams(B, H, d_qk, d_v, msl, rab_pos.shape[-1], rab_time.shape[-1],
+                       int(time_bucket_sub_bits), int(bool(rab_per_head)), MASK_CAUSAL, dt,
+                       IMPL[impl], _row_stride(q, H, d_qk, "q"), _row_stride(k, H, d_qk, "k"),
+                       _row_stride(v, H, d_v, "v"), _row_stride(out, H, d_v, "out"), 0, 0, 0, 0,
+                       1.0 / math.sqrt(d_qk) if alpha is None else alpha,
+                       1.0 / max(1, msl) if silu_scale is None else silu_scale)
         upd, decay = int(weight_decay is not None), float(weight_decay or 0.0)
         n = ctypes.c_size_t(0)
+        pp, lens_p, coff_p = ctypes.byref(p), _np_ptr(lens), _np_ptr(coff)
         _check(LIB.hstu_attn_candidates_qcache_workspace_size(
-            ctypes.byref(p), lens.ctypes.data, coff.ctypes.data, upd, ctypes.byref(n)),
+            pp, lens_p, coff_p, upd, ctypes.byref(n)),
             "hstu_attn_candidates_qcache_workspace_size")
         ws = _workspace(int(n.value), q.device, workspace)
         _check(LIB.hstu_attn_fwd_candidates_qcache(
-            ctypes.byref(p), ctypes.byref(cache._c), rows.ctypes.data, lens.ctypes.data,
-            coff.ctypes.data, pos.ctypes.data, _ptr(cand_timestamps), _ptr(q), _ptr(k), _ptr(v),
+            pp, ctypes.byref(cache._c), _np_ptr(rows), lens_p, coff_p, _np_ptr(pos),
+            _ptr(cand_timestamps), _ptr(q), _ptr(k), _ptr(v),
             _ptr(rab_pos), _ptr(rab_time), upd, decay, _ptr(out), _ptr(ws),
             ws.numel() * ws.element_size(), st), "hstu_attn_fwd_candidates_qcache")
     return out
@@ -682,7 +718,7 @@ def layer_fwd_candidates_qcache(x_cand, w1, b1, ln_gamma, ln_beta, w2, b2, rab_p
     Tc, D = x_cand.shape
     H, F = num_heads, num_heads * d_v
     n1 = 2 * (F + H * d_qk)
-    coff = _host_i64(cand_offsets)
+    coff = _host_offsets(cand_offsets)
     B = len(coff) - 1
     rows = _host_vec(cache_rows, B, np.int64, "cache_rows")
     lens = _host_vec(cache_lens, B, np.int64, "cache_lens")
@@ -705,8 +741,9 @@ def layer_fwd_candidates_qcache(x_cand, w1, b1, ln_gamma, ln_beta, w2, b2, rab_p
     if weight_decay is not None and cache.weight is None:
         raise ValueError("weight_decay needs a cache with weights")
     _typed(cand_timestamps, torch.int64, "cand_timestamps")
-    with _Launch(cache.device, stream, x_cand, w1, b1, ln_gamma, ln_beta, w2, b2, rab_pos,
-                 rab_time, cand_timestamps, out, proj_out, workspace) as st:
+    with _Launch(_cuda_index(cache.k_codes, x_cand, w1, b1, ln_gamma, ln_beta, w2, b2, rab_pos,
+                             rab_time, cand_timestamps, out, proj_out, workspace),
+                 stream) as st:
         if out is None:
             out = torch.empty((Tc, D), dtype=bf, device=x_cand.device)
         lp, _, _ = _layer_params(x_cand, rab_pos, rab_time, coff, None, num_heads=H, d_qk=d_qk,
@@ -716,12 +753,12 @@ def layer_fwd_candidates_qcache(x_cand, w1, b1, ln_gamma, ln_beta, w2, b2, rab_p
         upd, decay = int(weight_decay is not None), float(weight_decay or 0.0)
         n = ctypes.c_size_t(0)
         _check(LIB.hstu_layer_candidates_qcache_workspace_size(
-            ctypes.byref(lp), lens.ctypes.data, coff.ctypes.data, upd, ctypes.byref(n)),
+            ctypes.byref(lp), _np_ptr(lens), _np_ptr(coff), upd, ctypes.byref(n)),
             "hstu_layer_candidates_qcache_workspace_size")
         ws = _workspace(int(n.value), x_cand.device, workspace)
         _check(LIB.hstu_layer_fwd_candidates_qcache(
-            ctypes.byref(lp), ctypes.byref(cache._c), rows.ctypes.data, lens.ctypes.data,
-            coff.ctypes.data, pos.ctypes.data, _ptr(cand_timestamps), _ptr(x_cand), _ptr(w1),
+            ctypes.byref(lp), ctypes.byref(cache._c), _np_ptr(rows), _np_ptr(lens),
+            _np_ptr(coff), _np_ptr(pos), _ptr(cand_timestamps), _ptr(x_cand), _ptr(w1),
             _ptr(b1), _ptr(ln_gamma), _ptr(ln_beta), _ptr(w2), _ptr(b2), _ptr(rab_pos),
             _ptr(rab_time), upd, decay, _ptr(out), _ptr(proj_out), _ptr(ws),
             ws.numel() * ws.element_size(), st), "hstu_layer_fwd_candidates_qcache")
