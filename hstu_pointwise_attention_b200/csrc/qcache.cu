@@ -19,28 +19,43 @@ namespace qc {
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 
-// rne(x / s) of the exact quotient, given inv = 1 / s: the product rounds to
-// within one of it, and the remainder x - y s (exact in one fma) settles it.
-__device__ __forceinline__ float rne_div(float x, float s, float inv) {
-  float y = rintf(x * inv);
-  const float rem = fmaf(-y, s, x), half = 0.5f * s;
-  if (rem > half || rem < -half || (fabsf(rem) == half && fmodf(y, 2.0f) != 0.0f))
-    y += rem > 0.f ? 1.f : -1.f;
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// Scale and zero point of a group from its extremes, lo <= 0 <= hi.
-__device__ __forceinline__ void group_scale(float lo, float hi, float &s, float &inv, int &z) {
+// rne(x / s) of the exact quotient, given inv ~ 1 / s (to 2^-22): the product
+// rounds to within one of it, and the remainder x - y s (exact in one fma)
+// settles it.
+__device__ __forceinline__ int rne_div(float x, float s, float inv) {
+  const float y = rintf(x * inv);
+  const float rem = fmaf(-y, s, x), half = 0.5f * s;
+  const int i = int(y);
+  if (fabsf(rem) > half || (fabsf(rem) == half && (i & 1))) return i + (rem > 0.f ? 1 : -1);
+  return i;
+}
+
+// The same where x has 8 significant bits (bf16) and s 4: x / s is then a tie
+// between two integers or at least 2^-13 of its size away from one, so the
+// float32 quotient (product and one correction) rounds to the integer that the
+// exact one rounds to.  Adding 1.5 2^23 rounds to the nearest even integer.
+__device__ __forceinline__ int rne_div_bf16(float x, float s, float inv) {
+  const float q = x * inv;
+  return __float_as_int(fmaf(fmaf(-q, s, x), inv, q) + 12582912.0f) - 0x4B400000;
+}
+
+// Scale of a group from its extremes, lo <= 0 <= hi: 4 significant bits.
+__device__ __forceinline__ float group_scale(float lo, float hi) {
   // span = hi - lo exactly: rounded difference r plus its rounding error
   const float r = hi - lo, bb = r - hi, err = (hi - (r - bb)) + (-lo - bb);
-  // the scale's 4 significant bits: truncate r / 15, one step up unless
-  // 15 s (exact) already covers the span
-  s = __uint_as_float(__float_as_uint(r / 15.0f) & 0xFFF00000u);
+  // r / 15 to within an ulp, truncated, is the scale or one step below it (a
+  // product an ulp too large that reaches the next step reaches a scale that
+  // 15 s >= span holds for); the exact 15 s decides
+  float s = __uint_as_float(__float_as_uint(r * (1.0f / 15.0f)) & 0xFFF00000u);
   const float p = 15.0f * s;
   if (p < r || (p == r && err > 0.f)) s = __uint_as_float(__float_as_uint(s) + 0x00100000u);
-  s = fmaxf(s, 0x1p-126f);
-  inv = 1.0f / s;
-  z = int(rne_div(-lo, s, inv));
+  return fmaxf(s, 0x1p-126f);
 }
 
 __device__ __forceinline__ float held(float x) {   // NaN as 0, magnitudes to 2^126
@@ -66,29 +81,19 @@ struct Eight<float> {
       for (int i = 0; i < 8; ++i) x[i] = p[i];
     }
   }
-  __device__ __forceinline__ void quantise(uint32_t quad, uint32_t &word, uint32_t &param) {
-    float lo = 0.f, hi = 0.f;
+  // This lane's extremes with 0; values brought into range.
+  __device__ __forceinline__ void extremes(float &lo, float &hi) {
+    lo = hi = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       x[i] = held(x[i]);
       lo = fminf(lo, x[i]);
       hi = fmaxf(hi, x[i]);
     }
-#pragma unroll
-    for (int m = 1; m < 4; m <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(quad, lo, m));
-      hi = fmaxf(hi, __shfl_xor_sync(quad, hi, m));
-    }
-    word = param = 0;
-    if (hi > lo) {
-      float s, inv;
-      int z;
-      group_scale(lo, hi, s, inv, z);
-      param = (__float_as_uint(s) >> 16) | uint32_t(z);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        word |= uint32_t(min(int(rne_div(x[i], s, inv)) + z, 15)) << (4 * (i >> 1) + 16 * (i & 1));
-    }
+  }
+  __device__ __forceinline__ float at(int i) const { return x[i]; }
+  static __device__ __forceinline__ int rne(float x, float s, float inv) {
+    return rne_div(x, s, inv);
   }
 };
 
@@ -109,15 +114,15 @@ struct Eight<__nv_bfloat16> {
   __device__ __forceinline__ float at(int i) const {
     return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
   }
-  __device__ __forceinline__ void quantise(uint32_t quad, uint32_t &word, uint32_t &param) {
-    // extremes two at a time (NaN and infinities show in them), then over the quad
+  __device__ __forceinline__ void extremes(float &lo, float &hi) {
+    // two at a time; NaN and infinities show in them
     auto b2 = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); };
     const __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(b2(w[0]), b2(w[1])),
                                            __hmin2_nan(b2(w[2]), b2(w[3])));
     const __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(b2(w[0]), b2(w[1])),
                                            __hmax2_nan(b2(w[2]), b2(w[3])));
-    float lo = __bfloat162float(__hmin_nan(lo2.x, lo2.y));
-    float hi = __bfloat162float(__hmax_nan(hi2.x, hi2.y));
+    lo = __bfloat162float(__hmin_nan(lo2.x, lo2.y));
+    hi = __bfloat162float(__hmax_nan(hi2.x, hi2.y));
     if (!(lo >= -0x1p126f && hi <= 0x1p126f)) {   // rare: bring the values into range
       lo = hi = 0.f;
 #pragma unroll
@@ -131,30 +136,25 @@ struct Eight<__nv_bfloat16> {
     }
     lo = fminf(lo, 0.f);
     hi = fmaxf(hi, 0.f);
-#pragma unroll
-    for (int m = 1; m < 4; m <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(quad, lo, m));
-      hi = fmaxf(hi, __shfl_xor_sync(quad, hi, m));
-    }
-    word = param = 0;
-    if (hi > lo) {
-      float s, inv;
-      int z;
-      group_scale(lo, hi, s, inv, z);
-      param = (__float_as_uint(s) >> 16) | uint32_t(z);
-      // x has 8 significant bits and s 4, so x / s is a tie between two integers
-      // or at least 2^-13 of its size away from one: the quotient to float32
-      // (product and one correction) rounds to the integer that the exact one
-      // rounds to.  Adding 1.5 2^23 rounds to the nearest even integer.
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = at(i), q = x * inv, y = fmaf(fmaf(-q, s, x), inv, q) + 12582912.0f;
-        word |= uint32_t(min(int(__float_as_uint(y)) + (z - 0x4B400000), 15))
-                << (4 * (i >> 1) + 16 * (i & 1));
-      }
-    }
+  }
+  static __device__ __forceinline__ int rne(float x, float s, float inv) {
+    return rne_div_bf16(x, s, inv);
   }
 };
+
+// Codes and parameter of a group with extremes lo <= 0 <= hi, from this lane's
+// eight values.  Zeros: s is at its floor, so z and the codes come out as 0.
+template <typename T>
+__device__ __forceinline__ void encode(const Eight<T> &x, float lo, float hi, uint32_t &word,
+                                       uint32_t &param) {
+  const float s = group_scale(lo, hi), inv = rcp_approx(s);
+  const int z = Eight<T>::rne(-lo, s, inv);
+  param = hi > lo ? (__float_as_uint(s) >> 16) | uint32_t(z) : 0u;
+  word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    word |= uint32_t(min(Eight<T>::rne(x.at(i), s, inv) + z, 15)) << (4 * (i >> 1) + 16 * (i & 1));
+}
 
 // A block takes tpb tokens side by side (or one in steps of the block), a thread
 // TPT of them one behind the other: with many tokens four, so that four loads
@@ -162,14 +162,29 @@ struct Eight<__nv_bfloat16> {
 struct RowPos {
   int64_t tok, row, pos;
 };
-__device__ __forceinline__ RowPos row_pos(const QcRowsParams &p, int64_t tok) {
-  const int s = qc_find(p.seqs, p.n_seqs, tok, [](const QcRows &r) { return r.tok; });
-  const int64_t i = tok - p.seqs[s].tok;
-  return {tok, p.seqs[s].row + i, p.seqs[s].pos + i};
+// The thread's tokens tok0, tok0 + step, ...: their number; the table is searched
+// once and then walked forward.
+template <int TPT>
+__device__ __forceinline__ int row_positions(const QcRowsParams &p, int64_t tok0, int step,
+                                             RowPos (&at)[TPT]) {
+  if (tok0 >= p.tok_end) return 0;
+  int s = qc_find(p.seqs, p.n_seqs, tok0, [](const QcRows &r) { return r.tok; });
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < TPT; ++k) {
+    const int64_t tok = tok0 + k * step;
+    if (tok < p.tok_end) {
+      while (s + 1 < p.n_seqs && p.seqs[s + 1].tok <= tok) ++s;
+      const int64_t i = tok - p.seqs[s].tok;
+      at[k] = {tok, p.seqs[s].row + i, p.seqs[s].pos + i};
+      n = k + 1;
+    }
+  }
+  return n;
 }
 
 template <typename T, int TPT>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 4)
     append_kernel(const __grid_constant__ QcRowsParams p) {
   const QCacheView &c = p.cache;
   const int kw = c.heads * (c.d_qk >> 3), units = kw + c.heads * (c.d_v >> 3);
@@ -181,34 +196,39 @@ __global__ void __launch_bounds__(kRowThreads)
   const uint32_t quad = 0xFu << (threadIdx.x & 28);   // other quads may have left the loops
   const int64_t tok0 = p.tok0 + int64_t(blockIdx.x) * (tpb * TPT) + tl;
   RowPos at[TPT];
-  int n = 0;   // this thread's tokens
-#pragma unroll
-  for (int k = 0; k < TPT; ++k)
-    if (tok0 + k * tpb < p.tok_end) {
-      at[k] = row_pos(p, tok0 + k * tpb);
-      n = k + 1;
-    }
+  const int n = row_positions<TPT>(p, tok0, tpb, at);
   for (int u = u0; u < units; u += (tpb > 1 ? units : kRowThreads)) {
     const bool is_v = u >= kw;
     const int d = is_v ? c.d_v : c.d_qk, e = (is_v ? u - kw : u) * 8;   // element of the row
-    const int h = e / d, ed = e - h * d;
+    const int h = int(__umulhi(uint32_t(e), is_v ? p.v_magic : p.k_magic)), ed = e - h * d;
     const T *src = static_cast<const T *>(is_v ? p.v : p.k) + e;
     const int64_t rs = is_v ? p.v_rs : p.k_rs;
     uint32_t *codes = (is_v ? c.v_codes : c.k_codes) + int64_t(h) * c.rows * (d >> 3) + (ed >> 3);
     uint16_t *scales = (is_v ? c.v_scales : c.k_scales) + int64_t(h) * c.rows * (d >> 5) + (ed >> 5);
-    Eight<T> x[TPT];
+    // each step for all of the thread's tokens, so that their chains overlap
+    Eight<T> x[TPT] = {};
+    float lo[TPT], hi[TPT];
 #pragma unroll
     for (int k = 0; k < TPT; ++k)
       if (k < n) x[k].load(src + at[k].tok * rs, p.vec);
 #pragma unroll
-    for (int k = 0; k < TPT; ++k) {
-      if (k < n) {
-        uint32_t word, param;
-        x[k].quantise(quad, word, param);
-        codes[at[k].row * (d >> 3)] = word;
-        if ((ed & 31) == 0) scales[at[k].row * (d >> 5)] = uint16_t(param);
+    for (int k = 0; k < TPT; ++k) x[k].extremes(lo[k], hi[k]);
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1)
+#pragma unroll
+      for (int k = 0; k < TPT; ++k) {
+        lo[k] = fminf(lo[k], __shfl_xor_sync(quad, lo[k], m));
+        hi[k] = fmaxf(hi[k], __shfl_xor_sync(quad, hi[k], m));
       }
-    }
+    uint32_t word[TPT], param[TPT];
+#pragma unroll
+    for (int k = 0; k < TPT; ++k) encode<T>(x[k], lo[k], hi[k], word[k], param[k]);
+#pragma unroll
+    for (int k = 0; k < TPT; ++k)
+      if (k < n) {
+        codes[at[k].row * (d >> 3)] = word[k];
+        if ((ed & 31) == 0) scales[at[k].row * (d >> 5)] = uint16_t(param[k]);
+      }
   }
   if (u0 == 0) {
 #pragma unroll
@@ -254,7 +274,7 @@ __device__ __forceinline__ void store_values(T *dst, uint32_t w, uint32_t param,
 }
 
 template <typename T, int TPT>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 6)
     read_kernel(const __grid_constant__ QcRowsParams p) {
   const QCacheView &c = p.cache;
   const int kw = c.heads * (c.d_qk >> 3), units = kw + c.heads * (c.d_v >> 3);
@@ -264,17 +284,11 @@ __global__ void __launch_bounds__(kRowThreads)
   const int u0 = int(threadIdx.x) - tl * units;
   const int64_t tok0 = p.tok0 + int64_t(blockIdx.x) * (tpb * TPT) + tl;
   RowPos at[TPT];
-  int n = 0;
-#pragma unroll
-  for (int k = 0; k < TPT; ++k)
-    if (tok0 + k * tpb < p.tok_end) {
-      at[k] = row_pos(p, tok0 + k * tpb);
-      n = k + 1;
-    }
+  const int n = row_positions<TPT>(p, tok0, tpb, at);
   for (int u = u0; u < units; u += (tpb > 1 ? units : kRowThreads)) {
     const bool is_v = u >= kw;
     const int d = is_v ? c.d_v : c.d_qk, e = (is_v ? u - kw : u) * 8;
-    const int h = e / d, ed = e - h * d;
+    const int h = int(__umulhi(uint32_t(e), is_v ? p.v_magic : p.k_magic)), ed = e - h * d;
     const uint32_t *codes =
         (is_v ? c.v_codes : c.k_codes) + int64_t(h) * c.rows * (d >> 3) + (ed >> 3);
     const uint16_t *scales =
@@ -321,8 +335,9 @@ cudaError_t launch_rows_t(const QcRowsParams &p, cudaStream_t st) {
 // Eviction, step 1: which row every kept row comes from.
 //
 // One CTA per sequence.  A row's key is its weight as an ordered 32-bit
-// integer.  Four passes over 8-bit digits (highest first) find the n-th
-// largest key; of the rows that share it the lowest are kept.  A kept row
+// integer, held in shared memory (up to kQcSelectKeys rows; recomputed from
+// memory beyond).  The n-th largest key is found from its highest bits down; of
+// the rows that share it the lowest are kept.  A kept row
 // below n stays where it is; kept rows at or behind n fill the holes below n,
 // both in ascending order, so the result does not depend on timing.
 // ---------------------------------------------------------------------------
@@ -385,34 +400,77 @@ __global__ void __launch_bounds__(kSelThreads)
     for (int32_t j = tid; j < L; j += kSelThreads)
       keys[j] = weight_key(weight[j], pos[j], sq.keep_pos);
   }
-  // ---- the n-th largest key, digit by digit ----
-  uint32_t prefix = 0, want = uint32_t(n);   // want: rank inside the prefix's rows
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int32_t j0 = 0; j0 < L; j0 += kSelThreads) {
-      const int32_t j = j0 + tid;
-      const uint32_t k = j < L ? key_of(j) : 0u;
-      const bool in = j < L && (k & mask) == prefix;
-      // equal digits of a warp are counted once (weights share exponents)
-      const uint32_t d = in ? (k >> shift) & 255u : 256u + uint32_t(lane);
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[d], uint32_t(__popc(same)));
+  // ---- the n-th largest key, and how many of its equals are kept (want) ----
+  uint32_t prefix = 0, want = uint32_t(n);
+  if (cached) {
+    // Two bits at a time: count the keys at or above each of the three next
+    // larger candidates.  16 rounds of a few compares per key and one barrier.
+    if (tid < 6) hist[tid] = 0;
+    __syncthreads();   // keys and counters
+    uint32_t above = 0;   // keys above the final prefix
+    for (int shift = 30, round = 0; shift >= 0; shift -= 2, ++round) {
+      uint32_t c1 = 0, c2 = 0, c3 = 0;
+      const uint32_t t1 = prefix | (1u << shift), t2 = prefix | (2u << shift),
+                     t3 = prefix | (3u << shift);
+      for (int32_t j = tid; j < L; j += kSelThreads) {
+        const uint32_t k = keys[j];
+        c1 += k >= t1;
+        c2 += k >= t2;
+        c3 += k >= t3;
+      }
+      c1 = __reduce_add_sync(0xffffffffu, c1);
+      c2 = __reduce_add_sync(0xffffffffu, c2);
+      c3 = __reduce_add_sync(0xffffffffu, c3);
+      uint32_t *cnt = hist + (round & 1) * 3;   // the other three are cleared meanwhile
+      if (lane < 3) atomicAdd(&cnt[lane], lane == 0 ? c1 : lane == 1 ? c2 : c3);
+      __syncthreads();
+      const uint32_t a1 = cnt[0], a2 = cnt[1], a3 = cnt[2];
+      // the largest candidate that at least n keys reach
+      if (a3 >= uint32_t(n)) {
+        prefix = t3;
+      } else if (a2 >= uint32_t(n)) {
+        prefix = t2;
+        above = a3;
+      } else if (a1 >= uint32_t(n)) {
+        prefix = t1;
+        above = a2;
+      } else {
+        above = a1;
+      }
+      // cleared for the round after next: everyone has read it at the next barrier
+      if (tid < 3) hist[((round + 1) & 1) * 3 + tid] = 0;
+      __syncthreads();
     }
-    __syncthreads();
-    // digits from 255 down: the one where the running count reaches want
-    const uint32_t cnt = tid < 256 ? hist[255 - tid] : 0u;
-    uint32_t total;
-    const uint32_t before = block_excl_sum(cnt, warp_sums, &total);
-    if (tid < 256 && before < want && before + cnt >= want) {
-      pick[0] = uint32_t(255 - tid);
-      pick[1] = before;
+    want = uint32_t(n) - above;
+  } else {
+    // Too long for shared memory: 8-bit digits, highest first, from a histogram.
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+      for (int32_t j0 = 0; j0 < L; j0 += kSelThreads) {
+        const int32_t j = j0 + tid;
+        const uint32_t k = j < L ? key_of(j) : 0u;
+        const bool in = j < L && (k & mask) == prefix;
+        // equal digits of a warp are counted once (weights share exponents)
+        const uint32_t d = in ? (k >> shift) & 255u : 256u + uint32_t(lane);
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[d], uint32_t(__popc(same)));
+      }
+      __syncthreads();
+      // digits from 255 down: the one where the running count reaches want
+      const uint32_t cnt = tid < 256 ? hist[255 - tid] : 0u;
+      uint32_t total;
+      const uint32_t before = block_excl_sum(cnt, warp_sums, &total);
+      if (tid < 256 && before < want && before + cnt >= want) {
+        pick[0] = uint32_t(255 - tid);
+        pick[1] = before;
+      }
+      __syncthreads();
+      prefix |= pick[0] << shift;
+      want -= pick[1];
+      __syncthreads();
     }
-    __syncthreads();
-    prefix |= pick[0] << shift;
-    want -= pick[1];
-    __syncthreads();
   }
   // ---- kept rows: every key above the threshold, and the first `want` at it ----
   // each thread owns a run of rows; an odd run length spreads the threads'
@@ -463,8 +521,8 @@ __global__ void __launch_bounds__(kMoveThreads)
                           [](const QcEvictSeq &s) { return s.block0; });
   const QcEvictSeq sq = p.seqs[sqi];
   const QCacheView &a = p.src, &b = p.dst;
-  const int64_t r0 = (int64_t(blockIdx.x) - sq.block0) * kQcMoveRows;
-  const int rows = int(min(int64_t(kQcMoveRows), int64_t(sq.keep) - r0));
+  const int64_t r0 = (int64_t(blockIdx.x) - sq.block0) * p.move_rows;
+  const int rows = int(min(int64_t(p.move_rows), int64_t(sq.keep) - r0));
   const int32_t *map = p.map + sq.map0 + r0;
   for (int r = threadIdx.x; r < rows; r += kMoveThreads) {
     const int32_t m = map[r];

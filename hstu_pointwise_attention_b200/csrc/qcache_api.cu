@@ -111,6 +111,8 @@ hstu_status_t run_rows(const hstu_qcache_t *cache, int32_t dtype, int32_t B, Tok
   p.k_rs = k_rs;
   p.v_rs = v_rs;
   p.ts = ts;
+  p.k_magic = uint32_t((uint64_t(1) << 32) / uint32_t(cache->d_qk)) + 1;
+  p.v_magic = uint32_t((uint64_t(1) << 32) / uint32_t(cache->d_v)) + 1;
   p.vec = aligned(k, 16) && aligned(v, 16) && k_rs % per16 == 0 && v_rs % per16 == 0;
   int64_t at = 0;
   for (int32_t b0 = 0; b0 < B; b0 += kQcMaxSeqs) {
@@ -543,6 +545,8 @@ hstu_status_t hstu_qcache_evict(const hstu_qcache_t *src, const hstu_qcache_t *d
   p.map = static_cast<int32_t *>(workspace);
   p.movers = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + half);
   p.in_place = in_place;
+  // 32 rows per block, 8 while that leaves SMs without one
+  p.move_rows = kept >= 32 * 4 * 148 ? 32 : 8;
   int64_t map0 = 0;
   for (int32_t b0 = 0; b0 < batch; b0 += kQcMaxSeqs) {
     p.n_seqs = std::min(kQcMaxSeqs, batch - b0);
@@ -561,7 +565,7 @@ hstu_status_t hstu_qcache_evict(const hstu_qcache_t *src, const hstu_qcache_t *d
       // nothing to move: everything is kept where it is
       if (in_place && s.keep == s.len) s.keep = s.len = 0;
       map0 += keep(b);
-      blocks += (s.keep + kQcMoveRows - 1) / kQcMoveRows;
+      blocks += (s.keep + p.move_rows - 1) / p.move_rows;
       longest = std::max(longest, s.len);
     }
     if (blocks == 0) continue;

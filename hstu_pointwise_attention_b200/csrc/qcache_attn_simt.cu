@@ -195,10 +195,34 @@ __global__ void __launch_bounds__(kFinThreads)
     const int64_t step = int64_t(sq.n) * H * dv;
     const float *a = p.acc + (sq.acc0 + x) * dv;
     T *o = static_cast<T *>(p.out) + (sq.q0 + x / H) * p.o_rs + int64_t(x % H) * dv;
-    for (int e = lane; e < dv; e += 32) {
-      float s = 0.f;
-      for (int k = 0; k < sq.splits; ++k) s += a[k * step + e];
-      o[e] = qc_round<T>(s * p.scale);
+    // four features per lane (d_v is a multiple of 32); eight key ranges' loads in flight
+    for (int e = lane * 4; e < dv; e += 128) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      int k = 0;
+      for (; k + 8 <= sq.splits; k += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          v[u] = *reinterpret_cast<const float4 *>(a + (k + u) * step + e);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          s.x += v[u].x;
+          s.y += v[u].y;
+          s.z += v[u].z;
+          s.w += v[u].w;
+        }
+      }
+      for (; k < sq.splits; ++k) {
+        const float4 v = *reinterpret_cast<const float4 *>(a + k * step + e);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+      o[e] = qc_round<T>(s.x * p.scale);
+      o[e + 1] = qc_round<T>(s.y * p.scale);
+      o[e + 2] = qc_round<T>(s.z * p.scale);
+      o[e + 3] = qc_round<T>(s.w * p.scale);
     }
     return;
   }
@@ -209,7 +233,9 @@ __global__ void __launch_bounds__(kFinThreads)
   const int64_t j = w - sq.wrow0;
   const int planes = (sq.n + plane - 1) / plane * H;
   float s = 0.f;
-  for (int k = 0; k < planes; ++k) s += p.wpart[sq.wp0 + int64_t(k) * sq.len + j];
+  const float *wp = p.wpart + sq.wp0 + j;
+#pragma unroll 8
+  for (int k = 0; k < planes; ++k) s += wp[int64_t(k) * sq.len];
   float *dst = c.weight + sq.row + j;
   const float old = p.decay == 0.f ? 0.f : p.decay * *dst;
   *dst = fmaf(p.scale, s, old);

@@ -20,13 +20,13 @@ struct QcRowsParams {
   int64_t k_rs, v_rs;
   const int64_t *ts;       // append
   int64_t tok0, tok_end;   // tokens of this launch
+  uint32_t k_magic, v_magic;   // 2^32 / d, rounded up: element / d for element < 2^20
   int32_t n_seqs;
   bool vec;                // 16-byte accesses to k and v are aligned
   QcRows seqs[kQcMaxSeqs];
 };
 
 // --- evict ---
-constexpr int kQcMoveRows = 32;          // kept rows per block of the copy
 constexpr int kQcSelectKeys = 40 * 1024; // keys the selection holds in shared memory
 struct QcEvictSeq {
   int64_t row, dst_row;
@@ -38,6 +38,7 @@ struct QcEvictParams {
   QCacheView src, dst;
   int32_t *map, *movers;
   int32_t n_seqs, key_cap;
+  int32_t move_rows;       // kept rows per block of the copy
   bool in_place;
   QcEvictSeq seqs[kQcMaxSeqs];
 };
