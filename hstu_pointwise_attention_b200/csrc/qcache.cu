@@ -32,8 +32,8 @@ __device__ __forceinline__ int rne_div(float x, float s, float inv) {
   const float y = rintf(x * inv);
   const float rem = fmaf(-y, s, x), half = 0.5f * s;
   const int i = int(y);
-  if (fabsf(rem) > half || (fabsf(rem) == half && (i & 1))) return i + (rem > 0.f ? 1 : -1);
-  return i;
+  const bool off = fabsf(rem) > half || (fabsf(rem) == half && (i & 1));
+  return i + (off ? (rem > 0.f ? 1 : -1) : 0);
 }
 
 // The same where x has 8 significant bits (bf16) and s 4: x / s is then a tie
@@ -156,88 +156,89 @@ __device__ __forceinline__ void encode(const Eight<T> &x, float lo, float hi, ui
     word |= uint32_t(min(Eight<T>::rne(x.at(i), s, inv) + z, 15)) << (4 * (i >> 1) + 16 * (i & 1));
 }
 
-// A block takes tpb tokens side by side (or one in steps of the block), a thread
-// TPT of them one behind the other: with many tokens four, so that four loads
-// are in flight per thread; with few one, to have more blocks.
-struct RowPos {
+// Up to 64 lanes share a token's units (a unit is 8 values, K's first), so a
+// thread finds its token's place once for several of them.  units is a multiple
+// of 4: a quad never straddles two tokens.
+
+struct RowThread {
   int64_t tok, row, pos;
+  int units, lanes, u0;
+  bool ok;
 };
-// The thread's tokens tok0, tok0 + step, ...: their number; the table is searched
-// once and then walked forward.
-template <int TPT>
-__device__ __forceinline__ int row_positions(const QcRowsParams &p, int64_t tok0, int step,
-                                             RowPos (&at)[TPT]) {
-  if (tok0 >= p.tok_end) return 0;
-  int s = qc_find(p.seqs, p.n_seqs, tok0, [](const QcRows &r) { return r.tok; });
-  int n = 0;
-#pragma unroll
-  for (int k = 0; k < TPT; ++k) {
-    const int64_t tok = tok0 + k * step;
-    if (tok < p.tok_end) {
-      while (s + 1 < p.n_seqs && p.seqs[s + 1].tok <= tok) ++s;
-      const int64_t i = tok - p.seqs[s].tok;
-      at[k] = {tok, p.seqs[s].row + i, p.seqs[s].pos + i};
-      n = k + 1;
-    }
+__host__ __device__ __forceinline__ int row_units(const QCacheView &c) {
+  return c.heads * ((c.d_qk + c.d_v) >> 3);
+}
+__device__ __forceinline__ RowThread row_thread(const QcRowsParams &p) {
+  RowThread t;
+  t.units = row_units(p.cache);
+  t.lanes = t.units < 64 ? t.units : 64;
+  const int tpb = kRowThreads / t.lanes, tl = int(threadIdx.x) / t.lanes;
+  t.u0 = int(threadIdx.x) - tl * t.lanes;
+  t.tok = p.tok0 + int64_t(blockIdx.x) * tpb + tl;
+  t.ok = tl < tpb && t.tok < p.tok_end;
+  if (t.ok) {
+    const int s = qc_find(p.seqs, p.n_seqs, t.tok, [](const QcRows &r) { return r.tok; });
+    const int64_t i = t.tok - p.seqs[s].tok;
+    t.row = p.seqs[s].row + i;
+    t.pos = p.seqs[s].pos + i;
   }
-  return n;
+  return t;
+}
+// A unit's place: element of the activation row, word of codes, parameter.
+struct UnitPlace {
+  bool is_v, first;
+  int e;
+  uint32_t *code;
+  uint16_t *scale;
+};
+__device__ __forceinline__ UnitPlace unit_place(const QcRowsParams &p, const RowThread &t, int u) {
+  const QCacheView &c = p.cache;
+  const int kw = c.heads * (c.d_qk >> 3);
+  UnitPlace q;
+  q.is_v = u >= kw;
+  const int w = q.is_v ? u - kw : u, d = q.is_v ? c.d_v : c.d_qk;
+  q.e = w * 8;
+  const int h = int(__umulhi(uint32_t(q.e), q.is_v ? p.v_magic : p.k_magic));
+  const int ew = w - h * (d >> 3);   // word of the head's row
+  const int64_t at = int64_t(h) * c.rows + t.row;
+  q.code = (q.is_v ? c.v_codes : c.k_codes) + (at * (d >> 3) + ew);
+  q.scale = (q.is_v ? c.v_scales : c.k_scales) + (at * (d >> 5) + (ew >> 2));
+  q.first = (ew & 3) == 0;
+  return q;
 }
 
-template <typename T, int TPT>
-__global__ void __launch_bounds__(kRowThreads, 4)
+// Bound by its instructions (about 16 per value pair for extremes, scale and
+// codes); many warps of one unit at a time beat fewer with several: 8 x 4096
+// tokens, 8 heads of 128 stored and read back in 94 us against 98-105 us with two
+// or four units in flight per thread.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads, 6)
     append_kernel(const __grid_constant__ QcRowsParams p) {
-  const QCacheView &c = p.cache;
-  const int kw = c.heads * (c.d_qk >> 3), units = kw + c.heads * (c.d_v >> 3);
-  // units is a multiple of 4: a group's quad never straddles two tokens
-  const int tpb = units < kRowThreads ? kRowThreads / units : 1;
-  const int tl = tpb > 1 ? int(threadIdx.x) / units : 0;
-  if (tl >= tpb) return;
-  const int u0 = int(threadIdx.x) - tl * units;
-  const uint32_t quad = 0xFu << (threadIdx.x & 28);   // other quads may have left the loops
-  const int64_t tok0 = p.tok0 + int64_t(blockIdx.x) * (tpb * TPT) + tl;
-  RowPos at[TPT];
-  const int n = row_positions<TPT>(p, tok0, tpb, at);
-  for (int u = u0; u < units; u += (tpb > 1 ? units : kRowThreads)) {
-    const bool is_v = u >= kw;
-    const int d = is_v ? c.d_v : c.d_qk, e = (is_v ? u - kw : u) * 8;   // element of the row
-    const int h = int(__umulhi(uint32_t(e), is_v ? p.v_magic : p.k_magic)), ed = e - h * d;
-    const T *src = static_cast<const T *>(is_v ? p.v : p.k) + e;
-    const int64_t rs = is_v ? p.v_rs : p.k_rs;
-    uint32_t *codes = (is_v ? c.v_codes : c.k_codes) + int64_t(h) * c.rows * (d >> 3) + (ed >> 3);
-    uint16_t *scales = (is_v ? c.v_scales : c.k_scales) + int64_t(h) * c.rows * (d >> 5) + (ed >> 5);
-    // each step for all of the thread's tokens, so that their chains overlap
-    Eight<T> x[TPT] = {};
-    float lo[TPT], hi[TPT];
+  const RowThread t = row_thread(p);
+  if (!t.ok) return;
+  const uint32_t quad = 0xFu << (threadIdx.x & 28);   // other quads may have left the loop
+  for (int u = t.u0; u < t.units; u += t.lanes) {
+    const UnitPlace at = unit_place(p, t, u);
+    const T *row = static_cast<const T *>(at.is_v ? p.v : p.k) + t.tok * (at.is_v ? p.v_rs : p.k_rs);
+    Eight<T> x;
+    x.load(row + at.e, p.vec);
+    float lo, hi;
+    x.extremes(lo, hi);
 #pragma unroll
-    for (int k = 0; k < TPT; ++k)
-      if (k < n) x[k].load(src + at[k].tok * rs, p.vec);
-#pragma unroll
-    for (int k = 0; k < TPT; ++k) x[k].extremes(lo[k], hi[k]);
-#pragma unroll
-    for (int m = 1; m < 4; m <<= 1)
-#pragma unroll
-      for (int k = 0; k < TPT; ++k) {
-        lo[k] = fminf(lo[k], __shfl_xor_sync(quad, lo[k], m));
-        hi[k] = fmaxf(hi[k], __shfl_xor_sync(quad, hi[k], m));
-      }
-    uint32_t word[TPT], param[TPT];
-#pragma unroll
-    for (int k = 0; k < TPT; ++k) encode<T>(x[k], lo[k], hi[k], word[k], param[k]);
-#pragma unroll
-    for (int k = 0; k < TPT; ++k)
-      if (k < n) {
-        codes[at[k].row * (d >> 3)] = word[k];
-        if ((ed & 31) == 0) scales[at[k].row * (d >> 5)] = uint16_t(param[k]);
-      }
+    for (int m = 1; m < 4; m <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(quad, lo, m));
+      hi = fmaxf(hi, __shfl_xor_sync(quad, hi, m));
+    }
+    uint32_t word, param;
+    encode<T>(x, lo, hi, word, param);
+    *at.code = word;
+    if (at.first) *at.scale = uint16_t(param);
   }
-  if (u0 == 0) {
-#pragma unroll
-    for (int k = 0; k < TPT; ++k)
-      if (k < n) {
-        c.times[at[k].row] = p.ts[at[k].tok];
-        c.pos[at[k].row] = int32_t(at[k].pos);
-        if (c.weight) c.weight[at[k].row] = 0.f;
-      }
+  if (t.u0 == 0) {
+    const QCacheView &c = p.cache;
+    c.times[t.row] = p.ts[t.tok];
+    c.pos[t.row] = int32_t(t.pos);
+    if (c.weight) c.weight[t.row] = 0.f;
   }
 }
 
@@ -273,60 +274,40 @@ __device__ __forceinline__ void store_values(T *dst, uint32_t w, uint32_t param,
   }
 }
 
-template <typename T, int TPT>
-__global__ void __launch_bounds__(kRowThreads, 6)
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
     read_kernel(const __grid_constant__ QcRowsParams p) {
-  const QCacheView &c = p.cache;
-  const int kw = c.heads * (c.d_qk >> 3), units = kw + c.heads * (c.d_v >> 3);
-  const int tpb = units < kRowThreads ? kRowThreads / units : 1;
-  const int tl = tpb > 1 ? int(threadIdx.x) / units : 0;
-  if (tl >= tpb) return;
-  const int u0 = int(threadIdx.x) - tl * units;
-  const int64_t tok0 = p.tok0 + int64_t(blockIdx.x) * (tpb * TPT) + tl;
-  RowPos at[TPT];
-  const int n = row_positions<TPT>(p, tok0, tpb, at);
-  for (int u = u0; u < units; u += (tpb > 1 ? units : kRowThreads)) {
-    const bool is_v = u >= kw;
-    const int d = is_v ? c.d_v : c.d_qk, e = (is_v ? u - kw : u) * 8;
-    const int h = int(__umulhi(uint32_t(e), is_v ? p.v_magic : p.k_magic)), ed = e - h * d;
-    const uint32_t *codes =
-        (is_v ? c.v_codes : c.k_codes) + int64_t(h) * c.rows * (d >> 3) + (ed >> 3);
-    const uint16_t *scales =
-        (is_v ? c.v_scales : c.k_scales) + int64_t(h) * c.rows * (d >> 5) + (ed >> 5);
-    T *dst = static_cast<T *>(const_cast<void *>(is_v ? p.v : p.k)) + e;
-    const int64_t rs = is_v ? p.v_rs : p.k_rs;
-    uint32_t w[TPT], par[TPT];
+  const RowThread t = row_thread(p);
+  if (!t.ok) return;
+  constexpr int N = 4;   // units in flight per thread
+  T *k_row = static_cast<T *>(const_cast<void *>(p.k)) + t.tok * p.k_rs;
+  T *v_row = static_cast<T *>(const_cast<void *>(p.v)) + t.tok * p.v_rs;
+  for (int u = t.u0; u < t.units; u += N * t.lanes) {
+    uint32_t w[N], par[N];
+    T *dst[N];
 #pragma unroll
-    for (int k = 0; k < TPT; ++k)
-      if (k < n) {
-        w[k] = codes[at[k].row * (d >> 3)];
-        par[k] = scales[at[k].row * (d >> 5)];
+    for (int k = 0; k < N; ++k)
+      if (u + k * t.lanes < t.units) {
+        const UnitPlace at = unit_place(p, t, u + k * t.lanes);
+        w[k] = *at.code;
+        par[k] = *at.scale;
+        dst[k] = (at.is_v ? v_row : k_row) + at.e;
       }
 #pragma unroll
-    for (int k = 0; k < TPT; ++k)
-      if (k < n) store_values<T>(dst + at[k].tok * rs, w[k], par[k], p.vec);
+    for (int k = 0; k < N; ++k)
+      if (u + k * t.lanes < t.units) store_values<T>(dst[k], w[k], par[k], p.vec);
   }
 }
 
 template <typename T, bool APPEND>
 cudaError_t launch_rows_t(const QcRowsParams &p, cudaStream_t st) {
-  const int units = p.cache.heads * ((p.cache.d_qk + p.cache.d_v) >> 3);
-  const int tpb = units < kRowThreads ? kRowThreads / units : 1;
+  const int units = row_units(p.cache), tpb = kRowThreads / (units < 64 ? units : 64);
   const int64_t blocks = (p.tok_end - p.tok0 + tpb - 1) / tpb;
   if (blocks <= 0) return cudaSuccess;
-  // four tokens per thread once that still fills the SMs (8 blocks of 256 each)
-  if (blocks >= 4 * 8 * 148) {
-    const unsigned n = unsigned((blocks + 3) / 4);
-    if constexpr (APPEND)
-      append_kernel<T, 4><<<n, kRowThreads, 0, st>>>(p);
-    else
-      read_kernel<T, 4><<<n, kRowThreads, 0, st>>>(p);
-  } else {
-    if constexpr (APPEND)
-      append_kernel<T, 1><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
-    else
-      read_kernel<T, 1><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
-  }
+  if constexpr (APPEND)
+    append_kernel<T><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
+  else
+    read_kernel<T><<<unsigned(blocks), kRowThreads, 0, st>>>(p);
   count_launch();
   return cudaGetLastError();
 }
