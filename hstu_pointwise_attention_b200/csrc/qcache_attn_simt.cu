@@ -6,11 +6,12 @@
 //   x_ij = alpha <q_i, k_j> + rab_pos[P_b - pos_j] + rab_time[tb(t_i - t_j)]
 //   w_j  <- decay w_j + c sum_{i, h} |SiLU(x_ij)|
 //
-// One CTA = 16 candidates of one (sequence, head) and a range of keys, 32 keys
-// at a time: rows of the cache are decoded to float32 in shared memory, each
-// thread makes the weights of one key for 4 candidates, then each thread sums
-// one or two output columns over the 32 keys.  It is bound by its shared-memory
-// reads (one per multiply-add in the first step).
+// One CTA = 16 candidates of one (sequence, head) and a range of keys, 64 keys
+// at a time: their rows are decoded to float32 in shared memory, each thread
+// makes the weights of one key for 8 candidates, then sums one or two output
+// columns over the 64 keys (with at most 64 columns, over every other key).  Bound
+// by shared-memory reads: 9 16-byte reads per 32 multiply-adds in the first step,
+// 5 per 16 in the second.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,21 +24,45 @@ namespace qc_simt {
 
 constexpr int kThreads = 128;
 constexpr int kQ = kQcSimtQueries;   // candidates per CTA
-constexpr int kKeys = 32;            // keys per step
+constexpr int kKeys = 64;            // keys per step
 constexpr int kPerThread = kQ / (kThreads / kKeys);
+constexpr int kPPitch = kQ + 4;      // P [kKeys][kPPitch]: 8 keys' rows in 8 bank groups
 
-// Shared memory in floats: q [kQ][d_qk], k [kKeys][d_qk + 1], v [kKeys][d_v],
-// p [kQ][kKeys + 1].
+// Shared memory in floats: q [kQ][d_qk], k [kKeys][d_qk + 4], v [kKeys][d_v], P.
 __host__ __device__ constexpr size_t smem_floats(int d_qk, int d_v) {
-  return size_t(kQ) * d_qk + size_t(kKeys) * (d_qk + 1) + size_t(kKeys) * d_v + kQ * (kKeys + 1);
+  return size_t(kQ) * d_qk + size_t(kKeys) * (d_qk + 4) + size_t(kKeys) * d_v + kKeys * kPPitch;
 }
 
 __device__ __forceinline__ float silu_exact(float x) { return x / (1.0f + expf(-x)); }
 
+// Rows [0, n) of codes to float32 rows of `pitch`, rows [n, kKeys) to zeros.
+__device__ __forceinline__ void decode_rows(float *dst, int pitch, const uint32_t *codes,
+                                            const uint16_t *scales, int64_t at, int d, int n) {
+  const int words = d >> 3;
+  for (int x = threadIdx.x; x < kKeys * words; x += kThreads) {
+    const int r = x / words, w = x - r * words;
+    uint32_t code = 0, par = 0;
+    if (r < n) {
+      code = codes[(at + r) * words + w];
+      par = scales[(at + r) * (d >> 5) + (w >> 2)];
+    }
+    const float s = q4_scale(par);
+    // 2^23 + q as a float is 0x4B000000 | q: less 2^23 + z leaves q - z
+    const float z = 8388608.0f + float(par & 15u);
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[e] = s * (__uint_as_float(0x4B000000u | uint32_t(q4_code(code, e))) - z);
+    float4 *p = reinterpret_cast<float4 *>(dst + r * pitch + 8 * w);
+    p[0] = make_float4(o[0], o[1], o[2], o[3]);
+    p[1] = make_float4(o[4], o[5], o[6], o[7]);
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     attn_kernel(const __grid_constant__ QcAttnParams p) {
-  extern __shared__ float sm[];
+  extern __shared__ float4 sm4[];
   const QCacheView &c = p.cache;
   const int H = c.heads, dq = c.d_qk, dv = c.d_v;
   const int item = int(blockIdx.x) / H, h = int(blockIdx.x) - item * H;
@@ -46,7 +71,8 @@ __global__ void __launch_bounds__(kThreads)
   const QcItem it = qc_item(p, item);
   const QcAttnSeq &sq = p.seqs[it.seq];
   const int i0 = it.qtile * kQ, nq = min(kQ, sq.n - i0);
-  float *sq_q = sm, *sk = sq_q + kQ * dq, *sv = sk + kKeys * (dq + 1), *sp = sv + kKeys * dv;
+  float *sq_q = reinterpret_cast<float *>(sm4), *sk = sq_q + kQ * dq, *sv = sk + kKeys * (dq + 4),
+        *sp = sv + kKeys * dv;
   __shared__ int64_t s_t[kQ];
   const float *rp = p.rab_p + (p.rab_per_head ? int64_t(h) * p.nb_p : 0);
   const float *rt = p.rab_t + (p.rab_per_head ? int64_t(h) * p.nb_t : 0);
@@ -65,77 +91,87 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < kQ; ++i) acc[a][i] = 0.f;
 
   const int kj = tid & (kKeys - 1), kg = tid / kKeys;   // key and candidate group of step 1
+  const bool paired = dv <= 64;                         // step 2: two threads per column
+  const int e0 = paired ? tid & 63 : tid;
   const int32_t j_end = min(it.t1 * kQcKeyTile, sq.len);
   for (int32_t jb = it.t0 * kQcKeyTile; jb < j_end; jb += kKeys) {
     const int nk = min(kKeys, j_end - jb);
     __syncthreads();
-    // decode 32 keys and values: a word of 8 codes per thread and step
     const int64_t at0 = int64_t(h) * c.rows + sq.row + jb;
-    for (int x = tid; x < kKeys * (dq >> 3); x += kThreads) {
-      const int r = x / (dq >> 3), w = x - r * (dq >> 3);
-      uint32_t code = 0, par = 0;
-      if (r < nk) {
-        code = c.k_codes[(at0 + r) * (dq >> 3) + w];
-        par = c.k_scales[(at0 + r) * (dq >> 5) + (w >> 2)];
-      }
-      const float s = q4_scale(par);
-      const int z = int(par & 15u);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sk[r * (dq + 1) + 8 * w + e] = s * float(q4_code(code, e) - z);
-    }
-    for (int x = tid; x < kKeys * (dv >> 3); x += kThreads) {
-      const int r = x / (dv >> 3), w = x - r * (dv >> 3);
-      uint32_t code = 0, par = 0;
-      if (r < nk) {
-        code = c.v_codes[(at0 + r) * (dv >> 3) + w];
-        par = c.v_scales[(at0 + r) * (dv >> 5) + (w >> 2)];
-      }
-      const float s = q4_scale(par);
-      const int z = int(par & 15u);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sv[r * dv + 8 * w + e] = s * float(q4_code(code, e) - z);
-    }
+    decode_rows(sk, dq + 4, c.k_codes, c.k_scales, at0, dq, nk);
+    decode_rows(sv, dv, c.v_codes, c.v_scales, at0, dv, nk);
+    const bool key_ok = kj < nk;
+    const int64_t row = sq.row + jb + (key_ok ? kj : 0);
+    const float bp = rp[pos_bucket(int64_t(sq.pos) - c.pos[row], p.nb_p)];
+    const int64_t tk = c.times[row];
     __syncthreads();
-    {
+    if (kg * kPerThread < nq) {
       float dot[kPerThread];
 #pragma unroll
       for (int u = 0; u < kPerThread; ++u) dot[u] = 0.f;
-      const float *kr = sk + kj * (dq + 1), *qr = sq_q + kg * kPerThread * dq;
-      for (int e = 0; e < dq; ++e) {
-        const float kv = kr[e];
+      const float *kr = sk + kj * (dq + 4), *qr = sq_q + kg * kPerThread * dq;
+      for (int e = 0; e < dq; e += 4) {
+        const float4 kv = *reinterpret_cast<const float4 *>(kr + e);
 #pragma unroll
-        for (int u = 0; u < kPerThread; ++u) dot[u] = fmaf(qr[u * dq + e], kv, dot[u]);
+        for (int u = 0; u < kPerThread; ++u) {
+          const float4 qv = *reinterpret_cast<const float4 *>(qr + u * dq + e);
+          dot[u] = fmaf(qv.x, kv.x, dot[u]);
+          dot[u] = fmaf(qv.y, kv.y, dot[u]);
+          dot[u] = fmaf(qv.z, kv.z, dot[u]);
+          dot[u] = fmaf(qv.w, kv.w, dot[u]);
+        }
       }
-      const bool key_ok = kj < nk;
-      const int64_t row = sq.row + jb + (key_ok ? kj : 0);
-      const float bp = rp[pos_bucket(int64_t(sq.pos) - c.pos[row], p.nb_p)];
-      const int64_t tk = c.times[row];
 #pragma unroll
       for (int u = 0; u < kPerThread; ++u) {
         const int i = kg * kPerThread + u;
-        const float b = qc_bias(bp + rt[time_bucket_i64(s_t[i] - tk, p.sub_bits, p.nb_t)]);
-        const float x = fmaf(p.alpha, dot[u], b);
-        sp[i * (kKeys + 1) + kj] = key_ok && i < nq ? silu_exact(x) : 0.f;
+        float pv = 0.f;
+        if (key_ok && i < nq) {
+          const float b = qc_bias(bp + rt[time_bucket_i64(s_t[i] - tk, p.sub_bits, p.nb_t)]);
+          pv = silu_exact(fmaf(p.alpha, dot[u], b));
+        }
+        sp[kj * kPPitch + i] = pv;
       }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kPerThread; ++u) sp[kj * kPPitch + kg * kPerThread + u] = 0.f;
     }
     __syncthreads();
     if (p.weight_rows > 0 && tid < nk) {
       float w = 0.f;
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) w += fabsf(sp[i * (kKeys + 1) + tid]);
+      for (int i = 0; i < kQ; ++i) w += fabsf(sp[tid * kPPitch + i]);
       p.wpart[sq.wp0 + (int64_t(it.qtile) * H + h) * sq.len + jb + tid] = w;
     }
+    const int quads = (nq + 3) >> 2;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      const int e = tid + a * kThreads;
+      const int e = e0 + a * kThreads;
       if (e < dv) {
-        for (int j = 0; j < nk; ++j) {
+        for (int j = paired ? tid >> 6 : 0; j < nk; j += paired ? 2 : 1) {
           const float vv = sv[j * dv + e];
 #pragma unroll
-          for (int i = 0; i < kQ; ++i) acc[a][i] = fmaf(sp[i * (kKeys + 1) + j], vv, acc[a][i]);
+          for (int i = 0; i < kQ / 4; ++i) {
+            if (i < quads) {
+              const float4 pv = *reinterpret_cast<const float4 *>(sp + j * kPPitch + 4 * i);
+              acc[a][4 * i] = fmaf(pv.x, vv, acc[a][4 * i]);
+              acc[a][4 * i + 1] = fmaf(pv.y, vv, acc[a][4 * i + 1]);
+              acc[a][4 * i + 2] = fmaf(pv.z, vv, acc[a][4 * i + 2]);
+              acc[a][4 * i + 3] = fmaf(pv.w, vv, acc[a][4 * i + 3]);
+            }
+          }
         }
       }
     }
+  }
+  if (paired) {   // the odd keys' sums join the even ones'
+    __syncthreads();
+    if (tid >= 64 && e0 < dv)
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) sv[i * 64 + e0] = acc[0][i];
+    __syncthreads();
+    if (tid < 64 && e0 < dv)
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) acc[0][i] += sv[i * 64 + e0];
   }
   // ---- the candidate's own pair (distance 0 in position and time) ----
   __syncthreads();
@@ -157,7 +193,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
     const int e = tid + a * kThreads;
-    if (e >= dv) continue;
+    if (e >= dv) continue;   // (paired: the upper threads' e is past d_v)
 #pragma unroll
     for (int i = 0; i < kQ; ++i) {
       if (i >= nq) break;
