@@ -108,10 +108,10 @@ struct Smem {
   alignas(16) uint8_t k_scales[C::kStages][C::kScaleBytes];
   alignas(16) uint8_t v_scales[C::kStages][C::kScaleBytes];
   KeyBias bias[kBias];
-  // of a segment and the next one: candidates' times relative to the earliest of
-  // them; the time table
+  // of a segment and the next one: candidates' times, and relative to the earliest
+  // of them; the time table
+  alignas(16) int64_t tq[2][NQ];
   alignas(16) float tqd[2][NQ];
-  alignas(16) float live[2][NQ];   // 1 for a candidate, 0 for padding
   float tbl_t[2][kTblT];
   int64_t tq_min[2], tq_max[2];
   uint64_t k_full[2], k_empty[2], v_full[C::kV], v_empty[C::kV];
@@ -199,50 +199,56 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// The time bias of one pair, bucket by bucket (times too far apart for floats).
-__device__ __noinline__ float time_bias_int(int64_t dt, const float *rt, int sub_bits, int nb_t) {
-  return qc_bias(rt[time_bucket_i64(dt, sub_bits, nb_t)]);
-}
-
-// 16 candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum
-// of |P| over the live ones.  With weights (returned in float32) SiLU is
-// x / (1 + 2^y), y = -x log2 e, good to a few 2^-22; else h (1 + tanh h) with
-// h = x / 2, half the special-function work, its error below P's rounding.  The
-// special-function unit (16 results a cycle and SM) is what bounds the weights'
-// form; every other pair of quotients shares a reciprocal, which trades one of its
-// results for three multiplications.
-template <int D, int NQ, bool WEIGHTS, int MODE>
-__device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8],
-                                      const Smem<D, NQ> &sm, int sb, int c0, float a, float c,
-                                      float c2, float t, int64_t tk, const float *rt, float half,
-                                      int sub_bits, int nb_t, const int64_t *ts, int nq,
-                                      float &wsum) {
+// W candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum
+// of |P| over the first `live` of them.  With weights (returned in float32)
+// SiLU is x / (1 + 2^y), y = -x log2 e, good to a few 2^-22; else h (1 + tanh h)
+// with h = x / 2, half the special-function work, its error below P's rounding.
+// The special-function unit (16 results a cycle and SM) is what bounds this
+// loop with weights; every other pair of quotients shares a reciprocal, which
+// trades one of its results for three multiplications and balances the two.
+template <int D, int NQ, bool WEIGHTS, int MODE, bool ALL, int W>
+__device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W / 2],
+                                        const Smem<D, NQ> &sm, int sb, int c0, float a, float c,
+                                        float c2, float t, int64_t tk, const float *rt, float half,
+                                        int sub_bits, int nb_t, int live, float &wsum) {
   const int sh = 23 - sub_bits;
   const int32_t r0 = fast_r0(sub_bits);
   constexpr float kL = -1.4426950408889634f;
+  const float ay = kL * a, cy = kL * c;
+  float tq[4];
 #pragma unroll
-  for (int e = 0; e < 16; e += 4) {
-    float x[4], pv[4];
-    float4 tq = make_float4(0.f, 0.f, 0.f, 0.f);
-    if constexpr (MODE == kTimeTwo || MODE == kTimeFloat)
-      tq = *reinterpret_cast<const float4 *>(&sm.tqd[sb][c0 + e]);
-    const float tqs[4] = {tq.x, tq.y, tq.z, tq.w};
+  for (int e = 0; e < W; e += 2) {
+    if constexpr (MODE == kTimeTwo || MODE == kTimeFloat) {
+      if ((e & 3) == 0) {
+        const float4 v = *reinterpret_cast<const float4 *>(&sm.tqd[sb][c0 + e]);
+        tq[0] = v.x;
+        tq[1] = v.y;
+        tq[2] = v.z;
+        tq[3] = v.w;
+      }
+    }
+    float x[2], y[2], pv[2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
       const float sv = __uint_as_float(s[e + u]);
       if constexpr (MODE == kTimeOne) {
         x[u] = fmaf(a, sv, c);
+        y[u] = fmaf(ay, sv, cy);
       } else if constexpr (MODE == kTimeTwo) {
-        x[u] = fmaf(a, sv, tqs[u] >= t ? c2 : c);
+        x[u] = fmaf(a, sv, tq[(e & 3) + u] >= t ? c2 : c);
+        y[u] = kL * x[u];
       } else if constexpr (MODE == kTimeFloat) {
-        const int32_t rr = __float_as_int(t + tqs[u]) >> sh;
+        const int32_t rr = __float_as_int(t + tq[(e & 3) + u]) >> sh;
         x[u] = fmaf(a, sv, c) + sm.tbl_t[sb][(rr > r0 ? rr : r0) - r0];
+        y[u] = kL * x[u];
       } else {
-        x[u] = fmaf(a, sv, c) + half * time_bias_int(ts[min(c0 + e + u, nq - 1)] - tk, rt, sub_bits, nb_t);
+        x[u] = fmaf(a, sv, c) +
+               half * qc_bias(rt[time_bucket_i64(sm.tq[sb][c0 + e + u] - tk, sub_bits, nb_t)]);
+        y[u] = kL * x[u];
       }
     }
     if constexpr (WEIGHTS) {
-      if constexpr (MODE == kTimeOne) {
+      if (MODE == kTimeOne && (e & 2) == 0) {
         // one reciprocal for two quotients; logits are held at -42.9, where SiLU
         // is -1e-17, so that the product of the two stays finite
         x[0] = fmaxf(x[0], -42.9f);
@@ -252,22 +258,17 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8]
         pv[0] = x[0] * (r * d1);
         pv[1] = x[1] * (r * d0);
       } else {
-        pv[0] = x[0] * rcp_approx(1.0f + ex2_approx(kL * x[0]));
-        pv[1] = x[1] * rcp_approx(1.0f + ex2_approx(kL * x[1]));
+        pv[0] = x[0] * rcp_approx(1.0f + ex2_approx(y[0]));
+        pv[1] = x[1] * rcp_approx(1.0f + ex2_approx(y[1]));
       }
-      pv[2] = x[2] * rcp_approx(1.0f + ex2_approx(kL * x[2]));
-      pv[3] = x[3] * rcp_approx(1.0f + ex2_approx(kL * x[3]));
-      const float4 live = *reinterpret_cast<const float4 *>(&sm.live[sb][c0 + e]);   // 1 or 0
-      wsum = fmaf(fabsf(pv[0]), live.x, wsum);
-      wsum = fmaf(fabsf(pv[1]), live.y, wsum);
-      wsum = fmaf(fabsf(pv[2]), live.z, wsum);
-      wsum = fmaf(fabsf(pv[3]), live.w, wsum);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (ALL || e + u < live) wsum += fabsf(pv[u]);
     } else {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) pv[u] = fmaf(x[u], tanh_approx(x[u]), x[u]);   // x halved
+      for (int u = 0; u < 2; ++u) pv[u] = fmaf(x[u], tanh_approx(x[u]), x[u]);   // x halved
     }
     pk[e / 2] = pack_bf16x2(pv[0], pv[1]);
-    pk[e / 2 + 1] = pack_bf16x2(pv[2], pv[3]);
   }
 }
 
@@ -623,12 +624,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && warp == 1) {
         // candidates' times, their range, and their distances to the earliest;
         // a padding candidate takes the first one's
-        int64_t lo = INT64_MAX, hi = INT64_MIN, t[NQ / 32];
+        int64_t lo = INT64_MAX, hi = INT64_MIN;
 #pragma unroll
-        for (int i = 0; i < NQ / 32; ++i) {
-          t[i] = p.cand_ts[s.q_row + (i * 32 + lane < s.nq ? i * 32 + lane : 0)];
-          lo = t[i] < lo ? t[i] : lo;
-          hi = t[i] > hi ? t[i] : hi;
+        for (int i = lane; i < NQ; i += 32) {
+          const int64_t t = p.cand_ts[s.q_row + (i < s.nq ? i : 0)];
+          sm.tq[sb][i] = t;
+          lo = t < lo ? t : lo;
+          hi = t > hi ? t : hi;
         }
 #pragma unroll
         for (int m = 16; m; m >>= 1) {
@@ -637,11 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           lo = a < lo ? a : lo;
           hi = b > hi ? b : hi;
         }
-#pragma unroll
-        for (int i = 0; i < NQ / 32; ++i) {
-          sm.tqd[sb][i * 32 + lane] = float(t[i] - lo);
-          sm.live[sb][i * 32 + lane] = i * 32 + lane < s.nq ? 1.0f : 0.0f;
-        }
+        __syncwarp();
+        for (int i = lane; i < NQ; i += 32) sm.tqd[sb][i] = float(sm.tq[sb][i] - lo);
         if (lane == 0) {
           sm.tq_min[sb] = lo;
           sm.tq_max[sb] = hi;
@@ -808,22 +807,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(v4[0], v4[1], v4[2], v4[3]);
           }
         } else {
-#define HSTU_QC_CHUNK(M_)                                                                       \
-  chunk<D, NQ, WEIGHTS, M_>(r, pk, sm, sb, c0, a, c, c2, t, tk, rt, half, p.sub_bits, p.nb_t, \
-                            p.cand_ts + s.q_row, nq, wsum)
+#define HSTU_QC_CHUNK(M_, A_)                                                                     \
+  chunk<D, NQ, WEIGHTS, M_, A_, 16>(r, pk, sm, sb, c0, a, c, c2, t, tk, rt, half, p.sub_bits,     \
+                                    p.nb_t, nq - c0, wsum)
 #pragma unroll 1
           for (int c0 = hf * 64; c0 < min(hf * 64 + 64, nq); c0 += 16) {
             uint32_t r[16], pk[8];
             tmem_ld16(s_col + c0, r);
             tmem_wait_ld(r);
-            if (mode == kTimeOne)
-              HSTU_QC_CHUNK(kTimeOne);
-            else if (mode == kTimeTwo)
-              HSTU_QC_CHUNK(kTimeTwo);
-            else if (mode == kTimeFloat)
-              HSTU_QC_CHUNK(kTimeFloat);
-            else
-              HSTU_QC_CHUNK(kTimeInt);
+            if (mode == kTimeOne) {
+              if (!WEIGHTS || nq - c0 >= 16)
+                HSTU_QC_CHUNK(kTimeOne, true);
+              else
+                HSTU_QC_CHUNK(kTimeOne, false);
+            } else if (mode == kTimeTwo) {
+              HSTU_QC_CHUNK(kTimeTwo, !WEIGHTS);
+            } else if (mode == kTimeFloat) {
+              HSTU_QC_CHUNK(kTimeFloat, !WEIGHTS);
+            } else {
+              HSTU_QC_CHUNK(kTimeInt, !WEIGHTS);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) pk[e] = valid ? pk[e] : 0;
 #pragma unroll
