@@ -178,7 +178,8 @@ hstu_status_t check_attn(const AttnArgs &a, bool have_cache) {
 // One launch's share of the call: sequences [b0, b0 + n_seqs), their key
 // ranges and their places in the scratch buffers.
 struct Share {
-  int plane;                 // candidates per weight partial
+  bool tc;                   // tensor cores
+  int nq, plane;             // candidates per CTA; candidates per weight partial
   int64_t acc_rows, wp;      // rows of `acc` (d_v floats each) and floats of `wpart` it uses
 };
 
@@ -235,27 +236,27 @@ int32_t pick_chunk(const AttnArgs &a, int32_t b0, int32_t n_seqs, int nq, int64_
   return int32_t(best);
 }
 
-// The plans assume a B200's SM count, so that workspace sizes do not depend on the
-// device a call runs on.
-constexpr int64_t kSms = 148;
-
 // Fills the table of one launch.  acc_row, wp: first free places of the scratch.
-// False when its counters do not fit.
-bool make_share(const AttnArgs &a, int32_t b0, int64_t acc_row, int64_t wp, QcAttnParams &p,
+void make_share(const AttnArgs &a, int32_t b0, int64_t acc_row, int64_t wp, QcAttnParams &p,
                 Share &s) {
   const hstu_attn_params_t &ap = *a.p;
   const int64_t H = ap.num_heads;
   p.n_seqs = std::min(kQcMaxSeqs, ap.batch - b0);
-  const bool tc = ap.dtype == HSTU_BF16 && ap.impl == HSTU_IMPL_AUTO && ap.d_qk == ap.d_v &&
-                  (ap.d_qk == 64 || ap.d_qk == 128);
-  int64_t most = 0;   // candidates of one sequence
-  for (int32_t b = b0; b < b0 + p.n_seqs; ++b) most = std::max(most, a.coff[b + 1] - a.coff[b]);
-  // tensor cores: 64 candidates per CTA while no sequence has more
-  p.nq = !tc ? 0 : most <= 64 ? 64 : 128;
-  s.plane = tc ? 64 : kQcSimtQueries;
-  if (!tc) p.chunk = pick_chunk(a, b0, p.n_seqs, kQcSimtQueries, 148 * 4, 1);
+  s.tc = ap.dtype == HSTU_BF16 && ap.impl == HSTU_IMPL_AUTO && ap.d_qk == ap.d_v &&
+         (ap.d_qk == 64 || ap.d_qk == 128);
+  if (s.tc) {
+    // 64 candidates per CTA while no sequence has more
+    int64_t most = 0;
+    for (int32_t b = b0; b < b0 + p.n_seqs; ++b) most = std::max(most, a.coff[b + 1] - a.coff[b]);
+    s.nq = most <= 64 ? 64 : 128;
+    s.plane = 64;
+    p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148, 3);
+  } else {
+    s.nq = s.plane = kQcSimtQueries;
+    p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148 * 4, 1);
+  }
   s.acc_rows = s.wp = 0;
-  int64_t items = 0, units = 0, fin = 0, wrow = 0;
+  int64_t items = 0, fin = 0, wrow = 0;
   for (int32_t i = 0; i < p.n_seqs; ++i) {
     const int32_t b = b0 + i;
     QcAttnSeq &q = p.seqs[i];
@@ -264,23 +265,17 @@ bool make_share(const AttnArgs &a, int32_t b0, int64_t acc_row, int64_t wp, QcAt
     q.len = int32_t(a.lens[b]);
     q.n = int32_t(a.coff[b + 1] - a.coff[b]);
     q.pos = a.pos ? a.pos[b] : 0;
+    q.item0 = int32_t(items);
     q.fin0 = int32_t(fin);
     q.wrow0 = wrow;
     q.acc0 = acc_row + s.acc_rows;
     q.wp0 = wp + s.wp;
     const int32_t tiles = (q.len + kQcKeyTile - 1) / kQcKeyTile;
-    if (tc) {
-      q.u0 = int32_t(std::min<int64_t>(units, INT32_MAX));
-      units += H * ((q.n + p.nq - 1) / p.nq) * (tiles + 1);
+    q.splits = std::max(1, (tiles + p.chunk - 1) / p.chunk);
+    items += int64_t((q.n + s.nq - 1) / s.nq) * q.splits;
+    if (q.splits > 1) {
       fin += q.n * H;
-    } else {
-      q.item0 = int32_t(items);
-      q.splits = std::max(1, (tiles + p.chunk - 1) / p.chunk);
-      items += int64_t((q.n + kQcSimtQueries - 1) / kQcSimtQueries) * q.splits;
-      if (q.splits > 1) {
-        fin += q.n * H;
-        s.acc_rows += int64_t(q.splits) * q.n * H;
-      }
+      s.acc_rows += int64_t(q.splits) * q.n * H;
     }
     if (a.weight) {
       wrow += q.len;
@@ -290,22 +285,11 @@ bool make_share(const AttnArgs &a, int32_t b0, int64_t acc_row, int64_t wp, QcAt
   p.items = int32_t(items);
   p.fin_rows = int32_t(fin);
   p.weight_rows = wrow;
-  if (tc) {
-    // every CTA takes the same number of units, one CTA per SM; a CTA leaves at
-    // most two partial outputs (its first segment's and its last's)
-    p.units = int32_t(units);
-    p.per_cta = int32_t(std::max<int64_t>(1, (units + kSms - 1) / kSms));
-    p.ctas = int32_t((units + p.per_cta - 1) / p.per_cta);
-    p.acc_rows = int32_t(std::min<int64_t>(p.nq, most));
-    s.acc_rows = 2 * int64_t(p.ctas) * p.acc_rows;
-  }
-  return units <= INT32_MAX && items * H <= INT32_MAX;
 }
 
 // Workspace: error word, partial outputs, weight partials.
 struct AttnWs {
   size_t acc, wpart, total;
-  bool ok;   // every launch's counters fit
 };
 AttnWs attn_layout(const AttnArgs &a) {
   AttnArgs shape = a;
@@ -314,13 +298,12 @@ AttnWs attn_layout(const AttnArgs &a) {
   QcAttnParams p{};
   Share s{};
   int64_t rows = 0, wp = 0;
-  AttnWs w{};
-  w.ok = true;
   for (int32_t b0 = 0; b0 < a.p->batch; b0 += kQcMaxSeqs) {
-    w.ok = make_share(shape, b0, rows, wp, p, s) && w.ok;
+    make_share(shape, b0, rows, wp, p, s);
     rows += s.acc_rows;
     wp += s.wp;
   }
+  AttnWs w{};
   w.acc = 256;
   w.wpart = align256(w.acc + size_t(rows) * a.p->d_v * sizeof(float));
   w.total = align256(w.wpart + size_t(wp) * sizeof(float));
@@ -347,7 +330,7 @@ hstu_status_t run_attn(const AttnArgs &a, const int64_t *cand_ts, const void *q,
   p.cand_ts = cand_ts;
   p.rab_p = rab_pos;
   p.rab_t = rab_time;
-  float *const acc = reinterpret_cast<float *>(ws + w.acc);
+  p.acc = reinterpret_cast<float *>(ws + w.acc);
   p.wpart = reinterpret_cast<float *>(ws + w.wpart);
   p.wait = WaitCtl{reinterpret_cast<uint32_t *>(ws), wait_limit_ns()};
   p.alpha = ap.alpha;
@@ -367,11 +350,8 @@ hstu_status_t run_attn(const AttnArgs &a, const int64_t *cand_ts, const void *q,
     make_share(a, b0, rows, wp, p, s);
     rows += s.acc_rows;
     wp += s.wp;
-    if (p.nq ? p.units > 0 : p.items > 0) {
-      // the launch's own part of the partial outputs (tensor cores number them
-      // from 0, the CUDA cores carry acc0 in their table)
-      p.acc = acc + (p.nq ? (rows - s.acc_rows) * ap.d_v : 0);
-      const cudaError_t e = p.nq ? launch_qcache_attn_tc(p, st)
+    if (p.items > 0) {
+      const cudaError_t e = s.tc ? launch_qcache_attn_tc(p, s.nq, st)
                                  : launch_qcache_attn_simt(p, bf16, st);
       if (e != cudaSuccess) return HSTU_ERR_CUDA;
       p.clear_err = false;
@@ -605,9 +585,7 @@ hstu_status_t hstu_attn_candidates_qcache_workspace_size(const hstu_attn_params_
              update_weight != 0};
   hstu_status_t st = check_attn(a, false);
   if (st != HSTU_OK) return st;
-  const AttnWs w = attn_layout(a);
-  if (!w.ok) return HSTU_ERR_UNSUPPORTED;
-  *bytes = w.total;
+  *bytes = attn_layout(a).total;
   return HSTU_OK;
 }
 
@@ -630,7 +608,6 @@ hstu_status_t hstu_attn_fwd_candidates_qcache(
                 !aligned(cand_timestamps_dev, 8) || !aligned(rab_pos, 4) || !aligned(rab_time, 4)))
     return HSTU_ERR_INVALID_ARG;
   const AttnWs w = attn_layout(a);
-  if (!w.ok) return HSTU_ERR_UNSUPPORTED;
   if (!workspace_ok(workspace, workspace_bytes, w.total)) return HSTU_ERR_WORKSPACE;
   return run_attn(a, cand_timestamps_dev, q, k, v, rab_pos, rab_time, weight_decay, out, w,
                   static_cast<uint8_t *>(workspace), true, static_cast<cudaStream_t>(stream));
@@ -646,9 +623,7 @@ hstu_status_t hstu_layer_candidates_qcache_workspace_size(const hstu_layer_param
   hstu_attn_params_t ap;
   hstu_status_t st = check_layer(params, a, ap, false);
   if (st != HSTU_OK) return st;
-  const LayerQcWs w = layer_layout(a);
-  if (!w.attn.ok) return HSTU_ERR_UNSUPPORTED;
-  *bytes = w.total;
+  *bytes = layer_layout(a).total;
   return HSTU_OK;
 }
 
@@ -672,7 +647,6 @@ hstu_status_t hstu_layer_fwd_candidates_qcache(
     return HSTU_ERR_INVALID_ARG;
   if (proj_out && !aligned(proj_out, 16)) return HSTU_ERR_INVALID_ARG;
   const LayerQcWs lw = layer_layout(a);
-  if (!lw.attn.ok) return HSTU_ERR_UNSUPPORTED;
   if (!workspace_ok(workspace, workspace_bytes, lw.total)) return HSTU_ERR_WORKSPACE;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);

@@ -224,38 +224,18 @@ __global__ void __launch_bounds__(kFinThreads)
   if (int(blockIdx.x) < out_blocks) {
     const int row = int(blockIdx.x) * (kFinThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    int64_t first = 0;   // the first partial sum lies that much further on
     if (row >= p.fin_rows) return;
     const int si = qc_find(p.seqs, p.n_seqs, row, [](const QcAttnSeq &s) { return s.fin0; });
     const QcAttnSeq &sq = p.seqs[si];
-    const int x = row - sq.fin0, i = x / H, h = x - i * H;
-    // where the row's partial sums lie: `parts` of them, `step` floats apart
-    const float *a;
-    int64_t step;
-    int parts;
-    if (p.nq) {
-      // tensor cores: the CTAs that share the item's units, each with two places;
-      // the item is the first segment of all but the first of them
-      const int tiles = (sq.len + kQcKeyTile - 1) / kQcKeyTile + 1;
-      const int per_seq = (sq.n + p.nq - 1) / p.nq, qt = i / p.nq;
-      const int u = sq.u0 + (h * per_seq + qt) * tiles;
-      const int c0 = u / p.per_cta, c1 = (u + tiles - 1) / p.per_cta;
-      parts = c1 - c0 + 1;
-      if (parts == 1) return;   // written by its CTA
-      step = int64_t(2) * p.acc_rows * dv;
-      a = p.acc + (int64_t(2 * c0) * p.acc_rows + i - qt * p.nq) * dv;
-      first = u > c0 * p.per_cta ? int64_t(p.acc_rows) * dv : 0;
-    } else {
-      parts = sq.splits;
-      step = int64_t(sq.n) * H * dv;
-      a = p.acc + (sq.acc0 + x) * dv;
-    }
-    T *o = static_cast<T *>(p.out) + (sq.q0 + i) * p.o_rs + int64_t(h) * dv;
+    const int x = row - sq.fin0;                       // i H + h
+    const int64_t step = int64_t(sq.n) * H * dv;
+    const float *a = p.acc + (sq.acc0 + x) * dv;
+    T *o = static_cast<T *>(p.out) + (sq.q0 + x / H) * p.o_rs + int64_t(x % H) * dv;
     // four features per lane (d_v is a multiple of 32); eight key ranges' loads in flight
     for (int e = lane * 4; e < dv; e += 128) {
-      float4 s = *reinterpret_cast<const float4 *>(a + first + e);
-      int k = 1;
-      for (; k + 8 <= parts; k += 8) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      int k = 0;
+      for (; k + 8 <= sq.splits; k += 8) {
         float4 v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
@@ -268,7 +248,7 @@ __global__ void __launch_bounds__(kFinThreads)
           s.w += v[u].w;
         }
       }
-      for (; k < parts; ++k) {
+      for (; k < sq.splits; ++k) {
         const float4 v = *reinterpret_cast<const float4 *>(a + k * step + e);
         s.x += v.x;
         s.y += v.y;

@@ -5,14 +5,8 @@
 //   x_ij = alpha <q_i, k_j> + rab_pos[P_b - pos_j] + rab_time[tb(t_i - t_j)]
 //   w_j  <- decay w_j + c sum_{i, h} |SiLU(x_ij)|
 //
-// Work is cut into units: a 128-key tile of one (sequence, head, NQ candidates),
-// those items one behind the other.  Every CTA (one per SM) takes the same number
-// of consecutive units, so it walks one or more segments, each a part of an item
-// or all of it; the roles below run on from one segment into the next (a CTA of
-// its own per item cost about 20,000 cycles of start and end, as much as 9 tiles).
-// A segment that is not its whole item leaves a partial O, which the summing pass
-// adds up in order.  Both products are turned so that a thread owns a key, not a
-// candidate:
+// One CTA = one (sequence, head, NQ candidates, range of 128-key tiles); both
+// products are turned so that a thread owns a key, not a candidate:
 //   S^T = K Q^T   [128 keys x NQ],   O^T += V^T P^T   [d x NQ]
 // Why: everything a key brings along is then one value per thread.  All
 // candidates of a call sit at one position and mostly share one time, so the
@@ -32,8 +26,8 @@
 //                (lane = key), from where the MMA takes it;
 //   and as many for values the same way, V to shared memory in the 128-byte
 //                swizzle.
-// The candidates' own pairs are one more tile, the first of an item: its keys are
-// the candidates and only P's diagonal is kept.
+// The candidates' own pairs are one more tile, the first of the range that has
+// them: its keys are the candidates and only P's diagonal is kept.
 // Shared-memory traffic is what bounds the loop once the decoding keeps up (an
 // MMA with both operands there and N = 128 takes all of its 128 bytes a cycle):
 // keeping K out of it saves 32 KB written and 32 KB read of about 260 KB per tile
@@ -81,12 +75,12 @@ struct Cfg {
   static_assert(kK + 2 * (D / 2) <= 512, "tensor memory");
 };
 
-// How the time bias of 32 keys of a tile is found.  kTimeOne: the same for all
+// How the time bias of a tile's keys is found.  kTimeOne: the same for all
 // candidates, part of c.  kTimeTwo: each key meets one or two neighbouring
 // buckets, c below and c2 from candidate time t on (relative to the earliest).
 // kTimeFloat: by the float-exponent table, t = earliest candidate - key.
-// kTimeInt: bucket by bucket in 64 bits.  kOwn: the tile of the candidates' own pairs.
-enum : int { kTimeOne = 0, kTimeTwo = 1, kTimeFloat = 2, kTimeInt = 3, kOwn = 4 };
+// kTimeInt: bucket by bucket in 64 bits.
+enum : int { kTimeOne = 0, kTimeTwo = 1, kTimeFloat = 2, kTimeInt = 3 };
 // Tiles of KeyBias in flight: a multiple of the 3 warps that fill them and of
 // the 2 warpgroups that take them, so a slot always has the same two parties and
 // none of them can be a whole round of its barriers ahead of the other (a parity
@@ -94,13 +88,13 @@ enum : int { kTimeOne = 0, kTimeTwo = 1, kTimeFloat = 2, kTimeInt = 3, kOwn = 4 
 constexpr int kBias = 6;
 struct KeyBias {
   float c[kTile], c2[kTile], t[kTile];
-  int mode[4];   // of 32 keys each
+  int mode;
 };
 
 template <int D, int NQ>
 struct Smem {
   using C = Cfg<D, NQ>;
-  alignas(1024) uint8_t q[2][NQ * D * 2];       // of a segment and the next one
+  alignas(1024) uint8_t q[NQ * D * 2];
   alignas(1024) uint8_t v[C::kV][C::kTileBytes];
   alignas(1024) uint8_t p[2][C::kPBytes];       // behind v: see the D = 64 note at issue_o
   alignas(16) uint8_t k_codes[C::kStages][C::kCodeBytes];
@@ -108,46 +102,39 @@ struct Smem {
   alignas(16) uint8_t k_scales[C::kStages][C::kScaleBytes];
   alignas(16) uint8_t v_scales[C::kStages][C::kScaleBytes];
   KeyBias bias[kBias];
-  // of a segment and the next one: candidates' times, and relative to the earliest
-  // of them; the time table
-  alignas(16) int64_t tq[2][NQ];
-  alignas(16) float tqd[2][NQ];
-  float tbl_t[2][kTblT];
-  int64_t tq_min[2], tq_max[2];
+  alignas(16) int64_t tq[NQ];     // candidates' times
+  alignas(16) float tqd[NQ];      // and relative to the earliest of them
+  float tbl_t[kTblT];
+  int64_t tq_min, tq_max;
   uint64_t k_full[2], k_empty[2], v_full[C::kV], v_empty[C::kV];
   uint64_t s_full[3];             // with three slots a warpgroup takes every other round of one:
                                   // the commits are in order, so the round between is over by then
   uint64_t p_full[2], p_empty[2];
   uint64_t bias_full[kBias], bias_empty[kBias];
-  uint64_t q_full[2], o_full, o_empty[2], drain;
+  uint64_t q_full, o_full, drain;
   uint32_t tmem_base;
   uint32_t abort;                 // a wait of this CTA ran out
+  static_assert(sizeof(p) >= NQ * D * sizeof(float), "O goes through the P tiles at the end");
 };
 
 // Bounded wait.  The CTA's own flag, not the error word of the workspace, tells
 // its other roles to leave: the word may hold anything until this call's first
 // CTA has cleared it.
-// The roles' loops run side by side on every scheduler and together have to stay
-// in the instruction cache: what a loop seldom needs (here, finding a segment) is
-// kept out of line.
-__device__ __noinline__ bool wait_cta_slow(uint64_t *bar, uint32_t parity, uint32_t *abort,
-                                           uint32_t *err, uint64_t limit_ns) {
+__device__ __forceinline__ bool wait_cta(uint64_t *bar, uint32_t parity, uint32_t *abort,
+                                         const WaitCtl &w) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile uint32_t *>(abort) != 0) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
+    if (globaltimer_ns() - t0 > w.limit_ns) {
       *reinterpret_cast<volatile uint32_t *>(abort) = 1;
-      record_error(err, kDevErrTimeout);
+      record_error(w.err, kDevErrTimeout);
       return false;
     }
   }
-}
-__device__ __forceinline__ bool wait_cta(uint64_t *bar, uint32_t parity, uint32_t *abort,
-                                         const WaitCtl &w) {
-  return mbar_try_wait(bar, parity) || wait_cta_slow(bar, parity, abort, w.err, w.limit_ns);
 }
 __device__ __forceinline__ bool wait_cta_warp(uint64_t *bar, uint32_t parity, uint32_t *abort,
                                               const WaitCtl &w) {
@@ -179,14 +166,21 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t *v) {
                : "memory");
 }
 // 8 values of a bf16 row.
-__device__ __noinline__ uint4 load_row8_scalar(const __nv_bfloat16 *src) {
+__device__ __forceinline__ uint4 load_row8(const __nv_bfloat16 *src, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4 *>(src);
   uint32_t e[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) e[i] = reinterpret_cast<const uint16_t *>(src)[i];
   return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
-__device__ __forceinline__ uint4 load_row8(const __nv_bfloat16 *src, bool vec) {
-  return vec ? *reinterpret_cast<const uint4 *>(src) : load_row8_scalar(src);
+__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float s) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+    s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
+  }
+  return s;
 }
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -208,8 +202,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // trades one of its results for three multiplications and balances the two.
 template <int D, int NQ, bool WEIGHTS, int MODE, bool ALL, int W>
 __device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W / 2],
-                                        const Smem<D, NQ> &sm, int sb, int c0, float a, float c,
-                                        float c2, float t, int64_t tk, const float *rt, float half,
+                                        const Smem<D, NQ> &sm, int c0, float a, float c, float c2,
+                                        float t, int64_t tk, const float *rt, float half,
                                         int sub_bits, int nb_t, int live, float &wsum) {
   const int sh = 23 - sub_bits;
   const int32_t r0 = fast_r0(sub_bits);
@@ -220,7 +214,7 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W /
   for (int e = 0; e < W; e += 2) {
     if constexpr (MODE == kTimeTwo || MODE == kTimeFloat) {
       if ((e & 3) == 0) {
-        const float4 v = *reinterpret_cast<const float4 *>(&sm.tqd[sb][c0 + e]);
+        const float4 v = *reinterpret_cast<const float4 *>(&sm.tqd[c0 + e]);
         tq[0] = v.x;
         tq[1] = v.y;
         tq[2] = v.z;
@@ -239,11 +233,11 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W /
         y[u] = kL * x[u];
       } else if constexpr (MODE == kTimeFloat) {
         const int32_t rr = __float_as_int(t + tq[(e & 3) + u]) >> sh;
-        x[u] = fmaf(a, sv, c) + sm.tbl_t[sb][(rr > r0 ? rr : r0) - r0];
+        x[u] = fmaf(a, sv, c) + sm.tbl_t[(rr > r0 ? rr : r0) - r0];
         y[u] = kL * x[u];
       } else {
         x[u] = fmaf(a, sv, c) +
-               half * qc_bias(rt[time_bucket_i64(sm.tq[sb][c0 + e + u] - tk, sub_bits, nb_t)]);
+               half * qc_bias(rt[time_bucket_i64(sm.tq[c0 + e + u] - tk, sub_bits, nb_t)]);
         y[u] = kL * x[u];
       }
     }
@@ -272,53 +266,37 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W /
   }
 }
 
-// A run of units of one item.
-struct Segment {
-  int seq, qtile, h;
-  int t, n, per;       // first unit in the item, units, units of the whole item
-  int nq;              // candidates
-  int64_t q_row;       // first candidate row
-};
-// The segment at unit u of a CTA whose units end at `end`.
-template <int NQ>
-__device__ __noinline__ Segment segment_at(const QcAttnParams &p, int u, int end) {
-  Segment g;
-  g.seq = qc_find(p.seqs, p.n_seqs, u, [](const QcAttnSeq &s) { return s.u0; });
-  const QcAttnSeq &s = p.seqs[g.seq];
-  const int x = u - s.u0;
-  g.per = (s.len + kTile - 1) / kTile + 1;
-  const int item = x / g.per, tiles = (s.n + NQ - 1) / NQ;
-  g.t = x - item * g.per;
-  g.n = min(g.per - g.t, end - u);
-  g.h = item / tiles;
-  g.qtile = item - g.h * tiles;
-  g.nq = min(NQ, s.n - g.qtile * NQ);
-  g.q_row = s.q0 + g.qtile * NQ;
-  return g;
-}
-
 // The decoding warps of K (IS_V false) or V: tiles of codes from the cache into
 // stages (cp.async), from there to bf16, K to tensor memory, V to shared memory.
-//   K: thread = key and half of the row (or all of it), since a warp writes its
-//   own 32 lanes of tensor memory; a row's chunks are permuted in the stage so
-//   that 8 lanes that read together touch every bank once.
+//   K: thread = key and half of the row (or all of it), since a warp writes its own 32 lanes of
+//   tensor memory; a row's chunks are permuted in the stage so that 8 lanes that
+//   read together touch every bank once.
 //   V: a warp takes 8 rows x 4 groups (16 x 2 at D = 64), 512 bytes in one piece;
 //   eight lanes that store together hold 4 rows x 2 neighbouring groups, whose
 //   16-byte chunks lie in eight different banks under the swizzle.
 template <int D, int NQ, bool IS_V>
-__device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> &sm, int u_first,
-                                             int u_end, uint32_t tmem, int dw, int lane) {
+__device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> &sm,
+                                             const QcItem &it, const QcAttnSeq &sq, int h,
+                                             int64_t q_row, int nq, uint32_t tmem, int dw,
+                                             int lane) {
   using C = Cfg<D, NQ>;
   constexpr int G = C::kG, kPer = C::kPer, kDecThreads = C::kDecThreads;
   constexpr int kStep = kDecThreads / G;         // V: rows between a thread's groups
   const QCacheView &cv = p.cache;
   const int dt = dw * 32 + lane, hx = dw >> 2;
+  const int n_tiles = it.t1 - it.t0, self = it.split == 0 ? 1 : 0, n_all = n_tiles + self;
   const int row = !IS_V    ? (dw & 3) * 32 + lane
                   : G == 4 ? dw * 8 + ((lane >> 4) << 2) + ((lane >> 1) & 3)
                            : dw * 16 + (lane >> 1);
   const int g = !IS_V ? hx * kPer : G == 4 ? ((lane >> 3) & 1) * 2 + (lane & 1) : lane & 1;
+  const int64_t at = (int64_t(h) * cv.rows + sq.row + int64_t(it.t0) * kTile + row) * G + g;
   const uint8_t *const src0 = reinterpret_cast<const uint8_t *>(IS_V ? cv.v_codes : cv.k_codes);
   const uint8_t *const psrc0 = reinterpret_cast<const uint8_t *>(IS_V ? cv.v_scales : cv.k_scales);
+  const uint8_t *src = src0 + at * 16;
+  // parameters travel 4 bytes and more at a time: K the thread's groups (a single
+  // one with its neighbour), V a whole row through the lane of its first group
+  const uint8_t *psrc = psrc0 + (at - (!IS_V && kPer == 1 ? (g & 1) : 0)) * 2;
+  int32_t left = sq.len - it.t0 * kTile - row;   // the sequence's rows from this one on
   uint8_t *const codes = IS_V ? sm.v_codes[0] : sm.k_codes[0];
   uint8_t *const scales = IS_V ? sm.v_scales[0] : sm.k_scales[0];
   uint32_t code_at[kPer];   // where the thread's codes lie in a stage
@@ -329,35 +307,10 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
                           : row * 32 + (((g + x) ^ ((row >> 2) & 1)) << 4);
   const uint32_t scale_at = IS_V ? row * 2 * G : (hx * kTile + row) * C::kParBytes;
   const uint32_t code_dst = smem_u32(codes), scale_dst = smem_u32(scales) + scale_at;
-
-  // ---- copies run ahead of the decoding, over the same units ----
-  int cu = u_first, c_left = 0;                  // next unit, units left of its segment
-  const uint8_t *src = src0, *psrc = psrc0;
-  int32_t rows_left = 0;                         // the sequence's rows from this thread's on
-  auto copy_next = [&](int st) {
-    if (c_left == 0 && cu < u_end) {
-      const Segment s = segment_at<NQ>(p, cu, u_end);
-      c_left = s.n;
-      int tile = s.t - 1;
-      if (s.t == 0) {   // the own pairs are not in the cache
-        tile = 0;
-        ++cu;
-        --c_left;
-        if (c_left == 0) return false;
-      }
-      const QcAttnSeq &sq = p.seqs[s.seq];
-      const int64_t at = (int64_t(s.h) * cv.rows + sq.row + int64_t(tile) * kTile + row) * G + g;
-      src = src0 + at * 16;
-      // parameters travel 4 bytes and more at a time: K the thread's groups (a
-      // single one with its neighbour), V a whole row through the lane of its
-      // first group
-      psrc = psrc0 + (at - (!IS_V && kPer == 1 ? (g & 1) : 0)) * 2;
-      rows_left = sq.len - tile * kTile - row;
-    }
-    if (c_left == 0) return true;   // no unit left
+  auto copy = [&](int st) {   // the next tile of the cache into stage st
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
-      const bool ok = (IS_V ? x * kStep : 0) < rows_left;
+      const bool ok = (IS_V ? x * kStep : 0) < left;
       cp_async<16>(code_dst + st * C::kCodeBytes + code_at[x],
                    ok ? src + (IS_V ? x * kDecThreads : x) * 16 : src0, ok);
       if (IS_V && g == 0)
@@ -365,23 +318,17 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
                         ok ? psrc + x * kDecThreads * 2 : psrc0, ok);
     }
     if (!IS_V)
-      cp_async<C::kParBytes>(scale_dst + st * C::kScaleBytes, 0 < rows_left ? psrc : psrc0,
-                             0 < rows_left);
+      cp_async<C::kParBytes>(scale_dst + st * C::kScaleBytes, 0 < left ? psrc : psrc0, 0 < left);
     src += kTile * G * 16;
     psrc += kTile * G * 2;
-    rows_left -= kTile;
-    ++cu;
-    --c_left;
-    return true;
+    left -= kTile;
   };
-  auto copy = [&](int st) {   // the next cached tile into stage st, one group of copies
-    while (!copy_next(st)) {
-    }
-    cp_async_commit();
-  };
+  int m_copy = 0;
 #pragma unroll 1
-  for (int st = 0; st < C::kStages; ++st) copy(st);
-
+  for (; m_copy < C::kStages; ++m_copy) {
+    if (m_copy < n_tiles) copy(m_copy);
+    cp_async_commit();
+  }
   uint64_t *const full = IS_V ? sm.v_full : sm.k_full;
   uint64_t *const empty = IS_V ? sm.v_empty : sm.k_empty;
   uint32_t off[4];   // V: where the group's chunks go in a tile
@@ -400,71 +347,7 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
       tmem_st16(k_tile + buf * (D / 2) + x * 16, o);
     }
   };
-  int st = 0, seg_end = u_first;
-#pragma unroll 1
-  for (int u = u_first, n = 0; u < u_end; ++u, ++n) {
-    const int buf = n & 1;
-    Segment s;
-    bool own = false;
-    if (u == seg_end) {
-      s = segment_at<NQ>(p, u, u_end);
-      seg_end = u + s.n;
-      own = s.t == 0;
-    }
-    uint4 code[kPer];
-    uint32_t par[kPer];
-    if (!own) {
-      cp_async_wait<C::kStages - 1>();
-      if (IS_V) __syncwarp();   // the row's parameters came through another lane of this warp
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        code[x] = *reinterpret_cast<const uint4 *>(codes + st * C::kCodeBytes + code_at[x]);
-        par[x] = *reinterpret_cast<const uint16_t *>(
-            scales + st * C::kScaleBytes + scale_at +
-            (IS_V ? x * kStep * 2 * G + g * 2 : kPer == 1 ? (g & 1) * 2 : x * 2));
-      }
-      __syncwarp();   // the warp has read the stage
-      copy(st);
-      st = st == C::kStages - 1 ? 0 : st + 1;
-    }
-    if (n >= 2 && !wait_cta_warp(&empty[buf], ((n >> 1) - 1) & 1, &sm.abort, p.wait)) break;
-    if (!IS_V) tc_fence_after();
-    if (own) {   // the candidates' own keys or values, bf16 already
-      const __nv_bfloat16 *src_row = static_cast<const __nv_bfloat16 *>(IS_V ? p.v : p.k) +
-                                     s.q_row * (IS_V ? p.v_rs : p.k_rs) + s.h * D + g * 32;
-#pragma unroll 1
-      for (int x = 0; x < kPer; ++x) {
-        const int i = row + (IS_V ? x * kStep : 0);
-        uint32_t o[16];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (i < s.nq)
-            w = load_row8(src_row + i * (IS_V ? p.v_rs : p.k_rs) + (IS_V ? 0 : x * 32) + e * 8,
-                          p.vec);
-          o[4 * e] = w.x;
-          o[4 * e + 1] = w.y;
-          o[4 * e + 2] = w.z;
-          o[4 * e + 3] = w.w;
-        }
-        put(buf, x, o);
-      }
-    } else {
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        uint32_t zz, ss, o[16];
-        q4_group(par[x], zz, ss);
-        const uint32_t w[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t v4[4];
-          q4_decode_bf16(w[e], zz, ss, v4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[4 * e + i] = v4[i];
-        }
-        put(buf, x, o);
-      }
-    }
+  auto done = [&](int buf) {
     if constexpr (IS_V) {
       fence_proxy_async_smem();
     } else {
@@ -472,6 +355,67 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
       tc_fence_before();
     }
     mbar_arrive(&full[buf]);
+  };
+  if (self) {   // tile 0: the candidates' own keys or values, bf16 already
+    const __nv_bfloat16 *own = static_cast<const __nv_bfloat16 *>(IS_V ? p.v : p.k) +
+                               q_row * (IS_V ? p.v_rs : p.k_rs) + h * D + g * 32;
+#pragma unroll 1
+    for (int x = 0; x < kPer; ++x) {
+      const int i = row + (IS_V ? x * kStep : 0);
+      uint32_t o[16];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (i < nq)
+          w = load_row8(own + i * (IS_V ? p.v_rs : p.k_rs) + (IS_V ? 0 : x * 32) + e * 8, p.vec);
+        o[4 * e] = w.x;
+        o[4 * e + 1] = w.y;
+        o[4 * e + 2] = w.z;
+        o[4 * e + 3] = w.w;
+      }
+      put(0, x, o);
+    }
+    done(0);
+  }
+  int st = 0;
+#pragma unroll 1
+  for (int n = self; n < n_all; ++n) {
+    const int buf = n & 1;
+    cp_async_wait<C::kStages - 1>();
+    if (IS_V) __syncwarp();   // the row's parameters came through another lane of this warp
+    uint4 code[kPer];
+    uint32_t par[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      code[x] = *reinterpret_cast<const uint4 *>(codes + st * C::kCodeBytes + code_at[x]);
+      par[x] = *reinterpret_cast<const uint16_t *>(
+          scales + st * C::kScaleBytes + scale_at +
+          (IS_V ? x * kStep * 2 * G + g * 2 : kPer == 1 ? (g & 1) * 2 : x * 2));
+    }
+    __syncwarp();   // the warp has read the stage
+    if (m_copy < n_tiles) copy(st);
+    cp_async_commit();
+    ++m_copy;
+    st = st == C::kStages - 1 ? 0 : st + 1;
+    if (n >= 2 &&
+        !wait_cta_warp(&empty[buf], ((n >> 1) - 1) & 1, &sm.abort, p.wait))
+      break;
+    if (!IS_V) tc_fence_after();
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      uint32_t zz, ss, o[16];
+      q4_group(par[x], zz, ss);
+      const uint32_t w[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t v4[4];
+        q4_decode_bf16(w[e], zz, ss, v4);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[4 * e + u] = v4[u];
+      }
+      put(buf, x, o);
+    }
+    done(buf);
   }
   cp_async_wait<0>();
 }
@@ -486,26 +430,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const QCacheView &cv = p.cache;
   const int H = cv.heads;
+  const int item = int(blockIdx.x) / H, h = int(blockIdx.x) - item * H;
   // The first CTA clears the error word.  A CTA records one only after a wait
   // of at least a microsecond, long after the first CTA has started.
   if (p.clear_err && blockIdx.x == 0 && tid < 4) p.wait.err[tid] = 0;
-  const int u_first = int(blockIdx.x) * p.per_cta, u_end = min(u_first + p.per_cta, p.units);
+  const QcItem it = qc_item(p, item);
+  const QcAttnSeq sq = p.seqs[it.seq];
+  const int i0 = it.qtile * NQ, nq = min(NQ, sq.n - i0);
+  const int64_t q_row = sq.q0 + i0;
+  const int n_tiles = it.t1 - it.t0;
+  const float *rp = p.rab_p + (p.rab_per_head ? int64_t(h) * p.nb_p : 0);
+  const float *rt = p.rab_t + (p.rab_per_head ? int64_t(h) * p.nb_t : 0);
   const float half = WEIGHTS ? 1.0f : 0.5f;     // the tanh form works on x / 2
   constexpr uint32_t kQHalf = NQ * 128;         // bytes of one 64-column box of Q
-  constexpr int kElemThreads = 32 * C::kElemWarps;
+
+  const int self = it.split == 0 ? 1 : 0;        // tile 0 is the candidates' own
+  const int n_all = n_tiles + self;
 
   if (tid == 64) {
+    mbar_init(&sm.q_full, 32 * C::kElemWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.k_full[i], C::kDecThreads);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], C::kDecThreads);
       mbar_init(&sm.v_empty[i], 1);
-      mbar_init(&sm.p_full[i], 128 * C::kHalves);
-      mbar_init(&sm.p_empty[i], 1);
-      mbar_init(&sm.q_full[i], 96);
-      mbar_init(&sm.o_empty[i], kElemThreads);
     }
     for (int i = 0; i < 3; ++i) mbar_init(&sm.s_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.p_full[i], 128 * C::kHalves);
+      mbar_init(&sm.p_empty[i], 1);
+    }
     for (int i = 0; i < kBias; ++i) {
       mbar_init(&sm.bias_full[i], 32);
       mbar_init(&sm.bias_empty[i], 4 * C::kHalves);
@@ -524,111 +478,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  if (warp == 0) {
-    // ===================== MMA issuer =====================
-    if (elect_one()) {
-      constexpr uint32_t idesc_s = idesc_bf16(kTile, NQ, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16(128, NQ, true, true);
-      const int n_all = u_end - u_first;
-      int ns = 0, no = 0, s_slot = 0;            // next S^T, next O^T; ns % kS
-      int s_left = 0, o_left = 0;                // units left of their segments
-      int s_seg = -1, o_seg = -1;                // their segments' numbers
-      bool s_new = false, o_new = false;         // the first of its segment
-      bool ok = true;
-      uint32_t idle = 0;
-      uint64_t t0 = 0;
-      while (ok && no < n_all) {
-        if (s_left == 0 && ns < n_all) {
-          s_left = segment_at<NQ>(p, u_first + ns, u_end).n;
-          ++s_seg;
-          s_new = true;
-        }
-        if (o_left == 0) {
-          o_left = segment_at<NQ>(p, u_first + no, u_end).n;
-          ++o_seg;
-          o_new = true;
-        }
-        // S^T first: the warpgroup that takes it may be waiting, and its columns
-        // are free once P of the tile that had them is there
-        if (ns < n_all && ns <= no + C::kS &&
-            mbar_test_wait(&sm.k_full[ns & 1], (ns >> 1) & 1) &&
-            (!s_new || mbar_test_wait(&sm.q_full[s_seg & 1], (s_seg >> 1) & 1)) &&
-            (ns < no + C::kS || mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1))) {
-          tc_fence_after();
-          const uint32_t k = tmem + C::kK + (ns & 1) * (D / 2);
-          const uint64_t dq = sdesc_sw128(smem_u32(sm.q[s_seg & 1]), 16, 1024);
-#pragma unroll 2
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ts(tmem + s_slot * NQ, k + kk * 8, dq + (((kk / 4) * kQHalf + (kk % 4) * 32) >> 4),
-                    idesc_s, kk > 0);
-          umma_commit(&sm.s_full[s_slot]);
-          umma_commit(&sm.k_empty[ns & 1]);
-          s_slot = s_slot == C::kS - 1 ? 0 : s_slot + 1;
-          ++ns;
-          --s_left;
-          s_new = false;
-          idle = 0;
-        } else if (no < ns && mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1) &&
-                   mbar_test_wait(&sm.v_full[no & 1], (no >> 1) & 1) &&
-                   (!o_new || o_seg == 0 ||
-                    mbar_test_wait(&sm.o_empty[(o_seg - 1) & 1], ((o_seg - 1) >> 1) & 1))) {
-          // D = 64: the instruction is 128 rows high all the same; rows 64-127
-          // read whatever lies one box behind the V tile (the next V tile or P,
-          // inside this struct) and fill tensor-memory lanes that nobody reads.
-          tc_fence_after();
-          const uint64_t dv = sdesc_sw128(smem_u32(sm.v[no & 1]), kBoxBytes, 1024);
-          const uint64_t dp = sdesc_sw128(smem_u32(sm.p[no & 1]), kBoxBytes, 1024);
-#pragma unroll 2
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            umma_ss(tmem + C::kO, dv + ((kk * 16 * 128) >> 4), dp + ((kk * 16 * 128) >> 4),
-                    idesc_o, (!o_new || kk > 0) ? 1u : 0u);
-          umma_commit(&sm.v_empty[no & 1]);
-          umma_commit(&sm.p_empty[no & 1]);
-          ++no;
-          if (--o_left == 0) umma_commit(&sm.o_full);
-          o_new = false;
-          idle = 0;
-        } else if ((++idle & 63) == 0) {   // bounded, like wait_cta
-          if (idle == 64) t0 = globaltimer_ns();
-          if (*reinterpret_cast<volatile uint32_t *>(&sm.abort) != 0) ok = false;
-          if (ok && globaltimer_ns() - t0 > p.wait.limit_ns) {
-            *reinterpret_cast<volatile uint32_t *>(&sm.abort) = 1;
-            record_error(p.wait.err, kDevErrTimeout);
-            ok = false;
+  if (warp < 4) {
+    if (warp == 0) {
+      // ===================== MMA issuer =====================
+      if (elect_one()) {
+        constexpr uint32_t idesc_s = idesc_bf16(kTile, NQ, false, false);
+        constexpr uint32_t idesc_o = idesc_bf16(128, NQ, true, true);
+        const uint64_t dq = sdesc_sw128(smem_u32(sm.q), 16, 1024);
+        bool ok = wait_cta(&sm.q_full, 0, &sm.abort, p.wait);
+        int ns = 0, no = 0, s_slot = 0;   // next S^T, next O^T; ns % kS
+        uint32_t idle = 0;
+        uint64_t t0 = 0;
+        while (ok && no < n_all) {
+          // S^T first: the warpgroup that takes it may be waiting, and its columns
+          // are free once P of the tile that had them is there
+          if (ns < n_all && ns <= no + C::kS &&
+              mbar_test_wait(&sm.k_full[ns & 1], (ns >> 1) & 1) &&
+              (ns < no + C::kS || mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1))) {
+            tc_fence_after();
+            const uint32_t k = tmem + C::kK + (ns & 1) * (D / 2);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ts(tmem + s_slot * NQ, k + kk * 8, dq + (((kk / 4) * kQHalf + (kk % 4) * 32) >> 4),
+                      idesc_s, kk > 0);
+            umma_commit(&sm.s_full[s_slot]);
+            umma_commit(&sm.k_empty[ns & 1]);
+            s_slot = s_slot == C::kS - 1 ? 0 : s_slot + 1;
+            ++ns;
+            idle = 0;
+          } else if (no < ns && mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1) &&
+                     mbar_test_wait(&sm.v_full[no & 1], (no >> 1) & 1)) {
+            // D = 64: the instruction is 128 rows high all the same; rows 64-127
+            // read whatever lies one box behind the V tile (the next V tile or P,
+            // inside this struct) and fill tensor-memory lanes that nobody reads.
+            tc_fence_after();
+            const uint64_t dv = sdesc_sw128(smem_u32(sm.v[no & 1]), kBoxBytes, 1024);
+            const uint64_t dp = sdesc_sw128(smem_u32(sm.p[no & 1]), kBoxBytes, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_ss(tmem + C::kO, dv + ((kk * 16 * 128) >> 4), dp + ((kk * 16 * 128) >> 4),
+                      idesc_o, (no > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&sm.v_empty[no & 1]);
+            umma_commit(&sm.p_empty[no & 1]);
+            ++no;
+            idle = 0;
+          } else if ((++idle & 63) == 0) {   // bounded, like wait_cta
+            if (idle == 64) t0 = globaltimer_ns();
+            if (*reinterpret_cast<volatile uint32_t *>(&sm.abort) != 0) ok = false;
+            if (ok && globaltimer_ns() - t0 > p.wait.limit_ns) {
+              *reinterpret_cast<volatile uint32_t *>(&sm.abort) = 1;
+              record_error(p.wait.err, kDevErrTimeout);
+              ok = false;
+            }
           }
         }
+        umma_commit(&sm.o_full);
+        umma_commit(&sm.drain);
+        drain_bar(&sm.drain, 0, p.wait.err, 4000000000ull);
       }
-      umma_commit(&sm.drain);
-      drain_bar(&sm.drain, 0, p.wait.err, 4000000000ull);
-    }
-    __syncwarp();
-  } else if (warp < 4) {
-    // ===================== queries, and what each key brings along =====================
-    const int sh = 23 - p.sub_bits;
-    const int32_t r0 = fast_r0(p.sub_bits);
-    const int64_t lim = int64_t(1) << 24;
-    // A wait that gave up does not end the loop over the segments: its warps and
-    // the others meet in the same named barriers to the end.
-    bool ok = true;
-    int n0 = 0;   // units before the segment
-#pragma unroll 1
-    for (int u = u_first, seg = 0; u < u_end; ++seg) {
-      const Segment s = segment_at<NQ>(p, u, u_end);
-      const QcAttnSeq &sq = p.seqs[s.seq];
-      const int sb = seg & 1;
-      const float *rp = p.rab_p + (p.rab_per_head ? int64_t(s.h) * p.nb_p : 0);
-      const float *rt = p.rab_t + (p.rab_per_head ? int64_t(s.h) * p.nb_t : 0);
-      // the segment two back is done with its queries, times and table
-      if (seg >= 2)
-        ok = wait_cta_warp(&sm.o_empty[sb], ((seg >> 1) - 1) & 1, &sm.abort, p.wait) && ok;
-      if (ok && warp == 1) {
+      __syncwarp();
+    } else {
+      // ===================== what each key brings along =====================
+      if (warp == 1) {
         // candidates' times, their range, and their distances to the earliest;
         // a padding candidate takes the first one's
         int64_t lo = INT64_MAX, hi = INT64_MIN;
 #pragma unroll
         for (int i = lane; i < NQ; i += 32) {
-          const int64_t t = p.cand_ts[s.q_row + (i < s.nq ? i : 0)];
-          sm.tq[sb][i] = t;
+          const int64_t t = p.cand_ts[q_row + (i < nq ? i : 0)];
+          sm.tq[i] = t;
           lo = t < lo ? t : lo;
           hi = t > hi ? t : hi;
         }
@@ -640,99 +558,89 @@ __global__ void __launch_bounds__(kThreads, 1)
           hi = b > hi ? b : hi;
         }
         __syncwarp();
-        for (int i = lane; i < NQ; i += 32) sm.tqd[sb][i] = float(sm.tq[sb][i] - lo);
+        for (int i = lane; i < NQ; i += 32) sm.tqd[i] = float(sm.tq[i] - lo);
         if (lane == 0) {
-          sm.tq_min[sb] = lo;
-          sm.tq_max[sb] = hi;
+          sm.tq_min = lo;
+          sm.tq_max = hi;
         }
-      }
-      if (ok) {
-        // the queries, K-major in the 128-byte swizzle; rows behind the last are zero
-        const __nv_bfloat16 *q =
-            static_cast<const __nv_bfloat16 *>(p.q) + s.q_row * p.q_rs + s.h * D;
-#pragma unroll 4
-        for (int x = tid - 32; x < NQ * (D / 8); x += 96) {
-          const int r = x / (D / 8), v = x % (D / 8);
-          uint4 val = make_uint4(0, 0, 0, 0);
-          if (r < s.nq) val = load_row8(q + r * p.q_rs + v * 8, p.vec);
-          *reinterpret_cast<uint4 *>(sm.q[sb] + (v >> 3) * kQHalf + r * 128 +
-                                     (((v & 7) ^ (r & 7)) << 4)) = val;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&sm.q_full[sb]);
       }
       named_bar_sync(2, 96);
-      const int64_t t_lo = sm.tq_min[sb], t_hi = sm.tq_max[sb];
-      if (t_lo != t_hi && p.sub_bits <= 4) {   // candidates of several times: the table
+      const int64_t t_lo = sm.tq_min, t_hi = sm.tq_max, lim = int64_t(1) << 24;
+      const int sh = 23 - p.sub_bits;
+      const int32_t r0 = fast_r0(p.sub_bits);
+      if (t_lo != t_hi && p.sub_bits <= 4) {   // candidates of several times: the exponent table
         const int n = fast_table_size(p.sub_bits);
         for (int x = tid - 32; x < n; x += 96)
-          sm.tbl_t[sb][x] = half * qc_bias(rt[fast_table_bucket(x, p.sub_bits, p.nb_t)]);
+          sm.tbl_t[x] = half * qc_bias(rt[fast_table_bucket(x, p.sub_bits, p.nb_t)]);
+        named_bar_sync(2, 96);
       }
-      named_bar_sync(2, 96);
 #pragma unroll 1
-      for (int n = n0 + (warp + 2 - n0 % 3) % 3; ok && n < n0 + s.n; n += 3) {   // n % 3 == warp - 1
+      for (int n = warp - 1; n < n_tiles; n += 3) {
         KeyBias &kb = sm.bias[n % kBias];
-        const int tile = s.t + (n - n0) - 1;   // of the cache; -1: the own pairs
-        if (n >= kBias) {
-          ok = wait_cta_warp(&sm.bias_empty[n % kBias], ((n / kBias) - 1) & 1, &sm.abort, p.wait);
-          if (!ok) break;
-        }
-        if (tile < 0) {
-          const float c = half * qc_bias(rp[0]) + half * qc_bias(rt[0]);
+        int64_t tk[4];
+        float c[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) kb.c[x * 32 + lane] = c;
-          if (lane < 4) kb.mode[lane] = kOwn;
-        } else {
-          // 32 keys (one quadrant) at a time, the next ones' rows on their way;
-          // keys behind the last take its values (their P is zeroed)
-          auto row_of = [&](int x) {
-            return sq.row + min(tile * kTile + x * 32 + lane, sq.len - 1);
-          };
-          int64_t tk = cv.times[row_of(0)];
-          int32_t pk = cv.pos[row_of(0)];
-#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          // keys behind the last take its values; their P is zeroed
+          const int32_t j = min((it.t0 + n) * kTile + x * 32 + lane, sq.len - 1);
+          tk[x] = cv.times[sq.row + j];
+          c[x] = __int_as_float(cv.pos[sq.row + j]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          c[x] = half * qc_bias(rp[pos_bucket(int64_t(sq.pos) - __float_as_int(c[x]), p.nb_p)]);
+        // float time differences are exact: every one, and its two parts, below 2^24
+        bool one = true, near = p.sub_bits <= 4 && t_hi - t_lo < lim;
+        int32_t b_lo[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          b_lo[x] = time_bucket_i64(t_lo - tk[x], p.sub_bits, p.nb_t);
+          if (t_hi != t_lo)
+            one = one && b_lo[x] == time_bucket_i64(t_hi - tk[x], p.sub_bits, p.nb_t);
+          near = near && t_hi - tk[x] < lim && t_lo - tk[x] > -lim;
+        }
+        one = __all_sync(0xffffffffu, one);
+        near = __all_sync(0xffffffffu, near);
+        if (n >= kBias &&
+            !wait_cta_warp(&sm.bias_empty[n % kBias], ((n / kBias) - 1) & 1, &sm.abort, p.wait))
+          break;
+        int mode = one ? kTimeOne : near ? kTimeFloat : kTimeInt;
+        if (one) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) c[x] += half * qc_bias(rt[b_lo[x]]);
+        } else if (near) {
+          // table entries of the earliest and the latest candidate
+          float base[4];
+          int32_t e_lo[4], e_hi[4];
+          bool two = true;
+#pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int64_t t = tk;
-            float c = half * qc_bias(rp[pos_bucket(int64_t(sq.pos) - pk, p.nb_p)]);
-            if (x < 3) {
-              tk = cv.times[row_of(x + 1)];
-              pk = cv.pos[row_of(x + 1)];
+            base[x] = float(t_lo - tk[x]);
+            e_lo[x] = max(__float_as_int(base[x]) >> sh, r0) - r0;
+            e_hi[x] = max(__float_as_int(float(t_hi - tk[x])) >> sh, r0) - r0;
+            two = two && e_hi[x] - e_lo[x] <= 1;
+          }
+          if (__all_sync(0xffffffffu, two)) {
+            // The entry is e_lo + 1 exactly from the distance on whose bits are
+            // (e_lo + 1 + r0) << sh: an integer below 2^24 where both entries
+            // occur, so its difference to base is exact.
+            mode = kTimeTwo;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              kb.c2[x * 32 + lane] = c[x] + sm.tbl_t[e_hi[x]];
+              kb.t[x * 32 + lane] = __int_as_float((e_lo[x] + 1 + r0) << sh) - base[x];
+              c[x] += sm.tbl_t[e_lo[x]];
             }
-            const int32_t b_lo = time_bucket_i64(t_lo - t, p.sub_bits, p.nb_t);
-            int mode = kTimeOne;
-            if (t_hi != t_lo &&
-                !__all_sync(0xffffffffu, b_lo == time_bucket_i64(t_hi - t, p.sub_bits, p.nb_t))) {
-              // float time differences are exact: every one, and its two parts, below 2^24
-              const bool near = __all_sync(0xffffffffu, p.sub_bits <= 4 && t_hi - t_lo < lim &&
-                                                            t_hi - t < lim && t_lo - t > -lim);
-              mode = near ? kTimeFloat : kTimeInt;
-            }
-            if (mode == kTimeOne) {
-              c += half * qc_bias(rt[b_lo]);
-            } else if (mode == kTimeFloat) {
-              // table entries of the earliest and the latest candidate
-              const float base = float(t_lo - t);
-              const int32_t e_lo = max(__float_as_int(base) >> sh, r0) - r0;
-              const int32_t e_hi = max(__float_as_int(float(t_hi - t)) >> sh, r0) - r0;
-              kb.t[x * 32 + lane] = base;
-              if (__all_sync(0xffffffffu, e_hi - e_lo <= 1)) {
-                // The entry is e_lo + 1 exactly from the distance on whose bits are
-                // (e_lo + 1 + r0) << sh: an integer below 2^24 where both entries
-                // occur, so its difference to base is exact.
-                mode = kTimeTwo;
-                kb.c2[x * 32 + lane] = c + sm.tbl_t[sb][e_hi];
-                kb.t[x * 32 + lane] = __int_as_float((e_lo + 1 + r0) << sh) - base;
-                c += sm.tbl_t[sb][e_lo];
-              }
-            }
-            kb.c[x * 32 + lane] = c;
-            if (lane == 0) kb.mode[x] = mode;
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) kb.t[x * 32 + lane] = base[x];
           }
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) kb.c[x * 32 + lane] = c[x];
+        if (lane == 0) kb.mode = mode;
         mbar_arrive(&sm.bias_full[n % kBias]);
       }
-      n0 += s.n;
-      u += s.n;
     }
   } else if (warp < 4 + C::kElemWarps) {
     // ===================== elementwise =====================
@@ -740,164 +648,172 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = (warp - 4) >> 2, par = w / C::kHalves, hf = w % C::kHalves, quad = warp & 3;
     const int key = quad * 32 + lane;
     const uint32_t lanes = tmem + (uint32_t(quad * 32) << 16);
+    {
+      // the queries, K-major in the 128-byte swizzle; rows behind the last are zero
+      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + q_row * p.q_rs + h * D;
+#pragma unroll 4
+      for (int x = tid - 128; x < NQ * (D / 8); x += 32 * C::kElemWarps) {
+        const int r = x / (D / 8), u = x % (D / 8);
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (r < nq) val = load_row8(q + r * p.q_rs + u * 8, p.vec);
+        *reinterpret_cast<uint4 *>(sm.q + (u >> 3) * kQHalf + r * 128 +
+                                   (((u & 7) ^ (r & 7)) << 4)) = val;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sm.q_full);
+    }
     const float a = half * p.alpha;
-    uint8_t *const pt = sm.p[par] + hf * kBoxBytes + key * 128;
-    // O of 32 candidates [32][D] goes through this warpgroup's own piece of P
-    float *const stage = reinterpret_cast<float *>(sm.p[par] + hf * kBoxBytes);
-    static_assert(32 * D * sizeof(float) <= kBoxBytes, "O stage");
-    bool ok = true;   // as above: every warp meets every segment's barriers
-    int n0 = 0;       // units before the segment
+    bool ok = true;
+    int slot = par, round = 0;   // n % kS, n / kS
 #pragma unroll 1
-    for (int u = u_first, seg = 0; u < u_end; ++seg) {
-      const Segment s = segment_at<NQ>(p, u, u_end);
-      const QcAttnSeq &sq = p.seqs[s.seq];
-      const int sb = seg & 1, nq = s.nq;
-      const float *rt = p.rab_t + (p.rab_per_head ? int64_t(s.h) * p.nb_t : 0);
-#pragma unroll 1
-      for (int n = n0 + ((n0 ^ par) & 1); ok && n < n0 + s.n; n += 2) {
-        const int slot = n % C::kS, round = n / C::kS, bs = n % kBias;
-        const uint32_t s_col = lanes + slot * NQ;
-        const int32_t j = (s.t + (n - n0) - 1) * kTile + key;   // row of the sequence
-        const KeyBias &kb = sm.bias[bs];
-        ok = wait_cta_warp(&sm.bias_full[bs], (n / kBias) & 1, &sm.abort, p.wait);
-        if (!ok) break;
-        const int mode = kb.mode[quad];
-        const float c = kb.c[key];
-        // a key behind the last, or in a hidden bucket, adds exactly nothing
-        const bool valid = j < sq.len && !(mode == kTimeOne && c <= 0.5f * kQcBiasFloor);
-        float c2 = 0.f, t = 0.f, wsum = 0.f;
-        int64_t tk = 0;
-        if (mode != kTimeOne && mode != kOwn) {
-          c2 = kb.c2[key];
-          t = kb.t[key];
-          if (mode == kTimeInt) tk = cv.times[sq.row + min(j, sq.len - 1)];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.bias_empty[bs]);
-        ok = wait_cta_warp(&sm.s_full[slot], round & 1, &sm.abort, p.wait);
-        if (ok && n >= 2)   // the product of the tile two back has read P
-          ok = wait_cta_warp(&sm.p_empty[par], ((n >> 1) - 1) & 1, &sm.abort, p.wait);
+    for (int n = par; n < n_all; n += 2, slot += 2, slot -= slot >= C::kS ? (++round, C::kS) : 0) {
+      const uint32_t s_col = lanes + slot * NQ;
+      uint8_t *pt = sm.p[par] + hf * kBoxBytes + key * 128;
+      if (n < self) {
+        // the candidates' own pairs: bias of distance 0, P's diagonal
+        ok = wait_cta_warp(&sm.s_full[0], 0, &sm.abort, p.wait);
         if (!ok) break;
         tc_fence_after();
-        if (mode == kOwn) {
-          // P's diagonal (this half's lies in quads 2 hf and 2 hf + 1)
-          uint32_t bits = 0;
-          if (quad >> 1 == hf && quad * 32 < nq) {
-            uint32_t sv = 0;
+        uint32_t bits = 0;
+        // (candidates of this warpgroup's half: its diagonal lies in quads 2 hf, 2 hf + 1)
+        if (quad >> 1 == hf && quad * 32 < nq) {
+          uint32_t sv = 0;
 #pragma unroll
-            for (int e0 = 0; e0 < 32; e0 += 16) {
-              uint32_t r[16];
-              tmem_ld16(s_col + quad * 32 + e0, r);
-              tmem_wait_ld(r);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) sv = lane == e0 + e ? r[e] : sv;
-            }
-            const float x = fmaf(p.alpha, __uint_as_float(sv), WEIGHTS ? c : 2.0f * c);
-            const float ps = x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
-            bits = key < nq ? pack_bf16x2(ps, 0.f) : 0u;
-          }
-          bits = key & 1 ? bits << 16 : bits;
-          const int at = key - hf * 64;   // its column in this half (other quads: bits are 0)
-#pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            uint32_t v4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v4[e] = (at >> 1) == v * 4 + e ? bits : 0u;
-            *reinterpret_cast<uint4 *>(pt + ((v ^ (key & 7)) << 4)) =
-                make_uint4(v4[0], v4[1], v4[2], v4[3]);
-          }
-        } else {
-#define HSTU_QC_CHUNK(M_, A_)                                                                     \
-  chunk<D, NQ, WEIGHTS, M_, A_, 16>(r, pk, sm, sb, c0, a, c, c2, t, tk, rt, half, p.sub_bits,     \
-                                    p.nb_t, nq - c0, wsum)
-#pragma unroll 1
-          for (int c0 = hf * 64; c0 < min(hf * 64 + 64, nq); c0 += 16) {
-            uint32_t r[16], pk[8];
-            tmem_ld16(s_col + c0, r);
+          for (int e0 = 0; e0 < 32; e0 += 16) {
+            uint32_t r[16];
+            tmem_ld16(s_col + quad * 32 + e0, r);
             tmem_wait_ld(r);
-            if (mode == kTimeOne) {
-              if (!WEIGHTS || nq - c0 >= 16)
-                HSTU_QC_CHUNK(kTimeOne, true);
-              else
-                HSTU_QC_CHUNK(kTimeOne, false);
-            } else if (mode == kTimeTwo) {
-              HSTU_QC_CHUNK(kTimeTwo, !WEIGHTS);
-            } else if (mode == kTimeFloat) {
-              HSTU_QC_CHUNK(kTimeFloat, !WEIGHTS);
-            } else {
-              HSTU_QC_CHUNK(kTimeInt, !WEIGHTS);
-            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) pk[e] = valid ? pk[e] : 0;
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              *reinterpret_cast<uint4 *>(pt + (((((c0 & 63) >> 3) + e) ^ (key & 7)) << 4)) =
-                  make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            for (int e = 0; e < 16; ++e) sv = lane == e0 + e ? r[e] : sv;
           }
-#undef HSTU_QC_CHUNK
+          const float x = fmaf(p.alpha, __uint_as_float(sv), qc_bias(rp[0]) + qc_bias(rt[0]));
+          const float ps = x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
+          bits = key < nq ? pack_bf16x2(ps, 0.f) : 0u;
         }
-        tc_fence_before();          // S^T has been read
-        fence_proxy_async_smem();   // P^T is written
-        mbar_arrive(&sm.p_full[par]);
-        if constexpr (WEIGHTS) {
-          if (mode != kOwn && j < sq.len && hf * 64 < nq)
-            p.wpart[sq.wp0 + (int64_t(s.qtile * C::kHalves + hf) * H + s.h) * sq.len + j] =
-                valid ? wsum : 0.f;
-        }
-      }
-      // ---- the segment's O^T (lane = feature) to rows: out, or a partial sum ----
-      const int c_first = w * 32, c_end = min(c_first + 32, nq);
-      ok = ok && wait_cta_warp(&sm.o_full, seg & 1, &sm.abort, p.wait);
-      tc_fence_after();
-      if (ok && quad * 32 < D) {
-#pragma unroll 1
-        for (int c0 = c_first; c0 < c_end; c0 += 16) {
-          uint32_t r[16];
-          tmem_ld16(lanes + C::kO + c0, r);
-          tmem_wait_ld(r);
+        bits = key & 1 ? bits << 16 : bits;
+        const int at = key - hf * 64;   // its column in this half (other quads: bits are 0)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) stage[(c0 - c_first + e) * D + key] = __uint_as_float(r[e]);
+        for (int u = 0; u < 8; ++u) {
+          uint32_t v4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v4[e] = (at >> 1) == u * 4 + e ? bits : 0u;
+          *reinterpret_cast<uint4 *>(pt + ((u ^ (key & 7)) << 4)) =
+              make_uint4(v4[0], v4[1], v4[2], v4[3]);
         }
+        tc_fence_before();
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.p_full[0]);
+        continue;
       }
-      tc_fence_before();
-      mbar_arrive(&sm.o_empty[sb]);
-      named_bar_sync(3 + w, 128);
+      const int m = n - self;                       // tile of the cache
+      const int32_t j = (it.t0 + m) * kTile + key;
+      const int bs = m % kBias;
+      const KeyBias &kb = sm.bias[bs];
+      ok = wait_cta_warp(&sm.bias_full[bs], (m / kBias) & 1, &sm.abort, p.wait);
+      if (!ok) break;
+      const int mode = kb.mode;
+      const float c = kb.c[key];
+      // a key behind the last, or in a hidden bucket, adds exactly nothing
+      const bool valid = j < sq.len && !(mode == kTimeOne && c <= 0.5f * kQcBiasFloor);
+      float c2 = 0.f, t = 0.f, wsum = 0.f;
+      int64_t tk = 0;
+      if (mode != kTimeOne) {
+        c2 = kb.c2[key];
+        t = kb.t[key];
+        if (mode == kTimeInt) tk = cv.times[sq.row + min(j, sq.len - 1)];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.bias_empty[bs]);
+      ok = wait_cta_warp(&sm.s_full[slot], round & 1, &sm.abort, p.wait);
+      if (ok && n >= 2)   // the product of the tile two back has read P
+        ok = wait_cta_warp(&sm.p_empty[par], ((n >> 1) - 1) & 1, &sm.abort, p.wait);
+      if (!ok) break;
+      tc_fence_after();
+#define HSTU_QC_CHUNK(M_, A_)                                                                   \
+  chunk<D, NQ, WEIGHTS, M_, A_, 16>(r, pk, sm, c0, a, c, c2, t, tk, rt, half, p.sub_bits, p.nb_t, \
+                                    nq - c0, wsum)
+#pragma unroll 1
+      for (int c0 = hf * 64; c0 < min(hf * 64 + 64, nq); c0 += 16) {
+        uint32_t r[16], pk[8];
+        tmem_ld16(s_col + c0, r);
+        tmem_wait_ld(r);
+        if (mode == kTimeOne) {
+          if (!WEIGHTS || nq - c0 >= 16)
+            HSTU_QC_CHUNK(kTimeOne, true);
+          else
+            HSTU_QC_CHUNK(kTimeOne, false);
+        } else if (mode == kTimeTwo) {
+          HSTU_QC_CHUNK(kTimeTwo, !WEIGHTS);
+        } else if (mode == kTimeFloat) {
+          HSTU_QC_CHUNK(kTimeFloat, !WEIGHTS);
+        } else {
+          HSTU_QC_CHUNK(kTimeInt, !WEIGHTS);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pk[e] = valid ? pk[e] : 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint4 *>(pt + (((((c0 & 63) >> 3) + e) ^ (key & 7)) << 4)) =
+              make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+      }
+#undef HSTU_QC_CHUNK
+      tc_fence_before();          // S^T has been read
+      fence_proxy_async_smem();   // P^T is written
+      mbar_arrive(&sm.p_full[par]);
+      if constexpr (WEIGHTS) {
+        if (j < sq.len && hf * 64 < nq)
+          p.wpart[sq.wp0 + (int64_t(it.qtile * C::kHalves + hf) * H + h) * sq.len + j] =
+              valid ? wsum : 0.f;
+      }
+    }
+    // ---- O^T (lane = feature) through the P tiles' memory to rows of out ----
+    const int c_first = w * 32, c_end = min(c_first + 32, nq);
+    if (ok) ok = wait_cta_warp(&sm.o_full, 0, &sm.abort, p.wait);
+    tc_fence_after();
+    float *stage = reinterpret_cast<float *>(&sm.p[0][0]);   // [NQ][D]
+    if (ok && quad * 32 < D) {
+#pragma unroll 1
+      for (int c0 = c_first; c0 < c_end; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld16(lanes + C::kO + c0, r);
+        tmem_wait_ld(r);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) stage[(c0 + e) * D + key] = __uint_as_float(r[e]);
+      }
+    }
+    named_bar_sync(3 + w, 128);
+    if (ok) {
       constexpr int kRowLanes = D / 4, kRows = 128 / kRowLanes;   // 4 features per lane
       const int wt = (tid - 128) & 127, e = (wt % kRowLanes) * 4;
-      // a partial sum's place: the CTA's first segment or its last
-      float *acc = s.n == s.per ? nullptr
-                                : p.acc + int64_t(2 * blockIdx.x + (u > u_first)) * p.acc_rows * D + e;
 #pragma unroll 2
-      for (int i = c_first + wt / kRowLanes; ok && i < c_end; i += kRows) {
-        const float4 o = *reinterpret_cast<const float4 *>(stage + (i - c_first) * D + e);
-        if (acc) {
-          *reinterpret_cast<float4 *>(acc + i * D) = o;
+      for (int i = c_first + wt / kRowLanes; i < c_end; i += kRows) {
+        const float4 o = *reinterpret_cast<const float4 *>(stage + i * D + e);
+        if (sq.splits > 1) {
+          *reinterpret_cast<float4 *>(
+              p.acc + ((sq.acc0 + (int64_t(it.split) * sq.n + i0 + i) * H + h) * D + e)) = o;
         } else {
           __nv_bfloat16 *dst =
-              static_cast<__nv_bfloat16 *>(p.out) + (s.q_row + i) * p.o_rs + s.h * D + e;
-          const uint2 v = make_uint2(pack_bf16x2(o.x * p.scale, o.y * p.scale),
+              static_cast<__nv_bfloat16 *>(p.out) + (q_row + i) * p.o_rs + h * D + e;
+          const uint2 w = make_uint2(pack_bf16x2(o.x * p.scale, o.y * p.scale),
                                      pack_bf16x2(o.z * p.scale, o.w * p.scale));
           if (p.vec) {
-            *reinterpret_cast<uint2 *>(dst) = v;
+            *reinterpret_cast<uint2 *>(dst) = w;
           } else {
-            reinterpret_cast<uint16_t *>(dst)[0] = uint16_t(v.x);
-            reinterpret_cast<uint16_t *>(dst)[1] = uint16_t(v.x >> 16);
-            reinterpret_cast<uint16_t *>(dst)[2] = uint16_t(v.y);
-            reinterpret_cast<uint16_t *>(dst)[3] = uint16_t(v.y >> 16);
+            reinterpret_cast<uint16_t *>(dst)[0] = uint16_t(w.x);
+            reinterpret_cast<uint16_t *>(dst)[1] = uint16_t(w.x >> 16);
+            reinterpret_cast<uint16_t *>(dst)[2] = uint16_t(w.y);
+            reinterpret_cast<uint16_t *>(dst)[3] = uint16_t(w.y >> 16);
           }
         }
       }
-      named_bar_sync(3 + w, 128);   // the stage is P again
-      n0 += s.n;
-      u += s.n;
     }
   } else {
     // ===================== decoding =====================
     const int dw = warp - 4 - C::kElemWarps;
     if (dw < C::kDecWarps)
-      decode_tiles<D, NQ, false>(p, sm, u_first, u_end, tmem, dw, lane);
+      decode_tiles<D, NQ, false>(p, sm, it, sq, h, q_row, nq, tmem, dw, lane);
     else
-      decode_tiles<D, NQ, true>(p, sm, u_first, u_end, tmem, dw - C::kDecWarps, lane);
+      decode_tiles<D, NQ, true>(p, sm, it, sq, h, q_row, nq, tmem, dw - C::kDecWarps, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -914,22 +830,23 @@ cudaError_t launch_t(const QcAttnParams &p, cudaStream_t st) {
   static PerDeviceOnce attr;
   cudaError_t e = set_smem_once(attr, attn_kernel<D, NQ, WEIGHTS>, smem);
   if (e != cudaSuccess) return e;
-  attn_kernel<D, NQ, WEIGHTS><<<unsigned(p.ctas), kThreads, smem, st>>>(p);
+  const unsigned grid = unsigned(p.items) * unsigned(p.cache.heads);
+  attn_kernel<D, NQ, WEIGHTS><<<grid, kThreads, smem, st>>>(p);
   count_launch();
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_d(const QcAttnParams &p, cudaStream_t st) {
+cudaError_t launch_d(const QcAttnParams &p, int nq, cudaStream_t st) {
   const bool w = p.weight_rows > 0;
-  if (p.nq == 64) return w ? launch_t<D, 64, true>(p, st) : launch_t<D, 64, false>(p, st);
+  if (nq == 64) return w ? launch_t<D, 64, true>(p, st) : launch_t<D, 64, false>(p, st);
   return w ? launch_t<D, 128, true>(p, st) : launch_t<D, 128, false>(p, st);
 }
 
 }  // namespace qc_tc
 
-cudaError_t launch_qcache_attn_tc(const QcAttnParams &p, cudaStream_t st) {
-  return p.cache.d_qk == 64 ? qc_tc::launch_d<64>(p, st) : qc_tc::launch_d<128>(p, st);
+cudaError_t launch_qcache_attn_tc(const QcAttnParams &p, int nq, cudaStream_t st) {
+  return p.cache.d_qk == 64 ? qc_tc::launch_d<64>(p, nq, st) : qc_tc::launch_d<128>(p, nq, st);
 }
 
 }  // namespace hstu

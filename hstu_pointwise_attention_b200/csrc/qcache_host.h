@@ -44,19 +44,14 @@ struct QcEvictParams {
 };
 
 // --- attention over the cache ---
-// Both kernels cut the keys: the CUDA-core one into `splits` ranges per sequence
-// (an item is 16 candidates x a range, times heads), the tensor-core one into
-// units of which every CTA takes the same number (qcache_attn_sm100.cu).
 struct QcAttnSeq {
   int64_t row, q0;         // first cache row, first candidate row
+  int64_t acc0;            // first row of its partial outputs [split][n][H]
   int64_t wp0;             // first float of its weight partials [plane][H][len]
   int64_t wrow0;           // its first row in the weight pass of this launch
-  int64_t acc0;            // CUDA cores: first row of its partial outputs [split][n][H]
   int32_t len, n, pos;     // cached rows, candidates, the candidates' position
-  int32_t item0, splits;   // CUDA cores: its first item, key ranges
-  int32_t u0;              // tensor cores: its first unit
-  int32_t fin0;            // its first row in the summing pass
-  int32_t pad;
+  int32_t item0;           // its first item (query tile x key range) in this launch
+  int32_t splits, fin0;    // key ranges; its first row in the summing pass
 };
 struct QcAttnParams {
   QCacheView cache;
@@ -69,12 +64,8 @@ struct QcAttnParams {
   WaitCtl wait;
   float alpha, scale, decay;
   int32_t nb_p, nb_t, sub_bits;
-  int32_t n_seqs;
-  int32_t items, chunk;           // CUDA cores: items, 128-key tiles per key range
-  int32_t nq;                     // tensor cores: candidates per CTA (64 or 128; else 0)
-  int32_t units, per_cta, ctas;   //   units, units per CTA, CTAs
-  int32_t acc_rows;               //   candidates per partial output, two of them per CTA
-  int32_t fin_rows;               // (candidate, head) rows of the summing pass
+  int32_t n_seqs, items, chunk;   // chunk: 128-key tiles per key range
+  int32_t fin_rows;               // (candidate, head) rows of split sequences
   int64_t weight_rows;            // cached rows whose weight is updated (0: none)
   bool rab_per_head, vec, clear_err;
   QcAttnSeq seqs[kQcMaxSeqs];
@@ -90,8 +81,8 @@ cudaError_t launch_qcache_append(const QcRowsParams &p, bool bf16, cudaStream_t 
 cudaError_t launch_qcache_read(const QcRowsParams &p, bool bf16, cudaStream_t st);
 cudaError_t launch_qcache_evict(const QcEvictParams &p, int32_t max_len, int64_t move_blocks,
                                 cudaStream_t st);
-// Tensor cores: bf16, d_qk = d_v in {64, 128}.
-cudaError_t launch_qcache_attn_tc(const QcAttnParams &p, cudaStream_t st);
+// Tensor cores: bf16, d_qk = d_v in {64, 128}; nq = 64 or 128 candidates per CTA.
+cudaError_t launch_qcache_attn_tc(const QcAttnParams &p, int nq, cudaStream_t st);
 cudaError_t launch_qcache_attn_simt(const QcAttnParams &p, bool bf16, cudaStream_t st);
 // Sums the partial outputs of split sequences and the weight partials
 // (planes of `plane` candidates each).
