@@ -250,7 +250,7 @@ void make_share(const AttnArgs &a, int32_t b0, int64_t acc_row, int64_t wp, QcAt
     for (int32_t b = b0; b < b0 + p.n_seqs; ++b) most = std::max(most, a.coff[b + 1] - a.coff[b]);
     s.nq = most <= 64 ? 64 : 128;
     s.plane = 64;
-    p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148, 3);
+    p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148, 9);
   } else {
     s.nq = s.plane = kQcSimtQueries;
     p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148 * 4, 1);

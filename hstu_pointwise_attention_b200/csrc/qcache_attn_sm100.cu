@@ -75,7 +75,7 @@ struct Cfg {
   static_assert(kK + 2 * (D / 2) <= 512, "tensor memory");
 };
 
-// How the time bias of a tile's keys is found.  kTimeOne: the same for all
+// How the time bias of 32 keys of a tile is found.  kTimeOne: the same for all
 // candidates, part of c.  kTimeTwo: each key meets one or two neighbouring
 // buckets, c below and c2 from candidate time t on (relative to the earliest).
 // kTimeFloat: by the float-exponent table, t = earliest candidate - key.
@@ -88,7 +88,7 @@ enum : int { kTimeOne = 0, kTimeTwo = 1, kTimeFloat = 2, kTimeInt = 3 };
 constexpr int kBias = 6;
 struct KeyBias {
   float c[kTile], c2[kTile], t[kTile];
-  int mode;
+  int mode[4];   // of 32 keys each
 };
 
 template <int D, int NQ>
@@ -102,8 +102,8 @@ struct Smem {
   alignas(16) uint8_t k_scales[C::kStages][C::kScaleBytes];
   alignas(16) uint8_t v_scales[C::kStages][C::kScaleBytes];
   KeyBias bias[kBias];
-  alignas(16) int64_t tq[NQ];     // candidates' times
-  alignas(16) float tqd[NQ];      // and relative to the earliest of them
+  alignas(16) float tqd[NQ];      // candidates' times relative to the earliest of them
+  alignas(16) float live[NQ];     // 1 for a candidate, 0 for padding
   float tbl_t[kTblT];
   int64_t tq_min, tq_max;
   uint64_t k_full[2], k_empty[2], v_full[C::kV], v_empty[C::kV];
@@ -120,21 +120,27 @@ struct Smem {
 // Bounded wait.  The CTA's own flag, not the error word of the workspace, tells
 // its other roles to leave: the word may hold anything until this call's first
 // CTA has cleared it.
-__device__ __forceinline__ bool wait_cta(uint64_t *bar, uint32_t parity, uint32_t *abort,
-                                         const WaitCtl &w) {
-  if (mbar_try_wait(bar, parity)) return true;
+// The roles' loops run side by side on every scheduler and together have to stay
+// in the instruction cache: what a loop seldom needs (here, finding a segment) is
+// kept out of line.
+__device__ __noinline__ bool wait_cta_slow(uint64_t *bar, uint32_t parity, uint32_t *abort,
+                                           uint32_t *err, uint64_t limit_ns) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile uint32_t *>(abort) != 0) return false;
-    if (globaltimer_ns() - t0 > w.limit_ns) {
+    if (globaltimer_ns() - t0 > limit_ns) {
       *reinterpret_cast<volatile uint32_t *>(abort) = 1;
-      record_error(w.err, kDevErrTimeout);
+      record_error(err, kDevErrTimeout);
       return false;
     }
   }
+}
+__device__ __forceinline__ bool wait_cta(uint64_t *bar, uint32_t parity, uint32_t *abort,
+                                         const WaitCtl &w) {
+  return mbar_try_wait(bar, parity) || wait_cta_slow(bar, parity, abort, w.err, w.limit_ns);
 }
 __device__ __forceinline__ bool wait_cta_warp(uint64_t *bar, uint32_t parity, uint32_t *abort,
                                               const WaitCtl &w) {
@@ -166,21 +172,14 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t *v) {
                : "memory");
 }
 // 8 values of a bf16 row.
-__device__ __forceinline__ uint4 load_row8(const __nv_bfloat16 *src, bool vec) {
-  if (vec) return *reinterpret_cast<const uint4 *>(src);
+__device__ __noinline__ uint4 load_row8_scalar(const __nv_bfloat16 *src) {
   uint32_t e[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) e[i] = reinterpret_cast<const uint16_t *>(src)[i];
   return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
-__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float s) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
-    s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
-  }
-  return s;
+__device__ __forceinline__ uint4 load_row8(const __nv_bfloat16 *src, bool vec) {
+  return vec ? *reinterpret_cast<const uint4 *>(src) : load_row8_scalar(src);
 }
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -193,56 +192,50 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// W candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum
-// of |P| over the first `live` of them.  With weights (returned in float32)
-// SiLU is x / (1 + 2^y), y = -x log2 e, good to a few 2^-22; else h (1 + tanh h)
-// with h = x / 2, half the special-function work, its error below P's rounding.
-// The special-function unit (16 results a cycle and SM) is what bounds this
-// loop with weights; every other pair of quotients shares a reciprocal, which
-// trades one of its results for three multiplications and balances the two.
-template <int D, int NQ, bool WEIGHTS, int MODE, bool ALL, int W>
-__device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W / 2],
-                                        const Smem<D, NQ> &sm, int c0, float a, float c, float c2,
-                                        float t, int64_t tk, const float *rt, float half,
-                                        int sub_bits, int nb_t, int live, float &wsum) {
+// The time bias of one pair, bucket by bucket (times too far apart for floats).
+__device__ __noinline__ float time_bias_int(int64_t dt, const float *rt, int sub_bits, int nb_t) {
+  return qc_bias(rt[time_bucket_i64(dt, sub_bits, nb_t)]);
+}
+
+// 16 candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum
+// of |P| over the live ones.  With weights (returned in float32) SiLU is
+// x / (1 + 2^y), y = -x log2 e, good to a few 2^-22; else h (1 + tanh h) with
+// h = x / 2, half the special-function work, its error below P's rounding.  The
+// special-function unit (16 results a cycle and SM) is what bounds the weights'
+// form; every other pair of quotients shares a reciprocal, which trades one of its
+// results for three multiplications.
+template <int D, int NQ, bool WEIGHTS, int MODE>
+__device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8],
+                                      const Smem<D, NQ> &sm, int c0, float a, float c,
+                                      float c2, float t, int64_t tk, const float *rt, float half,
+                                      int sub_bits, int nb_t, const int64_t *ts, int nq,
+                                      float &wsum) {
   const int sh = 23 - sub_bits;
   const int32_t r0 = fast_r0(sub_bits);
   constexpr float kL = -1.4426950408889634f;
-  const float ay = kL * a, cy = kL * c;
-  float tq[4];
 #pragma unroll
-  for (int e = 0; e < W; e += 2) {
-    if constexpr (MODE == kTimeTwo || MODE == kTimeFloat) {
-      if ((e & 3) == 0) {
-        const float4 v = *reinterpret_cast<const float4 *>(&sm.tqd[c0 + e]);
-        tq[0] = v.x;
-        tq[1] = v.y;
-        tq[2] = v.z;
-        tq[3] = v.w;
-      }
-    }
-    float x[2], y[2], pv[2];
+  for (int e = 0; e < 16; e += 4) {
+    float x[4], pv[4];
+    float4 tq = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (MODE == kTimeTwo || MODE == kTimeFloat)
+      tq = *reinterpret_cast<const float4 *>(&sm.tqd[c0 + e]);
+    const float tqs[4] = {tq.x, tq.y, tq.z, tq.w};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 4; ++u) {
       const float sv = __uint_as_float(s[e + u]);
       if constexpr (MODE == kTimeOne) {
         x[u] = fmaf(a, sv, c);
-        y[u] = fmaf(ay, sv, cy);
       } else if constexpr (MODE == kTimeTwo) {
-        x[u] = fmaf(a, sv, tq[(e & 3) + u] >= t ? c2 : c);
-        y[u] = kL * x[u];
+        x[u] = fmaf(a, sv, tqs[u] >= t ? c2 : c);
       } else if constexpr (MODE == kTimeFloat) {
-        const int32_t rr = __float_as_int(t + tq[(e & 3) + u]) >> sh;
+        const int32_t rr = __float_as_int(t + tqs[u]) >> sh;
         x[u] = fmaf(a, sv, c) + sm.tbl_t[(rr > r0 ? rr : r0) - r0];
-        y[u] = kL * x[u];
       } else {
-        x[u] = fmaf(a, sv, c) +
-               half * qc_bias(rt[time_bucket_i64(sm.tq[c0 + e + u] - tk, sub_bits, nb_t)]);
-        y[u] = kL * x[u];
+        x[u] = fmaf(a, sv, c) + half * time_bias_int(ts[min(c0 + e + u, nq - 1)] - tk, rt, sub_bits, nb_t);
       }
     }
     if constexpr (WEIGHTS) {
-      if (MODE == kTimeOne && (e & 2) == 0) {
+      if constexpr (MODE == kTimeOne) {
         // one reciprocal for two quotients; logits are held at -42.9, where SiLU
         // is -1e-17, so that the product of the two stays finite
         x[0] = fmaxf(x[0], -42.9f);
@@ -252,17 +245,22 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[W], uint32_t (&pk)[W /
         pv[0] = x[0] * (r * d1);
         pv[1] = x[1] * (r * d0);
       } else {
-        pv[0] = x[0] * rcp_approx(1.0f + ex2_approx(y[0]));
-        pv[1] = x[1] * rcp_approx(1.0f + ex2_approx(y[1]));
+        pv[0] = x[0] * rcp_approx(1.0f + ex2_approx(kL * x[0]));
+        pv[1] = x[1] * rcp_approx(1.0f + ex2_approx(kL * x[1]));
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (ALL || e + u < live) wsum += fabsf(pv[u]);
+      pv[2] = x[2] * rcp_approx(1.0f + ex2_approx(kL * x[2]));
+      pv[3] = x[3] * rcp_approx(1.0f + ex2_approx(kL * x[3]));
+      const float4 live = *reinterpret_cast<const float4 *>(&sm.live[c0 + e]);   // 1 or 0
+      wsum = fmaf(fabsf(pv[0]), live.x, wsum);
+      wsum = fmaf(fabsf(pv[1]), live.y, wsum);
+      wsum = fmaf(fabsf(pv[2]), live.z, wsum);
+      wsum = fmaf(fabsf(pv[3]), live.w, wsum);
     } else {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) pv[u] = fmaf(x[u], tanh_approx(x[u]), x[u]);   // x halved
+      for (int u = 0; u < 4; ++u) pv[u] = fmaf(x[u], tanh_approx(x[u]), x[u]);   // x halved
     }
     pk[e / 2] = pack_bf16x2(pv[0], pv[1]);
+    pk[e / 2 + 1] = pack_bf16x2(pv[2], pv[3]);
   }
 }
 
@@ -497,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               (ns < no + C::kS || mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1))) {
             tc_fence_after();
             const uint32_t k = tmem + C::kK + (ns & 1) * (D / 2);
-#pragma unroll
+#pragma unroll 2
             for (int kk = 0; kk < D / 16; ++kk)
               umma_ts(tmem + s_slot * NQ, k + kk * 8, dq + (((kk / 4) * kQHalf + (kk % 4) * 32) >> 4),
                       idesc_s, kk > 0);
@@ -514,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint64_t dv = sdesc_sw128(smem_u32(sm.v[no & 1]), kBoxBytes, 1024);
             const uint64_t dp = sdesc_sw128(smem_u32(sm.p[no & 1]), kBoxBytes, 1024);
-#pragma unroll
+#pragma unroll 2
             for (int kk = 0; kk < kTile / 16; ++kk)
               umma_ss(tmem + C::kO, dv + ((kk * 16 * 128) >> 4), dp + ((kk * 16 * 128) >> 4),
                       idesc_o, (no > 0 || kk > 0) ? 1u : 0u);
@@ -542,13 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == 1) {
         // candidates' times, their range, and their distances to the earliest;
         // a padding candidate takes the first one's
-        int64_t lo = INT64_MAX, hi = INT64_MIN;
+        int64_t lo = INT64_MAX, hi = INT64_MIN, t[NQ / 32];
 #pragma unroll
-        for (int i = lane; i < NQ; i += 32) {
-          const int64_t t = p.cand_ts[q_row + (i < nq ? i : 0)];
-          sm.tq[i] = t;
-          lo = t < lo ? t : lo;
-          hi = t > hi ? t : hi;
+        for (int i = 0; i < NQ / 32; ++i) {
+          t[i] = p.cand_ts[q_row + (i * 32 + lane < nq ? i * 32 + lane : 0)];
+          lo = t[i] < lo ? t[i] : lo;
+          hi = t[i] > hi ? t[i] : hi;
         }
 #pragma unroll
         for (int m = 16; m; m >>= 1) {
@@ -557,8 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           lo = a < lo ? a : lo;
           hi = b > hi ? b : hi;
         }
-        __syncwarp();
-        for (int i = lane; i < NQ; i += 32) sm.tqd[i] = float(sm.tq[i] - lo);
+#pragma unroll
+        for (int i = 0; i < NQ / 32; ++i) {
+          sm.tqd[i * 32 + lane] = float(t[i] - lo);
+          sm.live[i * 32 + lane] = i * 32 + lane < nq ? 1.0f : 0.0f;
+        }
         if (lane == 0) {
           sm.tq_min = lo;
           sm.tq_max = hi;
@@ -577,68 +577,54 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int n = warp - 1; n < n_tiles; n += 3) {
         KeyBias &kb = sm.bias[n % kBias];
-        int64_t tk[4];
-        float c[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          // keys behind the last take its values; their P is zeroed
-          const int32_t j = min((it.t0 + n) * kTile + x * 32 + lane, sq.len - 1);
-          tk[x] = cv.times[sq.row + j];
-          c[x] = __int_as_float(cv.pos[sq.row + j]);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          c[x] = half * qc_bias(rp[pos_bucket(int64_t(sq.pos) - __float_as_int(c[x]), p.nb_p)]);
-        // float time differences are exact: every one, and its two parts, below 2^24
-        bool one = true, near = p.sub_bits <= 4 && t_hi - t_lo < lim;
-        int32_t b_lo[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          b_lo[x] = time_bucket_i64(t_lo - tk[x], p.sub_bits, p.nb_t);
-          if (t_hi != t_lo)
-            one = one && b_lo[x] == time_bucket_i64(t_hi - tk[x], p.sub_bits, p.nb_t);
-          near = near && t_hi - tk[x] < lim && t_lo - tk[x] > -lim;
-        }
-        one = __all_sync(0xffffffffu, one);
-        near = __all_sync(0xffffffffu, near);
         if (n >= kBias &&
             !wait_cta_warp(&sm.bias_empty[n % kBias], ((n / kBias) - 1) & 1, &sm.abort, p.wait))
           break;
-        int mode = one ? kTimeOne : near ? kTimeFloat : kTimeInt;
-        if (one) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) c[x] += half * qc_bias(rt[b_lo[x]]);
-        } else if (near) {
-          // table entries of the earliest and the latest candidate
-          float base[4];
-          int32_t e_lo[4], e_hi[4];
-          bool two = true;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            base[x] = float(t_lo - tk[x]);
-            e_lo[x] = max(__float_as_int(base[x]) >> sh, r0) - r0;
-            e_hi[x] = max(__float_as_int(float(t_hi - tk[x])) >> sh, r0) - r0;
-            two = two && e_hi[x] - e_lo[x] <= 1;
+        // 32 keys (one quadrant) at a time, the next ones' rows on their way;
+        // keys behind the last take its values (their P is zeroed)
+        auto row_of = [&](int x) {
+          return sq.row + min((it.t0 + n) * kTile + x * 32 + lane, sq.len - 1);
+        };
+        int64_t tk = cv.times[row_of(0)];
+        int32_t pk = cv.pos[row_of(0)];
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          const int64_t t = tk;
+          float c = half * qc_bias(rp[pos_bucket(int64_t(sq.pos) - pk, p.nb_p)]);
+          if (x < 3) {
+            tk = cv.times[row_of(x + 1)];
+            pk = cv.pos[row_of(x + 1)];
           }
-          if (__all_sync(0xffffffffu, two)) {
-            // The entry is e_lo + 1 exactly from the distance on whose bits are
-            // (e_lo + 1 + r0) << sh: an integer below 2^24 where both entries
-            // occur, so its difference to base is exact.
-            mode = kTimeTwo;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              kb.c2[x * 32 + lane] = c[x] + sm.tbl_t[e_hi[x]];
-              kb.t[x * 32 + lane] = __int_as_float((e_lo[x] + 1 + r0) << sh) - base[x];
-              c[x] += sm.tbl_t[e_lo[x]];
+          const int32_t b_lo = time_bucket_i64(t_lo - t, p.sub_bits, p.nb_t);
+          int mode = kTimeOne;
+          if (t_hi != t_lo &&
+              !__all_sync(0xffffffffu, b_lo == time_bucket_i64(t_hi - t, p.sub_bits, p.nb_t))) {
+            // float time differences are exact: every one, and its two parts, below 2^24
+            const bool near = __all_sync(0xffffffffu, p.sub_bits <= 4 && t_hi - t_lo < lim &&
+                                                          t_hi - t < lim && t_lo - t > -lim);
+            mode = near ? kTimeFloat : kTimeInt;
+          }
+          if (mode == kTimeOne) {
+            c += half * qc_bias(rt[b_lo]);
+          } else if (mode == kTimeFloat) {
+            // table entries of the earliest and the latest candidate
+            const float base = float(t_lo - t);
+            const int32_t e_lo = max(__float_as_int(base) >> sh, r0) - r0;
+            const int32_t e_hi = max(__float_as_int(float(t_hi - t)) >> sh, r0) - r0;
+            kb.t[x * 32 + lane] = base;
+            if (__all_sync(0xffffffffu, e_hi - e_lo <= 1)) {
+              // The entry is e_lo + 1 exactly from the distance on whose bits are
+              // (e_lo + 1 + r0) << sh: an integer below 2^24 where both entries
+              // occur, so its difference to base is exact.
+              mode = kTimeTwo;
+              kb.c2[x * 32 + lane] = c + sm.tbl_t[e_hi];
+              kb.t[x * 32 + lane] = __int_as_float((e_lo + 1 + r0) << sh) - base;
+              c += sm.tbl_t[e_lo];
             }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) kb.t[x * 32 + lane] = base[x];
           }
+          kb.c[x * 32 + lane] = c;
+          if (lane == 0) kb.mode[x] = mode;
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) kb.c[x * 32 + lane] = c[x];
-        if (lane == 0) kb.mode = mode;
         mbar_arrive(&sm.bias_full[n % kBias]);
       }
     }
@@ -711,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const KeyBias &kb = sm.bias[bs];
       ok = wait_cta_warp(&sm.bias_full[bs], (m / kBias) & 1, &sm.abort, p.wait);
       if (!ok) break;
-      const int mode = kb.mode;
+      const int mode = kb.mode[quad];
       const float c = kb.c[key];
       // a key behind the last, or in a hidden bucket, adds exactly nothing
       const bool valid = j < sq.len && !(mode == kTimeOne && c <= 0.5f * kQcBiasFloor);
@@ -729,26 +715,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_cta_warp(&sm.p_empty[par], ((n >> 1) - 1) & 1, &sm.abort, p.wait);
       if (!ok) break;
       tc_fence_after();
-#define HSTU_QC_CHUNK(M_, A_)                                                                   \
-  chunk<D, NQ, WEIGHTS, M_, A_, 16>(r, pk, sm, c0, a, c, c2, t, tk, rt, half, p.sub_bits, p.nb_t, \
-                                    nq - c0, wsum)
+#define HSTU_QC_CHUNK(M_)                                                                       \
+  chunk<D, NQ, WEIGHTS, M_>(r, pk, sm, c0, a, c, c2, t, tk, rt, half, p.sub_bits, p.nb_t, \
+                        p.cand_ts + q_row, nq, wsum)
 #pragma unroll 1
       for (int c0 = hf * 64; c0 < min(hf * 64 + 64, nq); c0 += 16) {
         uint32_t r[16], pk[8];
         tmem_ld16(s_col + c0, r);
         tmem_wait_ld(r);
-        if (mode == kTimeOne) {
-          if (!WEIGHTS || nq - c0 >= 16)
-            HSTU_QC_CHUNK(kTimeOne, true);
-          else
-            HSTU_QC_CHUNK(kTimeOne, false);
-        } else if (mode == kTimeTwo) {
-          HSTU_QC_CHUNK(kTimeTwo, !WEIGHTS);
-        } else if (mode == kTimeFloat) {
-          HSTU_QC_CHUNK(kTimeFloat, !WEIGHTS);
-        } else {
-          HSTU_QC_CHUNK(kTimeInt, !WEIGHTS);
-        }
+        if (mode == kTimeOne)
+          HSTU_QC_CHUNK(kTimeOne);
+        else if (mode == kTimeTwo)
+          HSTU_QC_CHUNK(kTimeTwo);
+        else if (mode == kTimeFloat)
+          HSTU_QC_CHUNK(kTimeFloat);
+        else
+          HSTU_QC_CHUNK(kTimeInt);
 #pragma unroll
         for (int e = 0; e < 8; ++e) pk[e] = valid ? pk[e] : 0;
 #pragma unroll
