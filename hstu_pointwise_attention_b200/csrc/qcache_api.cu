@@ -178,7 +178,7 @@ hstu_status_t check_attn(const AttnArgs &a, bool have_cache) {
 // One launch's share of the call: sequences [b0, b0 + n_seqs), their key
 // ranges and their places in the scratch buffers.
 struct Share {
-  bool tc;                   // tensor cores
+  bool tc, few;              // bf16 kernels: wide tiles; up to kQcFewQueries candidates each
   int nq, plane;             // candidates per CTA; candidates per weight partial
   int64_t acc_rows, wp;      // rows of `acc` (d_v floats each) and floats of `wpart` it uses
 };
@@ -248,10 +248,13 @@ void make_share(const AttnArgs &a, int32_t b0, int64_t acc_row, int64_t wp, QcAt
     // 64 candidates per CTA while no sequence has more
     int64_t most = 0;
     for (int32_t b = b0; b < b0 + p.n_seqs; ++b) most = std::max(most, a.coff[b + 1] - a.coff[b]);
-    s.nq = most <= 64 ? 64 : 128;
-    s.plane = 64;
-    p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148, 9);
+    s.few = most <= kQcFewQueries;
+    s.nq = s.few ? kQcFewQueries : most <= 64 ? 64 : 128;
+    s.plane = s.few ? kQcFewQueries : 64;
+    p.chunk = s.few ? pick_chunk(a, b0, p.n_seqs, s.nq, 148 * 4, 1)
+                    : pick_chunk(a, b0, p.n_seqs, s.nq, 148, 9);
   } else {
+    s.few = false;
     s.nq = s.plane = kQcSimtQueries;
     p.chunk = pick_chunk(a, b0, p.n_seqs, s.nq, 148 * 4, 1);
   }
@@ -351,7 +354,8 @@ hstu_status_t run_attn(const AttnArgs &a, const int64_t *cand_ts, const void *q,
     rows += s.acc_rows;
     wp += s.wp;
     if (p.items > 0) {
-      const cudaError_t e = s.tc ? launch_qcache_attn_tc(p, s.nq, st)
+      const cudaError_t e = s.few  ? launch_qcache_attn_few(p, st)
+                            : s.tc ? launch_qcache_attn_tc(p, s.nq, st)
                                  : launch_qcache_attn_simt(p, bf16, st);
       if (e != cudaSuccess) return HSTU_ERR_CUDA;
       p.clear_err = false;

@@ -1,5 +1,5 @@
 // qcache_attn.cuh -- pieces shared by the attention kernels over the 4-bit
-// cache (CUDA-core and tensor-core) and by their summing pass.
+// cache and by their summing pass.
 #pragma once
 
 #include "qcache_host.h"
@@ -46,5 +46,46 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 qc_round<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
+
+// N bytes global -> shared, zeros when !ok (src is then not read).
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool ok) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? N : 0), "n"(N)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// 8 values of a bf16 row.
+static __device__ __noinline__ uint4 load_row8_scalar(const __nv_bfloat16 *src) {
+  uint32_t e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = reinterpret_cast<const uint16_t *>(src)[i];
+  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+__device__ __forceinline__ uint4 load_row8(const __nv_bfloat16 *src, bool vec) {
+  return vec ? *reinterpret_cast<const uint4 *>(src) : load_row8_scalar(src);
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 
 }  // namespace hstu

@@ -147,51 +147,11 @@ __device__ __forceinline__ bool wait_cta_warp(uint64_t *bar, uint32_t parity, ui
   return __all_sync(0xffffffffu, wait_cta(bar, parity, abort, w));
 }
 
-// N bytes global -> shared, zeros when !ok (src is then not read).
-template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool ok) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(ok ? 16 : 0)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src),
-                 "r"(ok ? N : 0), "n"(N)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t *v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3])
                : "memory");
 }
-// 8 values of a bf16 row.
-__device__ __noinline__ uint4 load_row8_scalar(const __nv_bfloat16 *src) {
-  uint32_t e[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = reinterpret_cast<const uint16_t *>(src)[i];
-  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-}
-__device__ __forceinline__ uint4 load_row8(const __nv_bfloat16 *src, bool vec) {
-  return vec ? *reinterpret_cast<const uint4 *>(src) : load_row8_scalar(src);
-}
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // The time bias of one pair, bucket by bucket (times too far apart for floats).
 __device__ __noinline__ float time_bias_int(int64_t dt, const float *rt, int sub_bits, int nb_t) {
   return qc_bias(rt[time_bucket_i64(dt, sub_bits, nb_t)]);

@@ -74,8 +74,9 @@ static_assert(sizeof(QcRowsParams) <= 4096 && sizeof(QcEvictParams) <= 4096 + 51
                   sizeof(QcAttnParams) <= 8192,
               "kernel parameters");
 
-constexpr int kQcKeyTile = 128;          // keys per tile (both kernels)
+constexpr int kQcKeyTile = 128;          // keys per tile (all kernels)
 constexpr int kQcSimtQueries = 16;       // candidates per CTA of the CUDA-core kernel
+constexpr int kQcFewQueries = 8;         // and of the one for few candidates
 
 cudaError_t launch_qcache_append(const QcRowsParams &p, bool bf16, cudaStream_t st);
 cudaError_t launch_qcache_read(const QcRowsParams &p, bool bf16, cudaStream_t st);
@@ -83,6 +84,8 @@ cudaError_t launch_qcache_evict(const QcEvictParams &p, int32_t max_len, int64_t
                                 cudaStream_t st);
 // Tensor cores: bf16, d_qk = d_v in {64, 128}; nq = 64 or 128 candidates per CTA.
 cudaError_t launch_qcache_attn_tc(const QcAttnParams &p, int nq, cudaStream_t st);
+// Warp-level products: the same types and sizes, 8 candidates per CTA.
+cudaError_t launch_qcache_attn_few(const QcAttnParams &p, cudaStream_t st);
 cudaError_t launch_qcache_attn_simt(const QcAttnParams &p, bool bf16, cudaStream_t st);
 // Sums the partial outputs of split sequences and the weight partials
 // (planes of `plane` candidates each).
