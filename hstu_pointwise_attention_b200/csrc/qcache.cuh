@@ -62,6 +62,13 @@ __device__ __forceinline__ float q4_scale(uint32_t param) {
   return __uint_as_float((param & 0xFFF0u) << 16);
 }
 
+// (x & mask) | bits as one instruction: written as two operations on constants,
+// it compiled to two (the attention of 64 single events took 98 us instead of 88).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
+}
 // The 8 values of one word as 4 bfloat16 pairs, exact: 0x4300 | q is the
 // bfloat16 128 + q, minus 128 + z leaves q - z (both exact), times s (exact,
 // see above).
@@ -69,18 +76,21 @@ __device__ __forceinline__ void q4_decode_bf16(uint32_t w, uint32_t zz, uint32_t
                                                uint32_t (&out)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t m = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    const uint32_t m = and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u);
     __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&m);
     x = __hsub2(x, *reinterpret_cast<const __nv_bfloat162 *>(&zz));
     x = __hmul2(x, *reinterpret_cast<const __nv_bfloat162 *>(&ss));
     out[i] = *reinterpret_cast<const uint32_t *>(&x);
   }
 }
-// The group's operands of q4_decode_bf16: 128 + z and s, each in both halves.
+// The group's operands of q4_decode_bf16, 128 + z and s; `pair` holds the parameters
+// of the two values of a pair (twice the same, or those of two rows).
+__device__ __forceinline__ void q4_group_pair(uint32_t pair, uint32_t &zz, uint32_t &ss) {
+  zz = and_or(pair, 0x000F000Fu, 0x43004300u);
+  ss = pair & 0xFFF0FFF0u;
+}
 __device__ __forceinline__ void q4_group(uint32_t param, uint32_t &zz, uint32_t &ss) {
-  const uint32_t z = 0x4300u | (param & 0xFu), s = param & 0xFFF0u;
-  zz = z | (z << 16);
-  ss = s | (s << 16);
+  q4_group_pair(__byte_perm(param, 0, 0x1010), zz, ss);
 }
 // Code of element e (0..7) of a word.
 __device__ __forceinline__ int q4_code(uint32_t w, int e) {

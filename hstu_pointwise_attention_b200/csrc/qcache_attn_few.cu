@@ -29,6 +29,7 @@
 // both reads of a stage free of bank conflicts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 
 #include "qcache_attn.cuh"
 #include "tile_common.cuh"
@@ -103,32 +104,50 @@ __global__ void __launch_bounds__(kThreads, 4)
   const float *rt = p.rab_t + (p.rab_per_head ? int64_t(h) * p.nb_t : 0);
 
   // ---- the warp's copies ----
+  // Copy u of a step is the lane's chunk (u * 32 + lane) of its K (or V) codes.  All
+  // copies of a lane have the same swizzle, so each is a constant away from the first.
   const int32_t j_end = min(it.t1 * kQcKeyTile, sq.len);
   int32_t jb = it.t0 * kQcKeyTile + warp * kKeys;   // first key of the step
+  const uint32_t st0 = smem_u32(&sm.st[warp][0]);
+  const uint32_t k_dst = k_chunk<D>(lane / G, lane % G), v_dst = v_chunk<D>(lane / G, lane % G);
   const int64_t at0 = int64_t(h) * cv.rows + sq.row;
-  auto copy = [&](int32_t j, Stage<D> &st) {   // keys [j, j + 32), zeros from j_end on
-    const int64_t at = at0 + j;
-#pragma unroll
-    for (int u = 0; u < G; ++u) {
-      const int x = u * 32 + lane, key = x / G, c = x % G;
-      const bool ok = j + key < j_end;
-      const int64_t src = ok ? (at * G + x) * 16 : 0;
-      cp_async<16>(smem_u32(st.k) + k_chunk<D>(key, c),
-                   reinterpret_cast<const uint8_t *>(cv.k_codes) + src, ok);
-      cp_async<16>(smem_u32(st.v) + v_chunk<D>(key, c),
-                   reinterpret_cast<const uint8_t *>(cv.v_codes) + src, ok);
-    }
-    const bool ok = j + lane < j_end;
-    const int64_t src = ok ? (at + lane) * G : 0;
-    cp_async<2 * G>(smem_u32(st.ks) + lane * 2 * G, cv.k_scales + src, ok);
-    cp_async<2 * G>(smem_u32(st.vs) + lane * 2 * G, cv.v_scales + src, ok);
-  };
+  const uint8_t *k_src = reinterpret_cast<const uint8_t *>(cv.k_codes) + (at0 + jb) * (D / 2) + lane * 16;
+  const uint8_t *v_src = reinterpret_cast<const uint8_t *>(cv.v_codes) + (at0 + jb) * (D / 2) + lane * 16;
+  const uint16_t *ks_src = cv.k_scales + (at0 + jb + lane) * G;
+  const uint16_t *vs_src = cv.v_scales + (at0 + jb + lane) * G;
   int32_t j_copy = jb;
+  auto copy = [&](uint32_t st) {   // keys [j_copy, j_copy + 32) of the cache, zeros from j_end on
+    const int32_t left = j_end - j_copy;
+    if (left >= kKeys) {
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        cp_async<16>(st + offsetof(Stage<D>, k) + k_dst + u * 512, k_src + u * 512, true);
+        cp_async<16>(st + offsetof(Stage<D>, v) + v_dst + u * 512, v_src + u * 512, true);
+      }
+      cp_async<2 * G>(st + offsetof(Stage<D>, ks) + lane * 2 * G, ks_src, true);
+      cp_async<2 * G>(st + offsetof(Stage<D>, vs) + lane * 2 * G, vs_src, true);
+    } else if (left > 0) {
 #pragma unroll 1
-  for (int s = 0; s < kStages; ++s, j_copy += kWarps * kKeys) {
-    if (j_copy < j_end) copy(j_copy, sm.st[warp][s]);
+      for (int u = 0; u < G; ++u) {
+        const bool ok = u * (32 / G) + lane / G < left;
+        cp_async<16>(st + offsetof(Stage<D>, k) + k_dst + u * 512,
+                     ok ? k_src + u * 512 : reinterpret_cast<const uint8_t *>(cv.k_codes), ok);
+        cp_async<16>(st + offsetof(Stage<D>, v) + v_dst + u * 512,
+                     ok ? v_src + u * 512 : reinterpret_cast<const uint8_t *>(cv.v_codes), ok);
+      }
+      const bool ok = lane < left;
+      cp_async<2 * G>(st + offsetof(Stage<D>, ks) + lane * 2 * G, ok ? ks_src : cv.k_scales, ok);
+      cp_async<2 * G>(st + offsetof(Stage<D>, vs) + lane * 2 * G, ok ? vs_src : cv.v_scales, ok);
+    }
     cp_async_commit();
-  }
+    j_copy += kWarps * kKeys;
+    k_src += kWarps * kKeys * D / 2;
+    v_src += kWarps * kKeys * D / 2;
+    ks_src += kWarps * kKeys * G;
+    vs_src += kWarps * kKeys * G;
+  };
+#pragma unroll 1
+  for (int s = 0; s < kStages; ++s) copy(st0 + s * uint32_t(sizeof(Stage<D>)));
 
   // ---- the candidates ----
   uint32_t bq[G][4];
@@ -188,6 +207,13 @@ __global__ void __launch_bounds__(kThreads, 4)
     kt = cv.times[r];
   };
   if (jb < j_end) load_key(jb);
+  // where the lane reads in a stage (the swizzles repeat every 8 keys)
+  const int ka0 = key_of(g);
+  uint32_t k_at[G];
+#pragma unroll
+  for (int u = 0; u < G; ++u) k_at[u] = k_chunk<D>(ka0, u) + 4 * t;
+  const uint32_t v_at = v_chunk<D>(t, (W * g) >> 2) + ((W * g) & 3) * 4;
+  const uint32_t vs_at = (t * G + ((W * g) >> 2)) * 2;
   int cur = 0;
 #pragma unroll 1
   for (; jb < j_end; jb += kWarps * kKeys) {
@@ -198,30 +224,39 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (jb + kWarps * kKeys < j_end) load_key(jb + kWarps * kKeys);
     cp_async_wait<kStages - 1>();
     __syncwarp();
-    Stage<D> &st = sm.st[warp][cur];
-#pragma unroll 1
+    const Stage<D> &st = sm.st[warp][cur];
+    const uint8_t *const k_base = st.k;
+    const uint8_t *kw[G];
+#pragma unroll
+    for (int u = 0; u < G; ++u) kw[u] = k_base + k_at[u];
+    const uint8_t *const vw = st.v + v_at;
+    const uint8_t *const kpar = reinterpret_cast<const uint8_t *>(st.ks) + ka0 * 2 * G;
+    const uint8_t *const vpar = reinterpret_cast<const uint8_t *>(st.vs) + vs_at;
+#pragma unroll
     for (int r0 = 0; r0 < kKeys; r0 += 16) {
       // ---- S^T = K Q^T: keys ka, kb = ka + 8 of this lane ----
-      const int ka = r0 + key_of(g), kb = ka + 8;
+      const int ka = r0 + ka0, kb = ka + 8;
       float s[2][4] = {};
       uint32_t pa[(G + 1) / 2], pb[(G + 1) / 2];
       if constexpr (G == 4) {
-        const uint2 a = *reinterpret_cast<const uint2 *>(&st.ks[ka * G]);
-        const uint2 b = *reinterpret_cast<const uint2 *>(&st.ks[kb * G]);
+        const uint2 a = *reinterpret_cast<const uint2 *>(kpar + r0 * 2 * G);
+        const uint2 b = *reinterpret_cast<const uint2 *>(kpar + (r0 + 8) * 2 * G);
         pa[0] = a.x, pa[1] = a.y, pb[0] = b.x, pb[1] = b.y;
       } else {
-        pa[0] = *reinterpret_cast<const uint32_t *>(&st.ks[ka * G]);
-        pb[0] = *reinterpret_cast<const uint32_t *>(&st.ks[kb * G]);
+        pa[0] = *reinterpret_cast<const uint32_t *>(kpar + r0 * 2 * G);
+        pb[0] = *reinterpret_cast<const uint32_t *>(kpar + (r0 + 8) * 2 * G);
       }
 #pragma unroll
       for (int u = 0; u < G; ++u) {
-        const uint32_t wa = *reinterpret_cast<const uint32_t *>(&st.k[k_chunk<D>(ka, u) + 4 * t]);
-        const uint32_t wb = *reinterpret_cast<const uint32_t *>(&st.k[k_chunk<D>(kb, u) + 4 * t]);
+        const uint32_t wa = *reinterpret_cast<const uint32_t *>(kw[u] + r0 * (D / 2));
+        const uint32_t wb = *reinterpret_cast<const uint32_t *>(kw[u] + (r0 + 8) * (D / 2));
         const uint32_t da = __byte_perm(pa[u / 2], 0, u & 1 ? 0x3232 : 0x1010);
         const uint32_t db = __byte_perm(pb[u / 2], 0, u & 1 ? 0x3232 : 0x1010);
-        uint32_t xa[4], xb[4];
-        q4_decode_bf16(wa, (da & 0x000F000Fu) | 0x43004300u, da & 0xFFF0FFF0u, xa);
-        q4_decode_bf16(wb, (db & 0x000F000Fu) | 0x43004300u, db & 0xFFF0FFF0u, xb);
+        uint32_t xa[4], xb[4], zz, ss;
+        q4_group_pair(da, zz, ss);
+        q4_decode_bf16(wa, zz, ss, xa);
+        q4_group_pair(db, zz, ss);
+        q4_decode_bf16(wb, zz, ss, xb);
         mma(s[0], xa[0], xb[0], xa[1], xb[1], bq[u][0], bq[u][1]);
         mma(s[1], xa[2], xb[2], xa[3], xb[3], bq[u][2], bq[u][3]);
       }
@@ -260,22 +295,18 @@ __global__ void __launch_bounds__(kThreads, 4)
       uint32_t par[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int key = r0 + 4 * e + t;
-        const uint8_t *src = &st.v[v_chunk<D>(key, (W * g) >> 2) + ((W * g) & 3) * 4];
+        const uint8_t *src = vw + (r0 + 4 * e) * (D / 2);
         if constexpr (W == 2) {
           const uint2 x = *reinterpret_cast<const uint2 *>(src);
           w[e][0] = x.x, w[e][1] = x.y;
         } else {
           w[e][0] = *reinterpret_cast<const uint32_t *>(src);
         }
-        par[e] = st.vs[key * G + ((W * g) >> 2)];
+        par[e] = *reinterpret_cast<const uint16_t *>(vpar + (r0 + 4 * e) * 2 * G);
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t d = par[2 * e] | par[2 * e + 1] << 16;
-        zz[e] = (d & 0x000F000Fu) | 0x43004300u;
-        ss[e] = d & 0xFFF0FFF0u;
-      }
+      for (int e = 0; e < 2; ++e)
+        q4_group_pair(__byte_perm(par[2 * e], par[2 * e + 1], 0x5410), zz[e], ss[e]);
 #pragma unroll
       for (int x = 0; x < W; ++x) {
         uint32_t a[4][4];   // features 2 i (a[0], a[2]) and 2 i + 1 of the key pairs
@@ -291,9 +322,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       }
     }
     __syncwarp();   // the warp has read the stage
-    if (j_copy < j_end) copy(j_copy, st);
-    cp_async_commit();
-    j_copy += kWarps * kKeys;
+    copy(st0 + cur * uint32_t(sizeof(Stage<D>)));
     cur ^= 1;
   }
   cp_async_wait<0>();
