@@ -62,6 +62,7 @@ struct Cfg {
   static constexpr int kParBytes = kPer == 1 ? 4 : 2 * kPer;   // K: parameters copied per thread
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kV = 2;
+  static constexpr int kP = 3;
   static constexpr int kPBytes = NQ / 64 * int(kBoxBytes);
   // Tiles of codes on their way: with few candidates the cache's bandwidth is
   // the limit, and bytes in flight per SM = bandwidth x latency, about 36 KB at
@@ -96,7 +97,7 @@ struct Smem {
   using C = Cfg<D, NQ>;
   alignas(1024) uint8_t q[NQ * D * 2];
   alignas(1024) uint8_t v[C::kV][C::kTileBytes];
-  alignas(1024) uint8_t p[2][C::kPBytes];       // behind v: see the D = 64 note at issue_o
+  alignas(1024) uint8_t p[C::kP][C::kPBytes];       // behind v: see the D = 64 note at issue_o
   alignas(16) uint8_t k_codes[C::kStages][C::kCodeBytes];
   alignas(16) uint8_t v_codes[C::kStages][C::kCodeBytes];
   alignas(16) uint8_t k_scales[C::kStages][C::kScaleBytes];
@@ -109,7 +110,7 @@ struct Smem {
   uint64_t k_full[2], k_empty[2], v_full[C::kV], v_empty[C::kV];
   uint64_t s_full[3];             // with three slots a warpgroup takes every other round of one:
                                   // the commits are in order, so the round between is over by then
-  uint64_t p_full[2], p_empty[2];
+  uint64_t p_full[C::kP], p_empty[C::kP];
   uint64_t bias_full[kBias], bias_empty[kBias];
   uint64_t q_full, o_full, drain;
   uint32_t tmem_base;
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.v_empty[i], 1);
     }
     for (int i = 0; i < 3; ++i) mbar_init(&sm.s_full[i], 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kP; ++i) {
       mbar_init(&sm.p_full[i], 128 * C::kHalves);
       mbar_init(&sm.p_empty[i], 1);
     }
@@ -445,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dq = sdesc_sw128(smem_u32(sm.q), 16, 1024);
         bool ok = wait_cta(&sm.q_full, 0, &sm.abort, p.wait);
         int ns = 0, no = 0, s_slot = 0;   // next S^T, next O^T; ns % kS
+        int p_slot = 0, p_par = 0;        // no % kP, (no / kP) & 1
         uint32_t idle = 0;
         uint64_t t0 = 0;
         while (ok && no < n_all) {
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // are free once P of the tile that had them is there
           if (ns < n_all && ns <= no + C::kS &&
               mbar_test_wait(&sm.k_full[ns & 1], (ns >> 1) & 1) &&
-              (ns < no + C::kS || mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1))) {
+              (ns < no + C::kS || mbar_test_wait(&sm.p_full[p_slot], p_par))) {
             tc_fence_after();
             const uint32_t k = tmem + C::kK + (ns & 1) * (D / 2);
 #pragma unroll 2
@@ -464,20 +466,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             s_slot = s_slot == C::kS - 1 ? 0 : s_slot + 1;
             ++ns;
             idle = 0;
-          } else if (no < ns && mbar_test_wait(&sm.p_full[no & 1], (no >> 1) & 1) &&
+          } else if (no < ns && mbar_test_wait(&sm.p_full[p_slot], p_par) &&
                      mbar_test_wait(&sm.v_full[no & 1], (no >> 1) & 1)) {
             // D = 64: the instruction is 128 rows high all the same; rows 64-127
             // read whatever lies one box behind the V tile (the next V tile or P,
             // inside this struct) and fill tensor-memory lanes that nobody reads.
             tc_fence_after();
             const uint64_t dv = sdesc_sw128(smem_u32(sm.v[no & 1]), kBoxBytes, 1024);
-            const uint64_t dp = sdesc_sw128(smem_u32(sm.p[no & 1]), kBoxBytes, 1024);
+            const uint64_t dp = sdesc_sw128(smem_u32(sm.p[p_slot]), kBoxBytes, 1024);
 #pragma unroll 2
             for (int kk = 0; kk < kTile / 16; ++kk)
               umma_ss(tmem + C::kO, dv + ((kk * 16 * 128) >> 4), dp + ((kk * 16 * 128) >> 4),
                       idesc_o, (no > 0 || kk > 0) ? 1u : 0u);
             umma_commit(&sm.v_empty[no & 1]);
-            umma_commit(&sm.p_empty[no & 1]);
+            umma_commit(&sm.p_empty[p_slot]);
+            if (++p_slot == C::kP) {
+              p_slot = 0;
+              p_par ^= 1;
+            }
             ++no;
             idle = 0;
           } else if ((++idle & 63) == 0) {   // bounded, like wait_cta
@@ -610,11 +616,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const float a = half * p.alpha;
     bool ok = true;
-    int slot = par, round = 0;   // n % kS, n / kS
+    int slot = par, round = 0;           // n % kS, n / kS
+    int p_slot = par, p_round = 0;       // n % kP, n / kP
 #pragma unroll 1
-    for (int n = par; n < n_all; n += 2, slot += 2, slot -= slot >= C::kS ? (++round, C::kS) : 0) {
+    for (int n = par; n < n_all;
+         n += 2, slot += 2, slot -= slot >= C::kS ? (++round, C::kS) : 0, p_slot += 2,
+             p_slot -= p_slot >= C::kP ? (++p_round, C::kP) : 0) {
       const uint32_t s_col = lanes + slot * NQ;
-      uint8_t *pt = sm.p[par] + hf * kBoxBytes + key * 128;
+      uint8_t *pt = sm.p[p_slot] + hf * kBoxBytes + key * 128;
       if (n < self) {
         // the candidates' own pairs: bias of distance 0, P's diagonal
         ok = wait_cta_warp(&sm.s_full[0], 0, &sm.abort, p.wait);
@@ -671,8 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.bias_empty[bs]);
       ok = wait_cta_warp(&sm.s_full[slot], round & 1, &sm.abort, p.wait);
-      if (ok && n >= 2)   // the product of the tile two back has read P
-        ok = wait_cta_warp(&sm.p_empty[par], ((n >> 1) - 1) & 1, &sm.abort, p.wait);
+      if (ok && n >= C::kP)   // the product of the tile kP back has read P
+        ok = wait_cta_warp(&sm.p_empty[p_slot], (p_round - 1) & 1, &sm.abort, p.wait);
       if (!ok) break;
       tc_fence_after();
 #define HSTU_QC_CHUNK(M_)                                                                       \
@@ -701,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef HSTU_QC_CHUNK
       tc_fence_before();          // S^T has been read
       fence_proxy_async_smem();   // P^T is written
-      mbar_arrive(&sm.p_full[par]);
+      mbar_arrive(&sm.p_full[p_slot]);
       if constexpr (WEIGHTS) {
         if (j < sq.len && hf * 64 < nq)
           p.wpart[sq.wp0 + (int64_t(it.qtile * C::kHalves + hf) * H + h) * sq.len + j] =
