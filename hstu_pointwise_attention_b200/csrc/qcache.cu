@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kSelThreads)
       c1 = __reduce_add_sync(0xffffffffu, c1);
       c2 = __reduce_add_sync(0xffffffffu, c2);
       c3 = __reduce_add_sync(0xffffffffu, c3);
-      uint32_t *cnt = hist + (round & 1) * 3;   // the other three are cleared meanwhile
+      uint32_t *cnt = hist + (round & 1) * 3;
       if (lane < 3) atomicAdd(&cnt[lane], lane == 0 ? c1 : lane == 1 ? c2 : c3);
       __syncthreads();
       const uint32_t a1 = cnt[0], a2 = cnt[1], a3 = cnt[2];
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kSelThreads)
       } else {
         above = a1;
       }
-      // cleared for the round after next: everyone has read it at the next barrier
+      // the next round's counters, last read before this round's first barrier
       if (tid < 3) hist[((round + 1) & 1) * 3 + tid] = 0;
       __syncthreads();
     }

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int64_t tq0 = 2 * t < nq ? p.cand_ts[q_row + 2 * t] : t_first;
   const int64_t tq1 = 2 * t + 1 < nq ? p.cand_ts[q_row + 2 * t + 1] : t_first;
   const bool one_time = __all_sync(0xffffffffu, tq0 == t_first && tq1 == t_first);
-  const float live0 = 2 * t < nq ? 1.f : 0.f, live1 = 2 * t + 1 < nq ? 1.f : 0.f;
+  const bool live0 = 2 * t < nq, live1 = 2 * t + 1 < nq;
   float *wp = p.weight_rows > 0
                   ? p.wpart + sq.wp0 + (int64_t(it.qtile) * H + h) * sq.len
                   : nullptr;
@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 4)
         pv[e] = (e < 2 ? ok_a : ok_b) ? x : 0.f;
       }
       if (wp) {
-        float w0 = fmaf(fabsf(pv[0]), live0, fabsf(pv[1]) * live1);
-        float w1 = fmaf(fabsf(pv[2]), live0, fabsf(pv[3]) * live1);
+        float w0 = (live0 ? fabsf(pv[0]) : 0.f) + (live1 ? fabsf(pv[1]) : 0.f);
+        float w1 = (live0 ? fabsf(pv[2]) : 0.f) + (live1 ? fabsf(pv[3]) : 0.f);
         w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
         w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
         w0 += __shfl_xor_sync(0xffffffffu, w0, 2);

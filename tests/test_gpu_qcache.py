@@ -292,6 +292,54 @@ def test_attention_candidate_counts(dtype, n):
     check(Problem([200], [n], 2, 64, 64, dtype, seed=240 + n))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", [dict(), dict(per_head=True, t_cand="apart"),
+                                dict(t_cand="before", sub=8, nb=(5000, 3000)),
+                                dict(t_step=10 ** 11, t_cand="apart", pad=8),
+                                dict(pad=5, shift=1, nb=(1, 1)), dict(alpha=-3.0)], ids=str)
+def test_attention_few_candidates(d, kw):
+    """Up to 8 candidates per sequence: histories that end at, before and behind
+    the 32 keys of a step and the 128 of a tile, and ones split over CTAs."""
+    check(Problem([0, 1, 31, 32, 33, 127, 128, 129, 160, 1000, 0, 3],
+                  [1, 2, 3, 4, 5, 6, 7, 8, 1, 3, 8, 0], 2, d, d, "bf16", seed=240 + d, **kw))
+
+
+def test_attention_few_candidates_hidden_buckets_and_one_more():
+    p = Problem([150, 150, 40], [5, 8, 2], 2, 128, 128, "bf16", seed=248, t_cand="apart")
+    p.rab_p[10:] = float("-inf")
+    p.rab_t[5:12] = float(torch.finfo(torch.float32).min)
+    check(p)
+    p.rab_p[:] = float("-inf")
+    out = p.run(0.0)
+    assert torch.all(out[:int(p.off[-1])].float() == 0)
+    for b in range(3):
+        assert torch.all(p.c.weight[p.rows[b]:p.rows[b] + p.lens[b]] == 0)
+    check(Problem([150, 150, 40], [5, 9, 2], 2, 128, 128, "bf16", seed=249))
+
+
+def test_attention_calls_on_two_streams_at_once():
+    """Each call has its own workspace: neither disturbs the other."""
+    ps = [Problem([3000, 700], n, 2, 128, 128, "bf16", seed=256 + n[0])
+          for n in ([1, 8], [70, 20], [200, 3])]
+    want, weights = [], []
+    for p in ps:
+        w0 = p.c.weight.clone()
+        want.append(p.run(0.5).clone())
+        weights.append(p.c.weight.clone())
+        p.c.weight.copy_(w0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    outs = [torch.full_like(w, float("nan")) for w in want]
+    torch.cuda.synchronize()
+    for p, s, o in zip(ps, streams, outs):
+        p.run(0.5, out=o, stream=s)
+    torch.cuda.synchronize()
+    for p, o, w, cw in zip(ps, outs, want, weights):
+        n = int(p.off[-1])
+        assert torch.equal(o[:n], w[:n])
+        assert torch.equal(p.c.weight.view(torch.int32), cw.view(torch.int32))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_split_over_keys_and_many_sequences(dtype):
     check(Problem([5000], [1], 1, 128, 128, dtype, seed=250))          # one row, many ranges
