@@ -191,22 +191,25 @@ struct Share {
 int32_t pick_chunk(const AttnArgs &a, int32_t b0, int32_t n_seqs, int nq, int64_t slots,
                    int64_t fixed) {
   const int64_t H = a.p->num_heads;
-  int64_t most = 1, work = 0;
+  uint32_t tiles[kQcMaxSeqs];        // sequences with candidates: 128-key tiles,
+  int64_t ctas[kQcMaxSeqs];          // and CTAs per key range
+  int32_t m = 0;
+  int64_t most = 1, work = 0, all = 0;
   for (int32_t i = 0; i < n_seqs; ++i) {
     const int64_t n = a.coff[b0 + i + 1] - a.coff[b0 + i];
+    if (n == 0) continue;
     const int64_t t = (a.lens[b0 + i] + kQcKeyTile - 1) / kQcKeyTile;
-    const int64_t qt = (n + nq - 1) / nq;
-    if (qt == 0) continue;
+    tiles[m] = uint32_t(t > 1 ? t : 1);
+    ctas[m] = H * ((n + nq - 1) / nq);
     most = std::max(most, t);
-    work += H * qt * t;
+    work += ctas[m] * t;
+    all += ctas[m];
+    ++m;
   }
   auto count = [&](int64_t c) {
+    const uint32_t d = uint32_t(c);
     int64_t items = 0;
-    for (int32_t i = 0; i < n_seqs; ++i) {
-      const int64_t n = a.coff[b0 + i + 1] - a.coff[b0 + i];
-      const int64_t t = (a.lens[b0 + i] + kQcKeyTile - 1) / kQcKeyTile;
-      items += H * ((n + nq - 1) / nq) * std::max<int64_t>(1, (t + c - 1) / c);
-    }
+    for (int32_t i = 0; i < m; ++i) items += ctas[i] * ((tiles[i] + d - 1) / d);
     return items;
   };
   int64_t best = most, best_cost = INT64_MAX;
@@ -214,10 +217,13 @@ int32_t pick_chunk(const AttnArgs &a, int32_t b0, int32_t n_seqs, int nq, int64_
     // the shortest chunk whose CTAs fit `waves` rounds; waves = 0: no split
     int64_t c = most;
     if (waves > 0) {
-      int64_t lo = 1, hi = most;
+      // count(c) lies between work / c and work / c + all
+      const int64_t room = slots * waves;
+      int64_t lo = std::min(most, std::max<int64_t>(1, work / room)), hi = most;
+      if (room > all) hi = std::max(lo, std::min(most, work / (room - all) + 1));
       while (lo < hi) {
         const int64_t mid = (lo + hi) / 2;
-        if (count(mid) <= slots * waves)
+        if (count(mid) <= room)
           hi = mid;
         else
           lo = mid + 1;
