@@ -156,24 +156,18 @@ __device__ __forceinline__ void encode(const Eight<T> &x, float lo, float hi, ui
     word |= uint32_t(min(Eight<T>::rne(x.at(i), s, inv) + z, 15)) << (4 * (i >> 1) + 16 * (i & 1));
 }
 
-// Up to 64 lanes share a token's units (a unit is 8 values, K's first), so a
-// thread finds its token's place once for several of them.  units is a multiple
-// of 4: a quad never straddles two tokens.
-
+// A unit is 8 values of one head's key or value row; `lanes` threads (a multiple
+// of 4: a quad never straddles two tokens or two groups) share a token's units,
+// keys first, then values.
 struct RowThread {
   int64_t tok, row, pos;
-  int units, lanes, u0;
+  int u0;
   bool ok;
 };
-__host__ __device__ __forceinline__ int row_units(const QCacheView &c) {
-  return c.heads * ((c.d_qk + c.d_v) >> 3);
-}
 __device__ __forceinline__ RowThread row_thread(const QcRowsParams &p) {
   RowThread t;
-  t.units = row_units(p.cache);
-  t.lanes = t.units < 64 ? t.units : 64;
-  const int tpb = kRowThreads / t.lanes, tl = int(threadIdx.x) / t.lanes;
-  t.u0 = int(threadIdx.x) - tl * t.lanes;
+  const int tpb = kRowThreads / p.lanes, tl = int(threadIdx.x) / p.lanes;
+  t.u0 = int(threadIdx.x) - tl * p.lanes;
   t.tok = p.tok0 + int64_t(blockIdx.x) * tpb + tl;
   t.ok = tl < tpb && t.tok < p.tok_end;
   if (t.ok) {
@@ -184,44 +178,47 @@ __device__ __forceinline__ RowThread row_thread(const QcRowsParams &p) {
   }
   return t;
 }
-// A unit's place: element of the activation row, word of codes, parameter.
-struct UnitPlace {
-  bool is_v, first;
-  int e;
+// Walks a thread's units of one operand: its place in the cache.  Where the lanes
+// cover whole heads (64, 128, 256 values and 32) the next unit is a constant
+// away; finding each by itself (a division, 64-bit products) cost as much as the
+// quantisation.
+template <bool IS_V>
+struct UnitWalk {
   uint32_t *code;
   uint16_t *scale;
+  int u;
+  __device__ __forceinline__ static int words(const QCacheView &c) {   // per head and row
+    return (IS_V ? c.d_v : c.d_qk) >> 3;
+  }
+  __device__ __forceinline__ UnitWalk(const QcRowsParams &p, int64_t row, int u_) : u(u_) {
+    const QCacheView &c = p.cache;
+    const int w = words(c);
+    const int h = int(__umulhi(uint32_t(u * 8), IS_V ? p.v_magic : p.k_magic)), ew = u - h * w;
+    const int64_t at = int64_t(h) * c.rows + row;
+    code = (IS_V ? c.v_codes : c.k_codes) + (at * w + ew);
+    scale = (IS_V ? c.v_scales : c.k_scales) + (at * (w >> 2) + (ew >> 2));
+  }
+  __device__ __forceinline__ void next(const QcRowsParams &p, int64_t row) {
+    const int64_t step = IS_V ? p.v_step : p.k_step;   // heads x rows to the next unit, or 0
+    u += p.lanes;
+    if (step) {
+      code += step * words(p.cache);
+      scale += step * (words(p.cache) >> 2);
+    } else {
+      *this = UnitWalk(p, row, u);
+    }
+  }
 };
-__device__ __forceinline__ UnitPlace unit_place(const QcRowsParams &p, const RowThread &t, int u) {
-  const QCacheView &c = p.cache;
-  const int kw = c.heads * (c.d_qk >> 3);
-  UnitPlace q;
-  q.is_v = u >= kw;
-  const int w = q.is_v ? u - kw : u, d = q.is_v ? c.d_v : c.d_qk;
-  q.e = w * 8;
-  const int h = int(__umulhi(uint32_t(q.e), q.is_v ? p.v_magic : p.k_magic));
-  const int ew = w - h * (d >> 3);   // word of the head's row
-  const int64_t at = int64_t(h) * c.rows + t.row;
-  q.code = (q.is_v ? c.v_codes : c.k_codes) + (at * (d >> 3) + ew);
-  q.scale = (q.is_v ? c.v_scales : c.k_scales) + (at * (d >> 5) + (ew >> 2));
-  q.first = (ew & 3) == 0;
-  return q;
-}
 
-// Bound by its instructions (about 16 per value pair for extremes, scale and
-// codes); many warps of one unit at a time beat fewer with several: 8 x 4096
-// tokens, 8 heads of 128 stored and read back in 94 us against 98-105 us with two
-// or four units in flight per thread.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 6)
-    append_kernel(const __grid_constant__ QcRowsParams p) {
-  const RowThread t = row_thread(p);
-  if (!t.ok) return;
+template <typename T, bool IS_V>
+__device__ __forceinline__ void append_units(const QcRowsParams &p, const RowThread &t) {
   const uint32_t quad = 0xFu << (threadIdx.x & 28);   // other quads may have left the loop
-  for (int u = t.u0; u < t.units; u += t.lanes) {
-    const UnitPlace at = unit_place(p, t, u);
-    const T *row = static_cast<const T *>(at.is_v ? p.v : p.k) + t.tok * (at.is_v ? p.v_rs : p.k_rs);
+  const T *x0 = static_cast<const T *>(IS_V ? p.v : p.k) + t.tok * (IS_V ? p.v_rs : p.k_rs);
+  UnitWalk<IS_V> w(p, t.row, t.u0);
+  const int units = p.cache.heads * w.words(p.cache);
+  for (; w.u < units; w.next(p, t.row)) {
     Eight<T> x;
-    x.load(row + at.e, p.vec);
+    x.load(x0 + w.u * 8, p.vec);
     float lo, hi;
     x.extremes(lo, hi);
 #pragma unroll
@@ -231,9 +228,18 @@ __global__ void __launch_bounds__(kRowThreads, 6)
     }
     uint32_t word, param;
     encode<T>(x, lo, hi, word, param);
-    *at.code = word;
-    if (at.first) *at.scale = uint16_t(param);
+    *w.code = word;
+    if ((w.u & 3) == 0) *w.scale = uint16_t(param);
   }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads, 6)
+    append_kernel(const __grid_constant__ QcRowsParams p) {
+  const RowThread t = row_thread(p);
+  if (!t.ok) return;
+  append_units<T, false>(p, t);
+  append_units<T, true>(p, t);
   if (t.u0 == 0) {
     const QCacheView &c = p.cache;
     c.times[t.row] = p.ts[t.tok];
@@ -274,34 +280,42 @@ __device__ __forceinline__ void store_values(T *dst, uint32_t w, uint32_t param,
   }
 }
 
+template <typename T, bool IS_V>
+__device__ __forceinline__ void read_units(const QcRowsParams &p, const RowThread &t) {
+  constexpr int N = 4;   // units in flight per thread
+  T *row = static_cast<T *>(const_cast<void *>(IS_V ? p.v : p.k)) +
+           t.tok * (IS_V ? p.v_rs : p.k_rs);
+  UnitWalk<IS_V> at(p, t.row, t.u0);
+  const int units = p.cache.heads * at.words(p.cache);
+  while (at.u < units) {
+    uint32_t w[N], par[N];
+    const int u = at.u;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (at.u < units) {
+        w[k] = *at.code;
+        par[k] = *at.scale;
+        at.next(p, t.row);
+      }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (u + k * p.lanes < units)
+        store_values<T>(row + (u + k * p.lanes) * 8, w[k], par[k], p.vec);
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads)
     read_kernel(const __grid_constant__ QcRowsParams p) {
   const RowThread t = row_thread(p);
   if (!t.ok) return;
-  constexpr int N = 4;   // units in flight per thread
-  T *k_row = static_cast<T *>(const_cast<void *>(p.k)) + t.tok * p.k_rs;
-  T *v_row = static_cast<T *>(const_cast<void *>(p.v)) + t.tok * p.v_rs;
-  for (int u = t.u0; u < t.units; u += N * t.lanes) {
-    uint32_t w[N], par[N];
-    T *dst[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (u + k * t.lanes < t.units) {
-        const UnitPlace at = unit_place(p, t, u + k * t.lanes);
-        w[k] = *at.code;
-        par[k] = *at.scale;
-        dst[k] = (at.is_v ? v_row : k_row) + at.e;
-      }
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (u + k * t.lanes < t.units) store_values<T>(dst[k], w[k], par[k], p.vec);
-  }
+  read_units<T, false>(p, t);
+  read_units<T, true>(p, t);
 }
 
 template <typename T, bool APPEND>
 cudaError_t launch_rows_t(const QcRowsParams &p, cudaStream_t st) {
-  const int units = row_units(p.cache), tpb = kRowThreads / (units < 64 ? units : 64);
+  const int tpb = kRowThreads / p.lanes;
   const int64_t blocks = (p.tok_end - p.tok0 + tpb - 1) / tpb;
   if (blocks <= 0) return cudaSuccess;
   if constexpr (APPEND)

@@ -114,6 +114,12 @@ hstu_status_t run_rows(const hstu_qcache_t *cache, int32_t dtype, int32_t B, Tok
   p.k_magic = uint32_t((uint64_t(1) << 32) / uint32_t(cache->d_qk)) + 1;
   p.v_magic = uint32_t((uint64_t(1) << 32) / uint32_t(cache->d_v)) + 1;
   p.vec = aligned(k, 16) && aligned(v, 16) && k_rs % per16 == 0 && v_rs % per16 == 0;
+  const int kw = cache->d_qk / 8, vw = cache->d_v / 8;   // units per head
+  int64_t T = 0;
+  for (int32_t b = 0; b < B; ++b) T += tok(b);
+  p.lanes = std::min(T >= kQcManyRows ? 32 : 128, cache->num_heads * std::max(kw, vw));
+  p.k_step = p.lanes % kw == 0 ? p.lanes / kw * cache->rows : 0;
+  p.v_step = p.lanes % vw == 0 ? p.lanes / vw * cache->rows : 0;
   int64_t at = 0;
   for (int32_t b0 = 0; b0 < B; b0 += kQcMaxSeqs) {
     p.n_seqs = std::min(kQcMaxSeqs, B - b0);
