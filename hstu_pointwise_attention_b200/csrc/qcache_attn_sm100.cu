@@ -28,11 +28,20 @@
 //                swizzle.
 // The candidates' own pairs are one more tile, the first of the range that has
 // them: its keys are the candidates and only P's diagonal is kept.
-// Shared-memory traffic is what bounds the loop once the decoding keeps up (an
+// K stays out of shared memory, whose traffic would bound the loop (an
 // MMA with both operands there and N = 128 takes all of its 128 bytes a cycle):
-// keeping K out of it saves 32 KB written and 32 KB read of about 260 KB per tile
-// at D = 128, NQ = 128.
+// that saves 32 KB written and 32 KB read of about 260 KB per tile at D = 128,
+// NQ = 128.
 // Tensor memory: S^T slots, then O^T, then two K tiles (Cfg).
+//
+// Bound by the elementwise warps and their hand-overs: at 128 candidates one of the
+// two groups takes 3,600 cycles for its tile of 128 x 128 pairs and then waits about
+// 1,700 for the next S^T, whose slot it has only just freed (tensor memory has room
+// for two).  Measured (8 heads of 128): 8 histories of 4,096 with 256 candidates
+// and weights 77 us and 7 more to sum (445 TFLOP/s; issue slots 71 %, special
+// functions 41 %, tensor cores 24 % busy); 4 of 8,192 with 1,024 candidates 233 us
+// (590 TFLOP/s; 73 %, 32 %, 32 %).  Without the arithmetic of decoding and of the
+// elementwise pass the same pipeline takes 81 and 188 us in all.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -41,7 +50,6 @@
 
 namespace hstu {
 namespace qc_tc {
-
 
 constexpr int kTile = kQcKeyTile;
 constexpr int kThreads = 896;         // 4 control, 24 elementwise and decoding warps
@@ -62,6 +70,8 @@ struct Cfg {
   static constexpr int kParBytes = kPer == 1 ? 4 : 2 * kPer;   // K: parameters copied per thread
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kV = 2;
+  // Tiles of P: with two a warpgroup waited for the product of its last tile (4 x
+  // 1,024 candidates 240 us, with three 233).
   static constexpr int kP = 3;
   static constexpr int kPBytes = NQ / 64 * int(kBoxBytes);
   // Tiles of codes on their way: with few candidates the cache's bandwidth is
