@@ -340,8 +340,8 @@ cudaError_t launch_rows_t(const QcRowsParams &p, cudaStream_t st) {
 // the rows that share it the lowest are kept.  A kept row
 // below n stays where it is; kept rows at or behind n fill the holes below n,
 // both in ascending order, so the result does not depend on timing.
-// Bound by latency: 16 rounds of two barriers, then five passes over the keys; 4,096
-// rows 20 us, 32 sequences of up to 8,192 30 us.
+// Bound by latency: 16 rounds of one barrier, then five passes over the keys; 4,096
+// rows 19 us, 32 sequences of up to 8,192 25 us.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
@@ -406,11 +406,14 @@ __global__ void __launch_bounds__(kSelThreads)
   uint32_t prefix = 0, want = uint32_t(n);
   if (cached) {
     // Two bits at a time: count the keys at or above each of the three next
-    // larger candidates.  16 rounds of a few compares per key and one barrier.
-    if (tid < 6) hist[tid] = 0;
+    // larger candidates.  16 rounds of a few compares per key and one barrier, with
+    // three sets of counters: this round's, the last round's (still being read),
+    // and the next one's (zero).
+    if (tid < 9) hist[tid] = 0;
+    uint32_t *cnt = hist, *next = hist + 3, *last = hist + 6;
     __syncthreads();   // keys and counters
     uint32_t above = 0;   // keys above the final prefix
-    for (int shift = 30, round = 0; shift >= 0; shift -= 2, ++round) {
+    for (int shift = 30; shift >= 0; shift -= 2) {
       uint32_t c1 = 0, c2 = 0, c3 = 0;
       const uint32_t t1 = prefix | (1u << shift), t2 = prefix | (2u << shift),
                      t3 = prefix | (3u << shift);
@@ -423,7 +426,6 @@ __global__ void __launch_bounds__(kSelThreads)
       c1 = __reduce_add_sync(0xffffffffu, c1);
       c2 = __reduce_add_sync(0xffffffffu, c2);
       c3 = __reduce_add_sync(0xffffffffu, c3);
-      uint32_t *cnt = hist + (round & 1) * 3;
       if (lane < 3) atomicAdd(&cnt[lane], lane == 0 ? c1 : lane == 1 ? c2 : c3);
       __syncthreads();
       const uint32_t a1 = cnt[0], a2 = cnt[1], a3 = cnt[2];
@@ -439,10 +441,14 @@ __global__ void __launch_bounds__(kSelThreads)
       } else {
         above = a1;
       }
-      // the next round's counters, last read before this round's first barrier
-      if (tid < 3) hist[((round + 1) & 1) * 3 + tid] = 0;
-      __syncthreads();
+      // the last round's counters were read before this round's barrier
+      if (tid < 3) last[tid] = 0;
+      uint32_t *const spare = last;
+      last = cnt;
+      cnt = next;
+      next = spare;
     }
+    __syncthreads();   // the counters have been read: hist is free
     want = uint32_t(n) - above;
   } else {
     // Too long for shared memory: 8-bit digits, highest first, from a histogram.
@@ -515,9 +521,10 @@ __global__ void __launch_bounds__(kSelThreads)
 // its parameter); consecutive lanes write consecutive groups.  In place only
 // the holes are written, and every source lies at or behind `keep`.  Bound by
 // latency of scattered 16-byte reads: halving 32 histories of 1,024 to 8,192 rows, 8
-// heads of 128, takes 31 us, with 120 MB at the memory.
+// heads of 128, takes 29 us, with 120 MB at the memory.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
+constexpr int kMoveUnits = 2;   // 1 and 4: a microsecond or two longer, 8: four
 
 __global__ void __launch_bounds__(kMoveThreads)
     move_kernel(const __grid_constant__ QcEvictParams p) {
@@ -544,14 +551,33 @@ __global__ void __launch_bounds__(kMoveThreads)
     const uint16_t *as = part ? a.v_scales : a.k_scales;
     uint16_t *bs = part ? b.v_scales : b.k_scales;
     const int per_head = rows * gs, all = per_head * a.heads;
-    for (int x = threadIdx.x; x < all; x += kMoveThreads) {
-      const int h = x / per_head, y = x - h * per_head, r = y / gs, g = y - r * gs;
-      const int32_t m = map[r];
-      if (p.in_place && m == r0 + r) continue;
-      const int64_t from = (int64_t(h) * a.rows + sq.row + m) * gs + g;
-      const int64_t to = (int64_t(h) * b.rows + sq.dst_row + r0 + r) * gs + g;
-      bc[to] = ac[from];
-      bs[to] = as[from];
+    // kMoveUnits groups in flight per thread
+#pragma unroll 1
+    for (int x0 = threadIdx.x; x0 < all; x0 += kMoveUnits * kMoveThreads) {
+      int64_t to[kMoveUnits];
+      uint4 code[kMoveUnits];
+      uint16_t par[kMoveUnits];
+#pragma unroll
+      for (int k = 0; k < kMoveUnits; ++k) {
+        const int x = x0 + k * kMoveThreads;
+        to[k] = -1;
+        if (x < all) {
+          const int h = x / per_head, y = x - h * per_head, r = y / gs, g = y - r * gs;
+          const int32_t m = map[r];
+          if (!(p.in_place && m == r0 + r)) {
+            const int64_t from = (int64_t(h) * a.rows + sq.row + m) * gs + g;
+            to[k] = (int64_t(h) * b.rows + sq.dst_row + r0 + r) * gs + g;
+            code[k] = ac[from];
+            par[k] = as[from];
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kMoveUnits; ++k)
+        if (to[k] >= 0) {
+          bc[to[k]] = code[k];
+          bs[to[k]] = par[k];
+        }
     }
   }
 }
