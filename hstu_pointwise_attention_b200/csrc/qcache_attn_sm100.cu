@@ -35,13 +35,13 @@
 // Tensor memory: S^T slots, then O^T, then two K tiles (Cfg).
 //
 // Bound by the elementwise warps and their hand-overs: at 128 candidates one of the
-// two groups takes 3,600 cycles for its tile of 128 x 128 pairs and then waits about
-// 1,700 for the next S^T, whose slot it has only just freed (tensor memory has room
-// for two).  Measured (8 heads of 128): 8 histories of 4,096 with 256 candidates
-// and weights 77 us and 7 more to sum (445 TFLOP/s; issue slots 71 %, special
-// functions 41 %, tensor cores 24 % busy); 4 of 8,192 with 1,024 candidates 233 us
-// (590 TFLOP/s; 73 %, 32 %, 32 %).  Without the arithmetic of decoding and of the
-// elementwise pass the same pipeline takes 81 and 188 us in all.
+// two groups takes 3,600 cycles for its tile of 128 x 128 pairs and then waits for
+// the next S^T (tensor memory has room for two, so one is made while the other is
+// read; a slot is free once its last columns are in registers: with the wait for P
+// in its place 8 x 256 took 85.5 us and 4 x 1,024 233).  Measured (8 heads of 128): 8
+// histories of 4,096 with 256 candidates and weights 75 us and 7 more to sum (455
+// TFLOP/s; issue slots 71 %, special functions 41 %, tensor cores 24 % busy); 4 of
+// 8,192 with 1,024 candidates 227 us (605 TFLOP/s; 73 %, 32 %, 32 %).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -120,6 +120,7 @@ struct Smem {
   uint64_t k_full[2], k_empty[2], v_full[C::kV], v_empty[C::kV];
   uint64_t s_full[3];             // with three slots a warpgroup takes every other round of one:
                                   // the commits are in order, so the round between is over by then
+  uint64_t s_empty[3];            // the warpgroup has read S^T
   uint64_t p_full[C::kP], p_empty[C::kP];
   uint64_t bias_full[kBias], bias_empty[kBias];
   uint64_t q_full, o_full, drain;
@@ -424,7 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.v_full[i], C::kDecThreads);
       mbar_init(&sm.v_empty[i], 1);
     }
-    for (int i = 0; i < 3; ++i) mbar_init(&sm.s_full[i], 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.s_empty[i], 128 * C::kHalves);
+    }
     for (int i = 0; i < C::kP; ++i) {
       mbar_init(&sm.p_full[i], 128 * C::kHalves);
       mbar_init(&sm.p_empty[i], 1);
@@ -455,16 +459,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc_o = idesc_bf16(128, NQ, true, true);
         const uint64_t dq = sdesc_sw128(smem_u32(sm.q), 16, 1024);
         bool ok = wait_cta(&sm.q_full, 0, &sm.abort, p.wait);
-        int ns = 0, no = 0, s_slot = 0;   // next S^T, next O^T; ns % kS
+        int ns = 0, no = 0;               // next S^T, next O^T
+        int s_slot = 0, s_par = 0;        // ns % kS, (ns / kS) & 1
         int p_slot = 0, p_par = 0;        // no % kP, (no / kP) & 1
         uint32_t idle = 0;
         uint64_t t0 = 0;
         while (ok && no < n_all) {
-          // S^T first: the warpgroup that takes it may be waiting, and its columns
-          // are free once P of the tile that had them is there
-          if (ns < n_all && ns <= no + C::kS &&
-              mbar_test_wait(&sm.k_full[ns & 1], (ns >> 1) & 1) &&
-              (ns < no + C::kS || mbar_test_wait(&sm.p_full[p_slot], p_par))) {
+          // S^T first: the warpgroup that takes it may be waiting
+          if (ns < n_all && mbar_test_wait(&sm.k_full[ns & 1], (ns >> 1) & 1) &&
+              (ns < C::kS || mbar_test_wait(&sm.s_empty[s_slot], s_par ^ 1))) {
             tc_fence_after();
             const uint32_t k = tmem + C::kK + (ns & 1) * (D / 2);
 #pragma unroll 2
@@ -473,7 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                       idesc_s, kk > 0);
             umma_commit(&sm.s_full[s_slot]);
             umma_commit(&sm.k_empty[ns & 1]);
-            s_slot = s_slot == C::kS - 1 ? 0 : s_slot + 1;
+            if (++s_slot == C::kS) {
+              s_slot = 0;
+              s_par ^= 1;
+            }
             ++ns;
             idle = 0;
           } else if (no < ns && mbar_test_wait(&sm.p_full[p_slot], p_par) &&
@@ -666,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(v4[0], v4[1], v4[2], v4[3]);
         }
         tc_fence_before();
+        mbar_arrive(&sm.s_empty[0]);
         fence_proxy_async_smem();
         mbar_arrive(&sm.p_full[0]);
         continue;
@@ -697,11 +704,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #define HSTU_QC_CHUNK(M_)                                                                       \
   chunk<D, NQ, WEIGHTS, M_>(r, pk, sm, c0, a, c, c2, t, tk, rt, half, p.sub_bits, p.nb_t, \
                         p.cand_ts + q_row, nq, wsum)
+      const int c_end = min(hf * 64 + 64, nq);
+      if (c_end <= hf * 64) mbar_arrive(&sm.s_empty[slot]);   // no candidate in this half
 #pragma unroll 1
-      for (int c0 = hf * 64; c0 < min(hf * 64 + 64, nq); c0 += 16) {
+      for (int c0 = hf * 64; c0 < c_end; c0 += 16) {
         uint32_t r[16], pk[8];
         tmem_ld16(s_col + c0, r);
         tmem_wait_ld(r);
+        if (c0 + 16 >= c_end) {   // all of S^T is in registers: its columns are free
+          tc_fence_before();
+          mbar_arrive(&sm.s_empty[slot]);
+        }
         if (mode == kTimeOne)
           HSTU_QC_CHUNK(kTimeOne);
         else if (mode == kTimeTwo)
@@ -718,7 +731,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
       }
 #undef HSTU_QC_CHUNK
-      tc_fence_before();          // S^T has been read
       fence_proxy_async_smem();   // P^T is written
       mbar_arrive(&sm.p_full[p_slot]);
       if constexpr (WEIGHTS) {
