@@ -178,11 +178,11 @@ def _host_i32(a) -> Optional[np.ndarray]:
 
 def _row_stride(t: torch.Tensor, H: int, d: int, name: str) -> int:
     """t is [T, H, d] (or a [T, H*d] view) with contiguous heads."""
+    if t.shape[1:] == (H, d) and t.is_contiguous():
+        return H * d
     if t.shape[0] == 0 and tuple(t.shape[1:]) in ((H, d), (H * d,)):
         return H * d        # no rows: strides carry no meaning
     if t.dim() == 3:
-        if t.shape[1:] == (H, d) and t.is_contiguous():
-            return H * d
         if t.shape[1:] != (H, d) or t.stride()[1:] != (d, 1):
             raise ValueError(f"{name}: expected [T, {H}, {d}] with contiguous heads")
     elif t.dim() == 2:
@@ -523,7 +523,8 @@ class _Launch:
     def __enter__(self):
         if self._ctx is not None:
             self._ctx.__enter__()
-        return torch.cuda.current_stream(self._index).cuda_stream
+        # the raw stream without a Stream object around it (a microsecond per call)
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def __exit__(self, *exc):
         if self._ctx is not None:
@@ -593,9 +594,9 @@ def qcache_append(cache, k, v, timestamps, tok_offsets, rows, pos, *, stream=Non
 
 def qcache_read(cache, rows, lens, *, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """hstu_qcache_read: (k, v) [sum lens, H, d], the values that rows stand for."""
-    lens = _host_i64(lens)
+    lens = _host_vec(lens, len(lens), np.int64, "lens")
     rows = _host_vec(rows, len(lens), np.int64, "rows")
-    T = int(lens.sum())
+    T = sum(lens.tolist())
     with _Launch(_cuda_index(cache.k_codes, k, v), stream) as st:
         if k is None:
             k = torch.empty((T, cache.num_heads, cache.d_qk), dtype=dtype, device=cache.device)
