@@ -40,8 +40,8 @@
 // read; a slot is free once its last columns are in registers: with the wait for P
 // in its place 8 x 256 took 85.5 us and 4 x 1,024 233).  Measured (8 heads of 128): 8
 // histories of 4,096 with 256 candidates and weights 75 us and 7 more to sum (455
-// TFLOP/s; issue slots 71 %, special functions 41 %, tensor cores 24 % busy); 4 of
-// 8,192 with 1,024 candidates 227 us (605 TFLOP/s; 73 %, 32 %, 32 %).
+// TFLOP/s; issue slots 74 %, special functions 42 %, tensor cores 24 % busy); 4 of
+// 8,192 with 1,024 candidates 227 us (605 TFLOP/s; 78 %, 33 %, 33 %).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
