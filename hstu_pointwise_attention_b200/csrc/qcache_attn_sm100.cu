@@ -26,8 +26,10 @@
 //                (lane = key), from where the MMA takes it;
 //   and as many for values the same way, V to shared memory in the 128-byte
 //                swizzle.
-// The candidates' own pairs are one more tile, the first of the range that has
-// them: its keys are the candidates and only P's diagonal is kept.
+// The candidates' own pairs stay out of the products: the sum over keys of a
+// tile adds 0 v_i to every other candidate, so an infinity in one candidate's v
+// would reach all of them.  The elementwise warps make SiLU(x_ii) while they wait
+// for the first S^T, and SiLU(x_ii) v_i joins O where it is written.
 // K stays out of shared memory, whose traffic would bound the loop (an
 // MMA with both operands there and N = 128 takes all of its 128 bytes a cycle):
 // that saves 32 KB written and 32 KB read of about 260 KB per tile at D = 128,
@@ -115,6 +117,7 @@ struct Smem {
   KeyBias bias[kBias];
   alignas(16) float tqd[NQ];      // candidates' times relative to the earliest of them
   alignas(16) float live[NQ];     // 1 for a candidate, 0 for padding
+  float own[NQ];                  // SiLU of the candidates' own pairs, 0 outside the first key range
   float tbl_t[kTblT];
   int64_t tq_min, tq_max;
   uint64_t k_full[2], k_empty[2], v_full[C::kV], v_empty[C::kV];
@@ -167,6 +170,12 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t *v) {
 // The time bias of one pair, bucket by bucket (times too far apart for floats).
 __device__ __noinline__ float time_bias_int(int64_t dt, const float *rt, int sub_bits, int nb_t) {
   return qc_bias(rt[time_bucket_i64(dt, sub_bits, nb_t)]);
+}
+
+// acc plus the products of two bf16 pairs.
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
+  acc = fmaf(__uint_as_float(a << 16), __uint_as_float(b << 16), acc);
+  return fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u), acc);
 }
 
 // 16 candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum
@@ -247,14 +256,13 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8]
 template <int D, int NQ, bool IS_V>
 __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> &sm,
                                              const QcItem &it, const QcAttnSeq &sq, int h,
-                                             int64_t q_row, int nq, uint32_t tmem, int dw,
-                                             int lane) {
+                                             uint32_t tmem, int dw, int lane) {
   using C = Cfg<D, NQ>;
   constexpr int G = C::kG, kPer = C::kPer, kDecThreads = C::kDecThreads;
   constexpr int kStep = kDecThreads / G;         // V: rows between a thread's groups
   const QCacheView &cv = p.cache;
   const int dt = dw * 32 + lane, hx = dw >> 2;
-  const int n_tiles = it.t1 - it.t0, self = it.split == 0 ? 1 : 0, n_all = n_tiles + self;
+  const int n_tiles = it.t1 - it.t0;
   const int row = !IS_V    ? (dw & 3) * 32 + lane
                   : G == 4 ? dw * 8 + ((lane >> 4) << 2) + ((lane >> 1) & 3)
                            : dw * 16 + (lane >> 1);
@@ -326,30 +334,9 @@ __device__ __forceinline__ void decode_tiles(const QcAttnParams &p, Smem<D, NQ> 
     }
     mbar_arrive(&full[buf]);
   };
-  if (self) {   // tile 0: the candidates' own keys or values, bf16 already
-    const __nv_bfloat16 *own = static_cast<const __nv_bfloat16 *>(IS_V ? p.v : p.k) +
-                               q_row * (IS_V ? p.v_rs : p.k_rs) + h * D + g * 32;
-#pragma unroll 1
-    for (int x = 0; x < kPer; ++x) {
-      const int i = row + (IS_V ? x * kStep : 0);
-      uint32_t o[16];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (i < nq)
-          w = load_row8(own + i * (IS_V ? p.v_rs : p.k_rs) + (IS_V ? 0 : x * 32) + e * 8, p.vec);
-        o[4 * e] = w.x;
-        o[4 * e + 1] = w.y;
-        o[4 * e + 2] = w.z;
-        o[4 * e + 3] = w.w;
-      }
-      put(0, x, o);
-    }
-    done(0);
-  }
   int st = 0;
 #pragma unroll 1
-  for (int n = self; n < n_all; ++n) {
+  for (int n = 0; n < n_tiles; ++n) {
     const int buf = n & 1;
     cp_async_wait<C::kStages - 1>();
     if (IS_V) __syncwarp();   // the row's parameters came through another lane of this warp
@@ -414,9 +401,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float half = WEIGHTS ? 1.0f : 0.5f;     // the tanh form works on x / 2
   constexpr uint32_t kQHalf = NQ * 128;         // bytes of one 64-column box of Q
 
-  const int self = it.split == 0 ? 1 : 0;        // tile 0 is the candidates' own
-  const int n_all = n_tiles + self;
-
   if (tid == 64) {
     mbar_init(&sm.q_full, 32 * C::kElemWarps);
     for (int i = 0; i < 2; ++i) {
@@ -464,9 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int p_slot = 0, p_par = 0;        // no % kP, (no / kP) & 1
         uint32_t idle = 0;
         uint64_t t0 = 0;
-        while (ok && no < n_all) {
+        while (ok && no < n_tiles) {
           // S^T first: the warpgroup that takes it may be waiting
-          if (ns < n_all && mbar_test_wait(&sm.k_full[ns & 1], (ns >> 1) & 1) &&
+          if (ns < n_tiles && mbar_test_wait(&sm.k_full[ns & 1], (ns >> 1) & 1) &&
               (ns < C::kS || mbar_test_wait(&sm.s_empty[s_slot], s_par ^ 1))) {
             tc_fence_after();
             const uint32_t k = tmem + C::kK + (ns & 1) * (D / 2);
@@ -616,72 +600,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = (warp - 4) >> 2, par = w / C::kHalves, hf = w % C::kHalves, quad = warp & 3;
     const int key = quad * 32 + lane;
     const uint32_t lanes = tmem + (uint32_t(quad * 32) << 16);
+    // The warpgroup's 32 candidates of Q and of the output: a thread takes chunk u (8
+    // features) of rows r0 + x kRows.
+    constexpr int kRowLanes = D / 8, kRows = 128 / kRowLanes;
+    const int wt = (tid - 128) & 127, u = wt % kRowLanes, r0 = w * 32 + wt / kRowLanes;
     {
       // the queries, K-major in the 128-byte swizzle; rows behind the last are zero
-      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + q_row * p.q_rs + h * D;
-#pragma unroll 4
-      for (int x = tid - 128; x < NQ * (D / 8); x += 32 * C::kElemWarps) {
-        const int r = x / (D / 8), u = x % (D / 8);
+      const __nv_bfloat16 *q =
+          static_cast<const __nv_bfloat16 *>(p.q) + q_row * p.q_rs + h * D + u * 8;
+#pragma unroll
+      for (int x = 0; x < 32 / kRows; ++x) {
+        const int r = r0 + x * kRows;
         uint4 val = make_uint4(0, 0, 0, 0);
-        if (r < nq) val = load_row8(q + r * p.q_rs + u * 8, p.vec);
+        if (r < nq) val = load_row8(q + r * p.q_rs, p.vec);
         *reinterpret_cast<uint4 *>(sm.q + (u >> 3) * kQHalf + r * 128 +
                                    (((u & 7) ^ (r & 7)) << 4)) = val;
       }
       fence_proxy_async_smem();
       mbar_arrive(&sm.q_full);
     }
+    // the candidates' own pairs (distance 0 in position and time)
+    if (it.split == 0) {
+      const __nv_bfloat16 *k =
+          static_cast<const __nv_bfloat16 *>(p.k) + q_row * p.k_rs + h * D + u * 8;
+      const float b0 = qc_bias(rp[0] + rt[0]);
+#pragma unroll
+      for (int x = 0; x < 32 / kRows; ++x) {
+        const int r = r0 + x * kRows;
+        uint4 kw = make_uint4(0, 0, 0, 0);
+        if (r < nq) kw = load_row8(k + r * p.k_rs, p.vec);
+        const uint4 qw = *reinterpret_cast<const uint4 *>(
+            sm.q + (u >> 3) * kQHalf + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+        float dot = dot2(qw.x, kw.x, 0.f);
+        dot = dot2(qw.y, kw.y, dot);
+        dot = dot2(qw.z, kw.z, dot);
+        dot = dot2(qw.w, kw.w, dot);
+#pragma unroll
+        for (int m = 1; m < kRowLanes; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+        const float xs = fmaf(p.alpha, dot, b0);
+        if (u == 0) sm.own[r] = xs * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * xs));
+      }
+    }
     const float a = half * p.alpha;
     bool ok = true;
     int slot = par, round = 0;           // n % kS, n / kS
     int p_slot = par, p_round = 0;       // n % kP, n / kP
 #pragma unroll 1
-    for (int n = par; n < n_all;
+    for (int n = par; n < n_tiles;
          n += 2, slot += 2, slot -= slot >= C::kS ? (++round, C::kS) : 0, p_slot += 2,
              p_slot -= p_slot >= C::kP ? (++p_round, C::kP) : 0) {
       const uint32_t s_col = lanes + slot * NQ;
       uint8_t *pt = sm.p[p_slot] + hf * kBoxBytes + key * 128;
-      if (n < self) {
-        // the candidates' own pairs: bias of distance 0, P's diagonal
-        ok = wait_cta_warp(&sm.s_full[0], 0, &sm.abort, p.wait);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t bits = 0;
-        // (candidates of this warpgroup's half: its diagonal lies in quads 2 hf, 2 hf + 1)
-        if (quad >> 1 == hf && quad * 32 < nq) {
-          uint32_t sv = 0;
-#pragma unroll
-          for (int e0 = 0; e0 < 32; e0 += 16) {
-            uint32_t r[16];
-            tmem_ld16(s_col + quad * 32 + e0, r);
-            tmem_wait_ld(r);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sv = lane == e0 + e ? r[e] : sv;
-          }
-          const float x = fmaf(p.alpha, __uint_as_float(sv), qc_bias(rp[0]) + qc_bias(rt[0]));
-          const float ps = x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
-          bits = key < nq ? pack_bf16x2(ps, 0.f) : 0u;
-        }
-        bits = key & 1 ? bits << 16 : bits;
-        const int at = key - hf * 64;   // its column in this half (other quads: bits are 0)
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint32_t v4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v4[e] = (at >> 1) == u * 4 + e ? bits : 0u;
-          *reinterpret_cast<uint4 *>(pt + ((u ^ (key & 7)) << 4)) =
-              make_uint4(v4[0], v4[1], v4[2], v4[3]);
-        }
-        tc_fence_before();
-        mbar_arrive(&sm.s_empty[0]);
-        fence_proxy_async_smem();
-        mbar_arrive(&sm.p_full[0]);
-        continue;
-      }
-      const int m = n - self;                       // tile of the cache
-      const int32_t j = (it.t0 + m) * kTile + key;
-      const int bs = m % kBias;
+      const int32_t j = (it.t0 + n) * kTile + key;
+      const int bs = n % kBias;
       const KeyBias &kb = sm.bias[bs];
-      ok = wait_cta_warp(&sm.bias_full[bs], (m / kBias) & 1, &sm.abort, p.wait);
+      ok = wait_cta_warp(&sm.bias_full[bs], (n / kBias) & 1, &sm.abort, p.wait);
       if (!ok) break;
       const int mode = kb.mode[quad];
       const float c = kb.c[key];
@@ -747,35 +720,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && quad * 32 < D) {
 #pragma unroll 1
       for (int c0 = c_first; c0 < c_end; c0 += 16) {
-        uint32_t r[16];
-        tmem_ld16(lanes + C::kO + c0, r);
-        tmem_wait_ld(r);
+        uint32_t r[16] = {};
+        if (n_tiles > 0) {   // without a tile nothing has written O
+          tmem_ld16(lanes + C::kO + c0, r);
+          tmem_wait_ld(r);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) stage[(c0 + e) * D + key] = __uint_as_float(r[e]);
       }
     }
     named_bar_sync(3 + w, 128);
     if (ok) {
-      constexpr int kRowLanes = D / 4, kRows = 128 / kRowLanes;   // 4 features per lane
-      const int wt = (tid - 128) & 127, e = (wt % kRowLanes) * 4;
+      const __nv_bfloat16 *v =
+          static_cast<const __nv_bfloat16 *>(p.v) + q_row * p.v_rs + h * D + u * 8;
 #pragma unroll 2
-      for (int i = c_first + wt / kRowLanes; i < c_end; i += kRows) {
-        const float4 o = *reinterpret_cast<const float4 *>(stage + i * D + e);
+      for (int i = r0; i < c_end; i += kRows) {
+        const float4 oa = *reinterpret_cast<const float4 *>(stage + i * D + u * 8);
+        const float4 ob = *reinterpret_cast<const float4 *>(stage + i * D + u * 8 + 4);
+        float o[8] = {oa.x, oa.y, oa.z, oa.w, ob.x, ob.y, ob.z, ob.w};
+        if (it.split == 0) {
+          const uint4 vw = load_row8(v + i * p.v_rs, p.vec);
+          const uint32_t vs[4] = {vw.x, vw.y, vw.z, vw.w};
+          const float own = sm.own[i];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            o[e] = fmaf(own, __uint_as_float(e & 1 ? vs[e / 2] & 0xFFFF0000u : vs[e / 2] << 16),
+                        o[e]);
+        }
         if (sq.splits > 1) {
-          *reinterpret_cast<float4 *>(
-              p.acc + ((sq.acc0 + (int64_t(it.split) * sq.n + i0 + i) * H + h) * D + e)) = o;
+          float *dst =
+              p.acc + ((sq.acc0 + (int64_t(it.split) * sq.n + i0 + i) * H + h) * D + u * 8);
+          reinterpret_cast<float4 *>(dst)[0] = make_float4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<float4 *>(dst)[1] = make_float4(o[4], o[5], o[6], o[7]);
         } else {
           __nv_bfloat16 *dst =
-              static_cast<__nv_bfloat16 *>(p.out) + (q_row + i) * p.o_rs + h * D + e;
-          const uint2 w = make_uint2(pack_bf16x2(o.x * p.scale, o.y * p.scale),
-                                     pack_bf16x2(o.z * p.scale, o.w * p.scale));
+              static_cast<__nv_bfloat16 *>(p.out) + (q_row + i) * p.o_rs + h * D + u * 8;
+          uint32_t ow[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            ow[e] = pack_bf16x2(o[2 * e] * p.scale, o[2 * e + 1] * p.scale);
           if (p.vec) {
-            *reinterpret_cast<uint2 *>(dst) = w;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
           } else {
-            reinterpret_cast<uint16_t *>(dst)[0] = uint16_t(w.x);
-            reinterpret_cast<uint16_t *>(dst)[1] = uint16_t(w.x >> 16);
-            reinterpret_cast<uint16_t *>(dst)[2] = uint16_t(w.y);
-            reinterpret_cast<uint16_t *>(dst)[3] = uint16_t(w.y >> 16);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint16_t *>(dst)[e] = uint16_t(ow[e / 2] >> (16 * (e & 1)));
           }
         }
       }
@@ -784,9 +773,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================== decoding =====================
     const int dw = warp - 4 - C::kElemWarps;
     if (dw < C::kDecWarps)
-      decode_tiles<D, NQ, false>(p, sm, it, sq, h, q_row, nq, tmem, dw, lane);
+      decode_tiles<D, NQ, false>(p, sm, it, sq, h, tmem, dw, lane);
     else
-      decode_tiles<D, NQ, true>(p, sm, it, sq, h, q_row, nq, tmem, dw - C::kDecWarps, lane);
+      decode_tiles<D, NQ, true>(p, sm, it, sq, h, tmem, dw - C::kDecWarps, lane);
   }
   tc_fence_before();
   __syncthreads();
