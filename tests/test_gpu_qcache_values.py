@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_qcache import Problem
+import qcache_ref as R
+from test_gpu_qcache import Problem, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +58,85 @@ def test_a_candidates_own_query_and_key_stay_its_own(n, what):
         assert torch.isnan(got[i, 0]).all()
         got[i, 0] = clean[i, 0]
         assert torch.equal(bits(got), bits(clean)), i
+
+
+# The error of P beyond its logit's, by the kernel that takes the call: CUDA cores,
+# a few float32 roundings; bf16 kernels, P rounded to bf16 ahead of its product,
+# its exponential and quotient good to 2^-22 each.  The weights come from P ahead
+# of its rounding.
+U_P = {"simt": 16 * R.F32_U, "bf16": R.BF16_U + 2.0 ** -20}
+U_W = {"simt": 16 * R.F32_U, "bf16": 2.0 ** -20}
+
+
+def agree(got, ref, tol, what):
+    """NaN where the definition has NaN, the same infinities, and the rest within tol."""
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(ref), err_msg=what)
+    inf = np.isinf(ref)
+    np.testing.assert_array_equal(got[inf], ref[inf], err_msg=what)
+    fin = np.isfinite(ref)
+    assert np.all(np.isfinite(got[fin])), what
+    assert np.all(np.abs(got - ref)[fin] <= tol[fin]), \
+        (what, float((np.abs(got - ref) - tol)[fin].max()))
+
+
+def check_values(p, decay=0.75, impl="auto"):
+    """Outputs and weights against float64, non-finite ones among them."""
+    kind = "bf16" if p.dtype == "bf16" and impl == "auto" and p.dk == p.dv and \
+        p.dk in (64, 128) else "simt"
+    u_out = R.BF16_U if p.dtype == "bf16" else R.F32_U
+    w0 = p.c.weight.clone()
+    got, w = run(p, decay, w0, impl=impl)
+    got, w, w0 = f64(got), f64(w), f64(w0)
+    with np.errstate(invalid="ignore", over="ignore"):
+        outs = [x[3][:2] + (x[2],) for x in p.reference((U_P[kind], 0.0))]
+        steps = [x[3][2:] + (x[1],) for x in p.reference((U_W[kind], 0.0))]
+        for (ref, bound, a), (step, wb, sl) in zip(outs, steps):
+            agree(got[a], ref, bound + u_out * (np.abs(ref) + bound), "out")
+            if decay is None:
+                np.testing.assert_array_equal(w[sl], w0[sl])
+            else:
+                want = decay * w0[sl] + step
+                agree(w[sl], want, wb + 2 * R.F32_U * (np.abs(want) + wb), "weight")
+    return got, w
+
+
+def seen_buckets(p):
+    """Position and time buckets that the first sequence's pairs meet, by how often."""
+    sl = slice(int(p.rows[0]), int(p.rows[0] + p.lens[0]))
+    dp = np.clip(int(p.cand_pos[0]) - p.c.pos[sl].cpu().numpy().astype(np.int64), 0,
+                 p.rab_p.shape[-1] - 1)
+    bt = R.time_bucket(p.t[:p.n[0], None] - p.c.times[sl].cpu().numpy()[None], p.sub,
+                       p.rab_t.shape[-1])
+    order = lambda x: [b for _, b in sorted(zip(*np.unique(x, return_counts=True)[::-1]))]
+    return order(dp), order(bt)
+
+
+def problem(n, d, dtype, t_cand, seed):
+    return Problem([300, 0, 40], [n, 5, 3], 2, d, d, dtype, seed=seed, nb=(40, 400),
+                   t_cand=t_cand)
+
+
+KINDS = [("bf16", "auto", n) for n in (8, 20, 64, 70, 130)] + [("bf16", "simt", 20),
+                                                               ("f32", "auto", 20)]
+
+
+@pytest.mark.parametrize("dtype,impl,n", KINDS)
+@pytest.mark.parametrize("t_cand", [None, "apart"])
+def test_a_nan_table_entry_reaches_its_pairs_and_no_other(dtype, impl, n, t_cand):
+    for table in ("rab_p", "rab_t"):
+        p = problem(n, 128, dtype, t_cand, 540 + n)
+        pos, tim = seen_buckets(p)
+        getattr(p, table)[pos[1] if table == "rab_p" else tim[0]] = np.nan
+        got, w = check_values(p, impl=impl)
+        assert np.isnan(got).any() and np.isnan(w).any()
+
+
+@pytest.mark.parametrize("dtype,impl,n", KINDS)
+@pytest.mark.parametrize("t_cand", [None, "apart"])
+def test_a_nan_query_reaches_its_row_and_every_weight(dtype, impl, n, t_cand):
+    for i in (0, 1, 2, 3, n - 1):
+        p = problem(n, 64, dtype, t_cand, 550 + n)
+        p.q[i, 1, 2] = float("nan")
+        got, w = check_values(p, impl=impl)
+        sl = slice(int(p.rows[0]), int(p.rows[0] + p.lens[0]))
+        assert np.isnan(w[sl]).all() and np.isnan(got[i, 1]).all()
