@@ -116,7 +116,6 @@ struct Smem {
   alignas(16) uint8_t v_scales[C::kStages][C::kScaleBytes];
   KeyBias bias[kBias];
   alignas(16) float tqd[NQ];      // candidates' times relative to the earliest of them
-  alignas(16) float live[NQ];     // 1 for a candidate, 0 for padding
   float own[NQ];                  // SiLU of the candidates' own pairs, 0 outside the first key range
   float tbl_t[kTblT];
   int64_t tq_min, tq_max;
@@ -179,7 +178,7 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
 }
 
 // 16 candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum
-// of |P| over the live ones.  With weights (returned in float32) SiLU is
+// of |P| over the candidates.  With weights (returned in float32) SiLU is
 // x / (1 + 2^y), y = -x log2 e, good to a few 2^-22; else h (1 + tanh h) with
 // h = x / 2, half the special-function work, its error below P's rounding.  A
 // reciprocal for every pair: two pairs that share one are NaN together, and sharing
@@ -217,11 +216,10 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8]
     if constexpr (WEIGHTS) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) pv[u] = x[u] * rcp_approx(1.0f + ex2_approx(kL * x[u]));
-      const float4 live = *reinterpret_cast<const float4 *>(&sm.live[c0 + e]);   // 1 or 0
-      wsum = fmaf(fabsf(pv[0]), live.x, wsum);
-      wsum = fmaf(fabsf(pv[1]), live.y, wsum);
-      wsum = fmaf(fabsf(pv[2]), live.z, wsum);
-      wsum = fmaf(fabsf(pv[3]), live.w, wsum);
+      // padding has the bias of its key: left out, since 0 times it could be NaN
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c0 + e + u < nq) wsum += fabsf(pv[u]);
     } else {
 #pragma unroll
       for (int u = 0; u < 4; ++u) pv[u] = fmaf(x[u], tanh_approx(x[u]), x[u]);   // x halved
@@ -509,7 +507,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NQ / 32; ++i) {
           sm.tqd[i * 32 + lane] = float(t[i] - lo);
-          sm.live[i * 32 + lane] = i * 32 + lane < nq ? 1.0f : 0.0f;
         }
         if (lane == 0) {
           sm.tq_min = lo;

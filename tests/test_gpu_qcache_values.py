@@ -140,3 +140,16 @@ def test_a_nan_query_reaches_its_row_and_every_weight(dtype, impl, n, t_cand):
         got, w = check_values(p, impl=impl)
         sl = slice(int(p.rows[0]), int(p.rows[0] + p.lens[0]))
         assert np.isnan(w[sl]).all() and np.isnan(got[i, 1]).all()
+
+
+@pytest.mark.parametrize("dtype,impl,n", KINDS)
+@pytest.mark.parametrize("t_cand", [None, "apart"])
+def test_an_infinite_table_entry_gives_infinite_weights(dtype, impl, n, t_cand):
+    """A tile's padding has the bias of its keys: it must not turn inf into NaN,
+    which a trim would drop first instead of keeping."""
+    for table in ("rab_p", "rab_t"):
+        p = problem(n, 128, dtype, t_cand, 560 + n)
+        pos, tim = seen_buckets(p)
+        getattr(p, table)[pos[1] if table == "rab_p" else tim[0]] = np.inf
+        got, w = check_values(p, impl=impl)
+        assert np.isposinf(w).any()
