@@ -177,12 +177,24 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
   return fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u), acc);
 }
 
-// 16 candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum
-// of |P| over the candidates.  With weights (returned in float32) SiLU is
-// x / (1 + 2^y), y = -x log2 e, good to a few 2^-22; else h (1 + tanh h) with
-// h = x / 2, half the special-function work, its error below P's rounding.  A
-// reciprocal for every pair: two pairs that share one are NaN together, and sharing
-// saves no time (8 x 256 candidates 82.1 us shared, 81.3 not).
+__device__ __forceinline__ float silu(float x) {
+  return x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
+}
+// SiLU of four halved logits (out of line: seldom needed).
+__device__ __noinline__ float4 silu_far(float a, float b, float c, float d) {
+  return make_float4(silu(a + a), silu(b + b), silu(c + c), silu(d + d));
+}
+
+// 16 candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum of
+// |P|, ahead of its rounding, over the candidates.
+//   With weights SiLU is x / (1 + 2^y), y = -x log2 e, good to a few 2^-22 of itself.
+//   A reciprocal for every pair: two pairs that share one are NaN together, and sharing
+//   saves no time (8 x 256 candidates 82.1 us shared, 81.3 not).
+//   Without, it is h (1 + tanh h), h = x / 2, half the special-function work (4 x 1,024
+//   candidates 219 us, by the quotient 263).  Its sum cancels for negative x: over all
+//   floats of [-20, 12) the approximate tanh left SiLU at most 1e-5 off, from -7 up at
+//   most 0.035 of P's rounding to bf16, but below -8 up to 2.2 of it and at -16 all of P.
+//   So a thread that meets a logit below -7 takes its 16 by the quotient (the look: 226 us).
 template <int D, int NQ, bool WEIGHTS, int MODE>
 __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8],
                                       const Smem<D, NQ> &sm, int c0, float a, float c,
@@ -191,10 +203,9 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8]
                                       float &wsum) {
   const int sh = 23 - sub_bits;
   const int32_t r0 = fast_r0(sub_bits);
-  constexpr float kL = -1.4426950408889634f;
+  float x[16], pv[16];
 #pragma unroll
   for (int e = 0; e < 16; e += 4) {
-    float x[4], pv[4];
     float4 tq = make_float4(0.f, 0.f, 0.f, 0.f);
     if constexpr (MODE == kTimeTwo || MODE == kTimeFloat)
       tq = *reinterpret_cast<const float4 *>(&sm.tqd[c0 + e]);
@@ -203,30 +214,45 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8]
     for (int u = 0; u < 4; ++u) {
       const float sv = __uint_as_float(s[e + u]);
       if constexpr (MODE == kTimeOne) {
-        x[u] = fmaf(a, sv, c);
+        x[e + u] = fmaf(a, sv, c);
       } else if constexpr (MODE == kTimeTwo) {
-        x[u] = fmaf(a, sv, tqs[u] >= t ? c2 : c);
+        x[e + u] = fmaf(a, sv, tqs[u] >= t ? c2 : c);
       } else if constexpr (MODE == kTimeFloat) {
         const int32_t rr = __float_as_int(t + tqs[u]) >> sh;
-        x[u] = fmaf(a, sv, c) + sm.tbl_t[(rr > r0 ? rr : r0) - r0];
+        x[e + u] = fmaf(a, sv, c) + sm.tbl_t[(rr > r0 ? rr : r0) - r0];
       } else {
-        x[u] = fmaf(a, sv, c) + half * time_bias_int(ts[min(c0 + e + u, nq - 1)] - tk, rt, sub_bits, nb_t);
+        x[e + u] = fmaf(a, sv, c) + half * time_bias_int(ts[min(c0 + e + u, nq - 1)] - tk, rt,
+                                                         sub_bits, nb_t);
       }
     }
-    if constexpr (WEIGHTS) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) pv[u] = x[u] * rcp_approx(1.0f + ex2_approx(kL * x[u]));
-      // padding has the bias of its key: left out, since 0 times it could be NaN
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (c0 + e + u < nq) wsum += fabsf(pv[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) pv[u] = fmaf(x[u], tanh_approx(x[u]), x[u]);   // x halved
-    }
-    pk[e / 2] = pack_bf16x2(pv[0], pv[1]);
-    pk[e / 2 + 1] = pack_bf16x2(pv[2], pv[3]);
   }
+  if constexpr (WEIGHTS) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      pv[e] = silu(x[e]);
+      // padding has the bias of its key: left out, since 0 times it could be NaN
+      if (c0 + e < nq) wsum += fabsf(pv[e]);
+    }
+  } else {   // x halved
+    float lo = x[0];
+#pragma unroll
+    for (int e = 1; e < 15; e += 2) lo = fminf(fminf(lo, x[e]), x[e + 1]);
+    lo = fminf(lo, x[15]);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) pv[e] = fmaf(x[e], tanh_approx(x[e]), x[e]);
+    if (lo < -3.5f) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const float4 y = silu_far(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        pv[e] = y.x;
+        pv[e + 1] = y.y;
+        pv[e + 2] = y.z;
+        pv[e + 3] = y.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) pk[e / 2] = pack_bf16x2(pv[e], pv[e + 1]);
 }
 
 // The decoding warps of K (IS_V false) or V: tiles of codes from the cache into
@@ -621,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int m = 1; m < kRowLanes; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
         const float xs = fmaf(p.alpha, dot, b0);
-        if (u == 0) sm.own[r] = xs * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * xs));
+        if (u == 0) sm.own[r] = silu(xs);
       }
     }
     const float a = half * p.alpha;

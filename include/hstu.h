@@ -342,7 +342,8 @@ hstu_status_t hstu_qcache_read(const hstu_qcache_t *cache, int32_t dtype, int32_
  * order, so equal calls give equal bits.  A table entry of -inf (or below
  * -1e30) hides its bucket.  k_j, v_j are exactly the stored values; the
  * arithmetic is float32, on the tensor cores with P = SiLU(x) rounded to bf16
- * ahead of its product with v, as in hstu_attn_fwd.
+ * ahead of its product with v (without weights P itself is good to a twentieth
+ * of that rounding).
  *  params            as hstu_attn_fwd_candidates (mask is ignored); num_heads,
  *                    d_qk, d_v those of the cache; max_seq_len bounds the
  *                    cached rows plus candidates of a sequence.

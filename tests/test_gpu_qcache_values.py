@@ -153,3 +153,60 @@ def test_an_infinite_table_entry_gives_infinite_weights(dtype, impl, n, t_cand):
         getattr(p, table)[pos[1] if table == "rab_p" else tim[0]] = np.inf
         got, w = check_values(p, impl=impl)
         assert np.isposinf(w).any()
+
+
+# The weight-free form against the bounds of float32 arithmetic with P rounded to
+# bf16 and nothing else: every way a tile finds its time bias, both tile widths.
+FORMS = [dict(), dict(t_cand="apart", nb=(40, 400)), dict(t_cand="before", nb=(40, 400)),
+         dict(t_cand="apart", sub=8, nb=(5000, 3000)), dict(t_cand="before", sub=8, nb=(50, 3000)),
+         dict(t_cand="apart", t_step=10 ** 11, nb=(40, 400)), dict(t_cand="apart", sub=0),
+         dict(per_head=True, t_cand="apart", nb=(1000, 1000), sub=4), dict(pad=5, shift=1),
+         dict(alpha=-3.0)]
+
+
+@pytest.mark.parametrize("decay", [None, 0.75])
+@pytest.mark.parametrize("n", [7, 20, 64, 70, 128])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", FORMS, ids=str)
+def test_float32_arithmetic_with_and_without_weights(decay, n, d, kw):
+    check_values(Problem([260, 33, 0, 129], [n, 9, 2, n], 2, d, d, "bf16", seed=570 + n, **kw),
+                 decay)
+
+
+@pytest.mark.parametrize("decay", [None, 0.75])
+@pytest.mark.parametrize("n", [7, 20, 128])
+@pytest.mark.parametrize("logit", [-3.0, -6.0, -12.0, -30.0, -88.0, -1000.0, 20.0, 200.0])
+def test_logits_far_from_zero(decay, n, logit):
+    """SiLU of a negative logit is small against the logit: a sigmoid with an absolute
+    error would show."""
+    p = Problem([260, 40], [n, 3], 2, 128, 128, "bf16", seed=580 + n, t_cand="apart",
+                nb=(40, 400))
+    p.rab_p += np.float32(logit)
+    check_values(p, decay)
+
+
+@pytest.mark.parametrize("decay", [None, 0.75])
+@pytest.mark.parametrize("dtype,impl,n", KINDS)
+@pytest.mark.parametrize("logit", [-6.5, -7.5, -8.9, -11.3, -14.1, -16.3, -19.7, -40.1, -79.0,
+                                   1.7, 9.3])
+def test_silu_is_good_to_a_part_of_itself(decay, dtype, impl, n, logit):
+    """With alpha = 0 the bias is the logit, exactly, and P may be off by its
+    rounding alone, however small it is: 2^-20 and the rounding of the exponential's
+    argument, |x| (2^-24 + 2^-25), of itself, and for the tensor cores' product a
+    twentieth more than half a step of bf16."""
+    p = Problem([260, 33], [n, 9], 2, 64, 64, dtype, seed=600 + n, alpha=0.0)
+    p.rab_p[:] = logit
+    p.rab_t[:] = 0.0
+    tc = dtype == "bf16" and impl == "auto"
+    u = 2.0 ** -20 + abs(logit) * 2.0 ** -23
+    w0 = p.c.weight.clone()
+    got, w = run(p, decay, w0, impl=impl)
+    got, w, w0 = f64(got), f64(w), f64(w0)
+    u_out = R.BF16_U if dtype == "bf16" else R.F32_U
+    for (_, _, a, (ref, bound, _, _)), (_, sl, _, (_, _, step, wb)) in zip(
+            p.reference((u + (1.05 * R.BF16_U if tc else 0.0), 0.0, 0.0)),
+            p.reference((u, 0.0, 0.0))):
+        agree(got[a], ref, bound + u_out * (np.abs(ref) + bound), "out")
+        if decay is not None:
+            want = decay * w0[sl] + step
+            agree(w[sl], want, wb + 2 * R.F32_U * (np.abs(want) + wb), "weight")
