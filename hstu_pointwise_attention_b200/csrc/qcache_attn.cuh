@@ -2,15 +2,20 @@
 // cache and by their summing pass.
 #pragma once
 
+#include <math.h>
+
 #include "qcache_host.h"
 
 namespace hstu {
 
-// SiLU(x) = x / (1 + e^-x), 0 in the limit x -> -inf: the kernels keep the
-// bias of a logit at or above this, so a table entry of -inf or of the lowest
-// float hides its bucket instead of giving -inf * 0.  NaN stays NaN.
+// A table entry below this hides its bucket: a pair in it adds exactly nothing,
+// whatever its dot product and v are.  The kernels take such an entry as -inf, which a
+// sum of two others never is, and leave out the pairs of a hidden bias.  NaN stays NaN.
 constexpr float kQcBiasFloor = -1e30f;
-__device__ __forceinline__ float qc_bias(float b) { return b < kQcBiasFloor ? kQcBiasFloor : b; }
+constexpr float kQcHidden = -INFINITY;
+__device__ __forceinline__ float qc_bias(float b) { return b < kQcBiasFloor ? kQcHidden : b; }
+// SiLU of a candidate's own pair that is hidden: SiLU itself is never -inf.
+constexpr float kQcNoOwn = -INFINITY;
 
 // Where an item (blockIdx / heads) of the launch belongs.
 struct QcItem {

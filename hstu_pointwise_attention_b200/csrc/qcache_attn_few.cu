@@ -192,10 +192,11 @@ __global__ void __launch_bounds__(kThreads, 4)
         dot = fmaf(__bfloat162float(qr[e + lane]), __bfloat162float(kr[e + lane]), dot);
 #pragma unroll
       for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-      if (lane == 0) sm.own[i] = silu(fmaf(p.alpha, dot, qc_bias(rp[0] + rt[0])));
+      const float b = qc_bias(rp[0]) + qc_bias(rt[0]);
+      if (lane == 0) sm.own[i] = b == kQcHidden ? kQcNoOwn : silu(fmaf(p.alpha, dot, b));
     }
   } else if (tid < kQ) {
-    sm.own[tid] = 0.f;
+    sm.own[tid] = kQcNoOwn;
   }
 
   float o[4 * W][4];
@@ -225,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   for (; jb < j_end; jb += kWarps * kKeys) {
     // the key's bias, with the time's where all candidates share it
     const int64_t tk = kt;
-    float bias = rp[pos_bucket(int64_t(sq.pos) - kp, p.nb_p)];
-    if (one_time) bias = qc_bias(bias + rt[time_bucket_i64(t_first - tk, p.sub_bits, p.nb_t)]);
+    float bias = qc_bias(rp[pos_bucket(int64_t(sq.pos) - kp, p.nb_p)]);
+    if (one_time) bias += qc_bias(rt[time_bucket_i64(t_first - tk, p.sub_bits, p.nb_t)]);
     if (jb + kWarps * kKeys < j_end) load_key(jb + kWarps * kKeys);
     cp_async_wait<kStages - 1>();
     __syncwarp();
@@ -272,17 +273,17 @@ __global__ void __launch_bounds__(kThreads, 4)
       if (!one_time) {
         const int64_t ta = __shfl_sync(0xffffffffu, (long long)tk, ka);
         const int64_t tb = __shfl_sync(0xffffffffu, (long long)tk, kb);
-        b[0] = qc_bias(ca + rt[time_bucket_i64(tq0 - ta, p.sub_bits, p.nb_t)]);
-        b[1] = qc_bias(ca + rt[time_bucket_i64(tq1 - ta, p.sub_bits, p.nb_t)]);
-        b[2] = qc_bias(cb + rt[time_bucket_i64(tq0 - tb, p.sub_bits, p.nb_t)]);
-        b[3] = qc_bias(cb + rt[time_bucket_i64(tq1 - tb, p.sub_bits, p.nb_t)]);
+        b[0] += qc_bias(rt[time_bucket_i64(tq0 - ta, p.sub_bits, p.nb_t)]);
+        b[1] += qc_bias(rt[time_bucket_i64(tq1 - ta, p.sub_bits, p.nb_t)]);
+        b[2] += qc_bias(rt[time_bucket_i64(tq0 - tb, p.sub_bits, p.nb_t)]);
+        b[3] += qc_bias(rt[time_bucket_i64(tq1 - tb, p.sub_bits, p.nb_t)]);
       }
       const bool ok_a = jb + ka < j_end, ok_b = jb + kb < j_end;
       float pv[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float x = silu(fmaf(p.alpha, s[0][e] + s[1][e], b[e]));
-        pv[e] = (e < 2 ? ok_a : ok_b) ? x : 0.f;
+        pv[e] = (e < 2 ? ok_a : ok_b) && b[e] != kQcHidden ? x : 0.f;
       }
       if (wp) {
         float w0 = (live0 ? fabsf(pv[0]) : 0.f) + (live1 ? fabsf(pv[1]) : 0.f);
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += sm.o[w][i][e];
     const int64_t row = q_row + i;
-    if (it.split == 0)
+    if (sm.own[i] != kQcNoOwn)
       sum = fmaf(sm.own[i],
                  __bfloat162float(
                      static_cast<const __nv_bfloat16 *>(p.v)[row * p.v_rs + int64_t(h) * D + e]),

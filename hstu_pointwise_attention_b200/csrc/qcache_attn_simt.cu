@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads)
     decode_rows(sv, dv, c.v_codes, c.v_scales, at0, dv, nk);
     const bool key_ok = kj < nk;
     const int64_t row = sq.row + jb + (key_ok ? kj : 0);
-    const float bp = rp[pos_bucket(int64_t(sq.pos) - c.pos[row], p.nb_p)];
+    const float bp = qc_bias(rp[pos_bucket(int64_t(sq.pos) - c.pos[row], p.nb_p)]);
     const int64_t tk = c.times[row];
     __syncthreads();
     if (kg * kPerThread < nq) {
@@ -128,8 +128,9 @@ __global__ void __launch_bounds__(kThreads)
         const int i = kg * kPerThread + u;
         float pv = 0.f;
         if (key_ok && i < nq) {
-          const float b = qc_bias(bp + rt[time_bucket_i64(s_t[i] - tk, p.sub_bits, p.nb_t)]);
+          const float b = bp + qc_bias(rt[time_bucket_i64(s_t[i] - tk, p.sub_bits, p.nb_t)]);
           pv = silu_exact(fmaf(p.alpha, dot[u], b));
+          pv = b == kQcHidden ? 0.f : pv;
         }
         sp[kj * kPPitch + i] = pv;
       }
@@ -186,7 +187,8 @@ __global__ void __launch_bounds__(kThreads)
       for (int e = lane; e < dq; e += 32) dot = fmaf(sq_q[i * dq + e], qc_float<T>(kr[e]), dot);
 #pragma unroll
       for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-      if (lane == 0) sp[i] = silu_exact(fmaf(p.alpha, dot, qc_bias(rp[0] + rt[0])));
+      const float b = qc_bias(rp[0]) + qc_bias(rt[0]);
+      if (lane == 0) sp[i] = b == kQcHidden ? kQcNoOwn : silu_exact(fmaf(p.alpha, dot, b));
     }
   }
   __syncthreads();
@@ -201,7 +203,8 @@ __global__ void __launch_bounds__(kThreads)
       if (i >= nq) break;
       const int64_t row = sq.q0 + i0 + i;
       float o = acc[a][i];
-      if (it.split == 0) o = fmaf(sp[i], qc_float<T>(v[row * p.v_rs + int64_t(h) * dv + e]), o);
+      if (it.split == 0 && sp[i] != kQcNoOwn)
+        o = fmaf(sp[i], qc_float<T>(v[row * p.v_rs + int64_t(h) * dv + e]), o);
       if (sq.splits > 1)
         p.acc[(sq.acc0 + (int64_t(it.split) * sq.n + i0 + i) * H + h) * dv + e] = o;
       else

@@ -90,7 +90,8 @@ struct Cfg {
 
 // How the time bias of 32 keys of a tile is found.  kTimeOne: the same for all
 // candidates, part of c.  kTimeTwo: each key meets one or two neighbouring
-// buckets, c below and c2 from candidate time t on (relative to the earliest).
+// buckets, both hidden or neither, c below and c2 from candidate time t on
+// (relative to the earliest).
 // kTimeFloat: by the float-exponent table, t = earliest candidate - key.
 // kTimeInt: bucket by bucket in 64 bits.
 enum : int { kTimeOne = 0, kTimeTwo = 1, kTimeFloat = 2, kTimeInt = 3 };
@@ -116,7 +117,7 @@ struct Smem {
   alignas(16) uint8_t v_scales[C::kStages][C::kScaleBytes];
   KeyBias bias[kBias];
   alignas(16) float tqd[NQ];      // candidates' times relative to the earliest of them
-  float own[NQ];                  // SiLU of the candidates' own pairs, 0 outside the first key range
+  float own[NQ];                  // SiLU of the candidates' own pairs (first key range only)
   float tbl_t[kTblT];
   int64_t tq_min, tq_max;
   uint64_t k_full[2], k_empty[2], v_full[C::kV], v_empty[C::kV];
@@ -180,9 +181,14 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
 __device__ __forceinline__ float silu(float x) {
   return x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
 }
-// SiLU of four halved logits (out of line: seldom needed).
-__device__ __noinline__ float4 silu_far(float a, float b, float c, float d) {
-  return make_float4(silu(a + a), silu(b + b), silu(c + c), silu(d + d));
+// SiLU of a halved logit: by tanh, far below zero by the quotient.
+__device__ __forceinline__ float silu_tanh(float h) { return fmaf(h, tanh_approx(h), h); }
+__device__ __forceinline__ float silu_half(float h) {
+  return h < -3.5f ? silu(h + h) : silu_tanh(h);
+}
+// Of four (out of line: seldom needed).
+__device__ __noinline__ float4 silu_half4(float a, float b, float c, float d) {
+  return make_float4(silu_half(a), silu_half(b), silu_half(c), silu_half(d));
 }
 
 // 16 candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum of
@@ -194,7 +200,7 @@ __device__ __noinline__ float4 silu_far(float a, float b, float c, float d) {
 //   candidates 219 us, by the quotient 263).  Its sum cancels for negative x: over all
 //   floats of [-20, 12) the approximate tanh left SiLU at most 1e-5 off, from -7 up at
 //   most 0.035 of P's rounding to bf16, but below -8 up to 2.2 of it and at -16 all of P.
-//   So a thread that meets a logit below -7 takes its 16 by the quotient (the look: 226 us).
+//   So logits below -7 go by the quotient (looking for them costs 7 us).
 template <int D, int NQ, bool WEIGHTS, int MODE>
 __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8],
                                       const Smem<D, NQ> &sm, int c0, float a, float c,
@@ -219,10 +225,12 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8]
         x[e + u] = fmaf(a, sv, tqs[u] >= t ? c2 : c);
       } else if constexpr (MODE == kTimeFloat) {
         const int32_t rr = __float_as_int(t + tqs[u]) >> sh;
-        x[e + u] = fmaf(a, sv, c) + sm.tbl_t[(rr > r0 ? rr : r0) - r0];
+        const float b = c + sm.tbl_t[(rr > r0 ? rr : r0) - r0];
+        x[e + u] = b == kQcHidden ? 0.f : fmaf(a, sv, b);   // SiLU(0) = 0
       } else {
-        x[e + u] = fmaf(a, sv, c) + half * time_bias_int(ts[min(c0 + e + u, nq - 1)] - tk, rt,
-                                                         sub_bits, nb_t);
+        const float b = c + half * time_bias_int(ts[min(c0 + e + u, nq - 1)] - tk, rt, sub_bits,
+                                                 nb_t);
+        x[e + u] = b == kQcHidden ? 0.f : fmaf(a, sv, b);
       }
     }
   }
@@ -239,11 +247,11 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8]
     for (int e = 1; e < 15; e += 2) lo = fminf(fminf(lo, x[e]), x[e + 1]);
     lo = fminf(lo, x[15]);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) pv[e] = fmaf(x[e], tanh_approx(x[e]), x[e]);
+    for (int e = 0; e < 16; ++e) pv[e] = silu_tanh(x[e]);
     if (lo < -3.5f) {
 #pragma unroll
       for (int e = 0; e < 16; e += 4) {
-        const float4 y = silu_far(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        const float4 y = silu_half4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         pv[e] = y.x;
         pv[e + 1] = y.y;
         pv[e + 2] = y.z;
@@ -587,14 +595,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t e_lo = max(__float_as_int(base) >> sh, r0) - r0;
             const int32_t e_hi = max(__float_as_int(float(t_hi - t)) >> sh, r0) - r0;
             kb.t[x * 32 + lane] = base;
-            if (__all_sync(0xffffffffu, e_hi - e_lo <= 1)) {
+            const float c_lo = c + sm.tbl_t[e_lo], c_hi = c + sm.tbl_t[e_hi];
+            if (__all_sync(0xffffffffu, e_hi - e_lo <= 1 &&
+                                            (c_lo == kQcHidden) == (c_hi == kQcHidden))) {
               // The entry is e_lo + 1 exactly from the distance on whose bits are
               // (e_lo + 1 + r0) << sh: an integer below 2^24 where both entries
               // occur, so its difference to base is exact.
               mode = kTimeTwo;
-              kb.c2[x * 32 + lane] = c + sm.tbl_t[e_hi];
+              kb.c2[x * 32 + lane] = c_hi;
               kb.t[x * 32 + lane] = __int_as_float((e_lo + 1 + r0) << sh) - base;
-              c += sm.tbl_t[e_lo];
+              c = c_lo;
             }
           }
           kb.c[x * 32 + lane] = c;
@@ -632,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (it.split == 0) {
       const __nv_bfloat16 *k =
           static_cast<const __nv_bfloat16 *>(p.k) + q_row * p.k_rs + h * D + u * 8;
-      const float b0 = qc_bias(rp[0] + rt[0]);
-#pragma unroll
+      const float b0 = qc_bias(rp[0]) + qc_bias(rt[0]);
+#pragma unroll 1   // (unrolled, its registers spill: 4 x 1,024 candidates 237 us, so 229)
       for (int x = 0; x < 32 / kRows; ++x) {
         const int r = r0 + x * kRows;
         uint4 kw = make_uint4(0, 0, 0, 0);
@@ -647,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int m = 1; m < kRowLanes; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
         const float xs = fmaf(p.alpha, dot, b0);
-        if (u == 0) sm.own[r] = silu(xs);
+        if (u == 0) sm.own[r] = b0 == kQcHidden ? kQcNoOwn : silu(xs);
       }
     }
     const float a = half * p.alpha;
@@ -667,8 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const int mode = kb.mode[quad];
       const float c = kb.c[key];
-      // a key behind the last, or in a hidden bucket, adds exactly nothing
-      const bool valid = j < sq.len && !(mode == kTimeOne && c <= 0.5f * kQcBiasFloor);
+      // a key behind the last adds nothing, nor one whose buckets are hidden for all
+      const bool valid = j < sq.len && c != kQcHidden;
       float c2 = 0.f, t = 0.f, wsum = 0.f;
       int64_t tk = 0;
       if (mode != kTimeOne) {
@@ -747,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float4 oa = *reinterpret_cast<const float4 *>(stage + i * D + u * 8);
         const float4 ob = *reinterpret_cast<const float4 *>(stage + i * D + u * 8 + 4);
         float o[8] = {oa.x, oa.y, oa.z, oa.w, ob.x, ob.y, ob.z, ob.w};
-        if (it.split == 0) {
+        if (it.split == 0 && sm.own[i] != kQcNoOwn) {
           const uint4 vw = load_row8(v + i * p.v_rs, p.vec);
           const uint32_t vs[4] = {vw.x, vw.y, vw.z, vw.w};
           const float own = sm.own[i];

@@ -340,7 +340,9 @@ hstu_status_t hstu_qcache_read(const hstu_qcache_t *cache, int32_t dtype, int32_
  *   weight_j <- weight_decay weight_j + silu_scale sum_{i, heads} |SiLU(x_ij)|
  * (weight_decay 0: the old weight is not read); sums run in float32 in a fixed
  * order, so equal calls give equal bits.  A table entry of -inf (or below
- * -1e30) hides its bucket.  k_j, v_j are exactly the stored values; the
+ * -1e30) hides its bucket: a pair in it adds nothing, whatever the candidate
+ * holds.  Infinities and NaN of a candidate reach its own row of out and the
+ * weights of the rows it sees, nothing else.  k_j, v_j are exactly the stored values; the
  * arithmetic is float32, on the tensor cores with P = SiLU(x) rounded to bf16
  * ahead of its product with v (without weights P itself is good to a twentieth
  * of that rounding).

@@ -210,3 +210,60 @@ def test_silu_is_good_to_a_part_of_itself(decay, dtype, impl, n, logit):
         if decay is not None:
             want = decay * w0[sl] + step
             agree(w[sl], want, wb + 2 * R.F32_U * (np.abs(want) + wb), "weight")
+
+
+HIDING = ["far", "times", "own", "all"]
+
+
+@pytest.mark.parametrize("dtype,impl,n", KINDS)
+@pytest.mark.parametrize("t_cand", [None, "apart", "before"])
+@pytest.mark.parametrize("hide", HIDING)
+def test_a_hidden_bucket_hides_whatever_the_candidate_holds(dtype, impl, n, t_cand, hide):
+    """A pair in a hidden bucket adds nothing: not the infinity or NaN of a query's
+    dot product, nor 0 times the candidate's own infinite v.  Rows that a bad
+    candidate does not see keep the weights, and rows of out the bits, that they
+    have with an ordinary one."""
+    for low in (-np.inf, float(np.finfo(np.float32).min)):
+        p = problem(n, 64, dtype, t_cand, 620 + n)
+        pos, tim = seen_buckets(p)
+        if hide == "far":
+            p.rab_p[39] = low               # (all positions from 39 on)
+        elif hide == "times":
+            p.rab_t[tim[::2]] = low
+            p.rab_t[0] = 0.1
+        elif hide == "own":
+            p.rab_p[0] = low
+        else:
+            p.rab_p[:] = low
+        w0 = p.c.weight.clone()
+        for decay in (0.5, None):
+            clean, w_clean = run(p, decay, w0, impl=impl)
+            assert torch.isfinite(clean.float()).all()
+            for i in sorted({0, 3, n - 1}):
+                for bad in (float("inf"), float("nan")):
+                    kept = p.q[i, 1].clone()
+                    p.q[i, 1, 3] = bad
+                    got, w = run(p, decay, w0, impl=impl)
+                    p.q[i, 1] = kept
+                    sl = slice(int(p.rows[0]), int(p.rows[0] + p.lens[0]))
+                    dp = np.clip(int(p.cand_pos[0]) - p.c.pos[sl].cpu().numpy().astype(np.int64),
+                                 0, 39)
+                    bt = R.time_bucket(p.t[i] - p.c.times[sl].cpu().numpy(), p.sub, 400)
+                    seen = (p.rab_p[dp] > -1e30) & (p.rab_t[bt] > -1e30)
+                    own = p.rab_p[0] > -1e30 and p.rab_t[0] > -1e30
+                    if seen.any() or own:
+                        assert not torch.isfinite(got[i, 1].float()).any()
+                        got[i, 1] = clean[i, 1]
+                    assert torch.equal(bits(got), bits(clean)), (i, bad, decay)
+                    if decay is not None:
+                        hit = torch.from_numpy(seen).cuda()
+                        assert not torch.isfinite(w[sl][hit]).any()
+                        w[sl] = torch.where(hit, w_clean[sl], w[sl])
+                    assert torch.equal(bits(w), bits(w_clean)), (i, bad)
+            if not (p.rab_p[0] > -1e30):
+                for bad in (float("inf"), float("nan")):
+                    kept = p.v[1, 1].clone()
+                    p.v[1, 1, 3] = bad
+                    got, _ = run(p, decay, w0, impl=impl)
+                    p.v[1, 1] = kept
+                    assert torch.equal(bits(got), bits(clean)), bad
