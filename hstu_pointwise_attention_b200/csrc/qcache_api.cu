@@ -168,6 +168,7 @@ hstu_status_t check_attn(const AttnArgs &a, bool have_cache) {
   for (int32_t b = 0; b < p.batch; ++b) {
     const int64_t n = a.coff[b + 1] - a.coff[b], L = a.lens[b];
     if (L < 0 || n > p.max_seq_len || L > p.max_seq_len - n) return HSTU_ERR_INVALID_ARG;
+    if (L > kQcMaxLen || n > kQcMaxLen) return HSTU_ERR_UNSUPPORTED;
     if (have_cache && !in_rows(a.rows[b], L, a.cache->rows)) return HSTU_ERR_INVALID_ARG;
     all += L;
   }
@@ -494,7 +495,7 @@ static hstu_status_t evict_sizes(int32_t batch, const int64_t *lens, const int64
   *kept = 0;
   for (int32_t b = 0; b < batch; ++b) {
     if (lens[b] < 0 || budgets[b] < 0) return HSTU_ERR_INVALID_ARG;
-    if (lens[b] >= (int64_t(1) << 31)) return HSTU_ERR_UNSUPPORTED;
+    if (lens[b] > kQcMaxLen) return HSTU_ERR_UNSUPPORTED;
     *kept += std::min(lens[b], budgets[b]);
   }
   return *kept < (int64_t(1) << 36) ? HSTU_OK : HSTU_ERR_UNSUPPORTED;

@@ -8,6 +8,10 @@
 
 namespace hstu {
 
+// Rows (or candidates) of one sequence: the kernels' loops step int32 indices by up
+// to 1,024 and round lengths up to tiles.
+constexpr int64_t kQcMaxLen = (int64_t(1) << 31) - 1024;
+
 // --- append / read ---
 // From this many tokens on 32 threads share a token, which spares instructions
 // (8 heads of 128, 8 x 4096 tokens stored and read: 85 us, 64 threads 99, 128

@@ -287,7 +287,8 @@ hstu_status_t hstu_layer_fwd_candidates(
  * sequence by host arrays: sequence b owns rows [rows_host[b], + its length);
  * their order within the region carries no meaning.  Alignment: codes and
  * scales 16 bytes, the others their element.  weight may be NULL where no call updates
- * or reads it. */
+ * or reads it.  A sequence of more than 2^31 - 1024 rows is HSTU_ERR_UNSUPPORTED in
+ * the attention and the trimming. */
 typedef struct {
   int64_t rows;                  /* capacity, 0..2^40 */
   int32_t num_heads;             /* H, 1..4096 */

@@ -1,0 +1,48 @@
+"""The 4-bit history cache on the CPU: calls at the edge of what its kernels index,
+and calls that would race or read out of place, are refused before any launch (in a
+process that sees no device, where an accepted call ends with the CUDA error)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from hstu_pointwise_attention_b200 import ops
+
+from test_qcache_host import (CUDA, INVALID, OK, UNSUPPORTED, _attn, _attn_params, _cache, _evict,
+                              _hidden, _i64, _other, hidden)  # noqa: F401
+
+LONGEST = 2 ** 31 - 1024     # rows of a sequence: loops step int32 indices by up to 1,024
+
+
+def wrong(cases):
+    return [c for c in cases if c[0] != c[1]]
+
+
+def _lengths():
+    assert _hidden()
+    out = []
+    big = _cache(rows=2 ** 33, H=1, dk=32, dv=32)
+    far = _cache(rows=2 ** 33, H=1, dk=32, dv=32)
+    for i, (f, _) in enumerate(ops._QCacheStruct._fields_[5:]):
+        setattr(far, f, (i + 2) << 44)
+    for n in (LONGEST, LONGEST + 1, 2 ** 31 - 1):
+        want = CUDA if n <= LONGEST else UNSUPPORTED
+        kw = dict(src=big, rows=(0, 2 ** 32), to=(0, 2 ** 32), nbytes=1 << 40)
+        out += [(want, _evict(lens=(n, 30), budgets=(1000, 10), **kw), f"in place {n}"),
+                (want, _evict(lens=(30, n), budgets=(7, 1), dst=far, **kw), f"copied {n}")]
+        size = ctypes.c_size_t(0)
+        lens, budgets = _i64(n), _i64(5)
+        out.append((OK if n <= LONGEST else UNSUPPORTED,
+                    ops.LIB.hstu_qcache_evict_workspace_size(
+                        1, lens.ctypes.data, budgets.ctypes.data, ctypes.byref(size)), f"size {n}"))
+        for dtype in (0, 1):
+            p = _attn_params(H=1, dk=32, dv=32, msl=2 ** 31 - 1, dtype=dtype)
+            for upd in (0, 1):
+                out.append((want, _attn(p=p, cache=big, rows=(0, 2 ** 32),
+                                        lens=(n, 5), coff=(0, 0, 2), upd=upd, nbytes=1 << 50),
+                            f"attention {n} {dtype} {upd}"))
+    return out
+
+
+def test_longest_sequences(hidden):  # noqa: F811
+    assert not wrong(hidden.apply(_lengths))
