@@ -174,7 +174,8 @@ hstu_status_t check_attn(const AttnArgs &a, bool have_cache) {
   }
   // item and row counters of a launch are 32-bit
   const int64_t T = p.batch > 0 ? a.coff[p.batch] : 0;
-  if (T * p.num_heads >= (int64_t(1) << 31) || all >= (int64_t(1) << 40))
+  const int64_t most = int64_t(1) << 31;
+  if (T >= most || T * p.num_heads >= most || all >= (int64_t(1) << 40))
     return HSTU_ERR_UNSUPPORTED;
   if (have_cache && a.weight &&
       !disjoint(a.rows, [&](int32_t b) { return a.lens[b]; }, p.batch))

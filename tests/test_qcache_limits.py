@@ -46,3 +46,21 @@ def _lengths():
 
 def test_longest_sequences(hidden):  # noqa: F811
     assert not wrong(hidden.apply(_lengths))
+
+
+def _candidate_totals():
+    """Candidates times heads, which a launch counts in 32 bits, at sizes where the
+    product leaves 64."""
+    assert _hidden()
+    B = 1 << 21
+    n = 2 ** 31 - 1024
+    p = _attn_params(B=B, H=4096, dk=32, dv=32, msl=2 ** 31 - 1)
+    lens = np.zeros(B, np.int64)
+    coff = np.arange(B + 1, dtype=np.int64) * n
+    size = ctypes.c_size_t(0)
+    return [(UNSUPPORTED, ops.LIB.hstu_attn_candidates_qcache_workspace_size(
+        ctypes.byref(p), lens.ctypes.data, coff.ctypes.data, 0, ctypes.byref(size)), "total")]
+
+
+def test_candidate_totals(hidden):  # noqa: F811
+    assert not wrong(hidden.apply(_candidate_totals))
