@@ -88,6 +88,30 @@ bool disjoint(const int64_t *start, Len len, int32_t B) {
   }
 }
 
+// No buffer of one cache shares a byte with any buffer of the other.
+bool apart(const hstu_qcache_t *x, const hstu_qcache_t *y) {
+  struct Buf {
+    uintptr_t at, end;
+  };
+  auto bufs = [](const hstu_qcache_t *c, Buf (&b)[7]) {
+    const int64_t R = c->rows, k = R * c->num_heads * c->d_qk, v = R * c->num_heads * c->d_v;
+    const void *const p[7] = {c->k_codes, c->v_codes, c->k_scales, c->v_scales,
+                              c->times,   c->pos,     c->weight};
+    const int64_t n[7] = {k / 2, v / 2, k / 16, v / 16, R * 8, R * 4, R * 4};
+    for (int i = 0; i < 7; ++i) {
+      b[i].at = reinterpret_cast<uintptr_t>(p[i]);
+      b[i].end = b[i].at + uintptr_t(n[i]);
+    }
+  };
+  Buf a[7], b[7];
+  bufs(x, a);
+  bufs(y, b);
+  for (const Buf &i : a)
+    for (const Buf &j : b)
+      if (i.at < j.end && j.at < i.end) return false;
+  return true;
+}
+
 bool offsets_ok(const int64_t *off, int32_t B) {
   if (B > 0 && (!off || off[0] != 0)) return false;
   for (int32_t b = 0; b < B; ++b)
@@ -543,20 +567,7 @@ hstu_status_t hstu_qcache_evict(const hstu_qcache_t *src, const hstu_qcache_t *d
       return HSTU_ERR_INVALID_ARG;
   } else {
     if (!disjoint(dst_rows_host, keep, batch)) return HSTU_ERR_INVALID_ARG;
-    // two caches share no memory
-    auto apart = [](const void *a, int64_t an, const void *b, int64_t bn) {
-      const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-      return an == 0 || bn == 0 || x + uintptr_t(an) <= y || y + uintptr_t(bn) <= x;
-    };
-    const int64_t H = src->num_heads, a = src->rows, b = dst->rows, hk = H * src->d_qk,
-                  hv = H * src->d_v;
-    if (!apart(src->k_codes, a * hk / 2, dst->k_codes, b * hk / 2) ||
-        !apart(src->v_codes, a * hv / 2, dst->v_codes, b * hv / 2) ||
-        !apart(src->k_scales, a * hk / 16, dst->k_scales, b * hk / 16) ||
-        !apart(src->v_scales, a * hv / 16, dst->v_scales, b * hv / 16) ||
-        !apart(src->times, a * 8, dst->times, b * 8) || !apart(src->pos, a * 4, dst->pos, b * 4) ||
-        !apart(src->weight, a * 4, dst->weight, b * 4))
-      return HSTU_ERR_INVALID_ARG;
+    if (!apart(src, dst)) return HSTU_ERR_INVALID_ARG;
   }
   if (kept == 0) return HSTU_OK;
   const size_t half = align256(size_t(kept) * sizeof(int32_t));

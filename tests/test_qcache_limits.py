@@ -64,3 +64,39 @@ def _candidate_totals():
 
 def test_candidate_totals(hidden):  # noqa: F811
     assert not wrong(hidden.apply(_candidate_totals))
+
+
+FIELDS = ("k_codes", "k_scales", "v_codes", "v_scales", "times", "pos", "weight")
+
+
+def _apart(rows=64, H=2, d=64):
+    """Two caches whose buffers lie apart, and every buffer's bytes."""
+    size = dict(zip(FIELDS, (rows * H * d // 2, rows * H * d // 16) * 2 +
+                    (rows * 8, rows * 4, rows * 4)))
+    src, dst = _cache(rows=rows), _cache(rows=rows)
+    for i, f in enumerate(FIELDS):
+        setattr(src, f, (1 << 24) + (i << 20))
+        setattr(dst, f, (2 << 24) + (i << 20))
+    return src, dst, size
+
+
+def _shared_memory():
+    """A destination buffer that lies in any buffer of the source, at its first and
+    its last bytes, is refused; right behind or ahead of it is fine."""
+    out = []
+    src, dst, size = _apart()
+    out.append((CUDA, _evict(src=src, dst=dst), "apart"))
+    for a in FIELDS:
+        for b in FIELDS:
+            base = getattr(src, a)
+            for at, want in ((base, INVALID), (base + size[a] - 16, INVALID),
+                             (base - size[b] + 16, INVALID), (base + size[a], CUDA),
+                             (base - size[b], CUDA)):
+                src, dst, _ = _apart()
+                setattr(dst, b, at)
+                out.append((want, _evict(src=src, dst=dst), (a, b, at - base)))
+    return out
+
+
+def test_evict_refuses_any_shared_memory(hidden):  # noqa: F811
+    assert not wrong(hidden.apply(_shared_memory))
