@@ -108,7 +108,7 @@ bool apart(const hstu_qcache_t *x, const hstu_qcache_t *y) {
   bufs(y, b);
   for (const Buf &i : a)
     for (const Buf &j : b)
-      if (i.at < j.end && j.at < i.end) return false;
+      if (std::max(i.at, j.at) < std::min(i.end, j.end)) return false;
   return true;
 }
 

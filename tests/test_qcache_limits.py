@@ -95,6 +95,10 @@ def _shared_memory():
                 src, dst, _ = _apart()
                 setattr(dst, b, at)
                 out.append((want, _evict(src=src, dst=dst), (a, b, at - base)))
+    src, dst, _ = _apart()
+    dst.rows = 0                       # an empty cache shares nothing
+    dst.k_codes = src.k_codes + 32
+    out.append((OK, _evict(src=src, dst=dst, budgets=(0, 0), to=(0, 0)), "empty"))
     return out
 
 
