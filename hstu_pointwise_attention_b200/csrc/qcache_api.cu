@@ -678,6 +678,10 @@ hstu_status_t hstu_layer_fwd_candidates_qcache(
   if (T > 0 && (!cand_timestamps_dev || !x_cand || !w1 || !b1 || !ln_gamma || !ln_beta || !w2 ||
                 !b2 || !rab_pos || !rab_time || !y_cand || x_cand == y_cand))
     return HSTU_ERR_INVALID_ARG;
+  if (!aligned(cand_timestamps_dev, 8) || !aligned(x_cand, 2) || !aligned(w1, 2) ||
+      !aligned(w2, 2) || !aligned(y_cand, 2) || !aligned(b1, 4) || !aligned(ln_gamma, 4) ||
+      !aligned(ln_beta, 4) || !aligned(b2, 4) || !aligned(rab_pos, 4) || !aligned(rab_time, 4))
+    return HSTU_ERR_INVALID_ARG;
   if (proj_out && !aligned(proj_out, 16)) return HSTU_ERR_INVALID_ARG;
   const LayerQcWs lw = layer_layout(a);
   if (!workspace_ok(workspace, workspace_bytes, lw.total)) return HSTU_ERR_WORKSPACE;

@@ -104,3 +104,36 @@ def _shared_memory():
 
 def test_evict_refuses_any_shared_memory(hidden):  # noqa: F811
     assert not wrong(hidden.apply(_shared_memory))
+
+
+LAYER_ARGS = ("ts", "x", "w1", "b1", "gamma", "beta", "w2", "b2", "rab_p", "rab_t")
+
+
+def _layer_call(**kw):
+    """A layer call on 5 candidates of d_model 64; every buffer can be placed."""
+    assert _hidden()
+    at = {n: (i + 1) << 24 for i, n in enumerate(LAYER_ARGS + ("y", "ws"))}
+    at["proj"] = None
+    at.update(kw)
+    lp = ops.LayerParams()
+    lp.attn = _attn_params()
+    lp.d_model, lp.residual, lp.ln_eps = 64, 1, 1e-5
+    rows, lens, coff, pos = _i64(0, 32), _i64(20, 30), _i64(0, 3, 5), np.array([20, 30], np.int32)
+    return ops.LIB.hstu_layer_fwd_candidates_qcache(
+        ctypes.byref(lp), ctypes.byref(_cache()), rows.ctypes.data, lens.ctypes.data,
+        coff.ctypes.data, pos.ctypes.data, *(at[n] for n in LAYER_ARGS), 1, 0.5, at["y"],
+        at["proj"], at["ws"], 1 << 24, None)
+
+
+def _layer_alignment():
+    out = [(CUDA, _layer_call(), "aligned")]
+    for n in LAYER_ARGS + ("y",):
+        size = 8 if n == "ts" else 2 if n in ("x", "w1", "w2", "y") else 4
+        base = (20 << 24)
+        out += [(INVALID, _layer_call(**{n: base + size // 2}), n),
+                (CUDA, _layer_call(**{n: base + size}), n)]
+    return out
+
+
+def test_layer_refuses_buffers_off_their_elements(hidden):  # noqa: F811
+    assert not wrong(hidden.apply(_layer_alignment))
