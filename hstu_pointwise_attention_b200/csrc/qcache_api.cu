@@ -88,27 +88,30 @@ bool disjoint(const int64_t *start, Len len, int32_t B) {
   }
 }
 
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return std::max(x, y) < std::min(x + uintptr_t(a_bytes), y + uintptr_t(b_bytes));
+}
+
 // No buffer of one cache shares a byte with any buffer of the other.
 bool apart(const hstu_qcache_t *x, const hstu_qcache_t *y) {
   struct Buf {
-    uintptr_t at, end;
+    const void *at;
+    int64_t bytes;
   };
   auto bufs = [](const hstu_qcache_t *c, Buf (&b)[7]) {
     const int64_t R = c->rows, k = R * c->num_heads * c->d_qk, v = R * c->num_heads * c->d_v;
-    const void *const p[7] = {c->k_codes, c->v_codes, c->k_scales, c->v_scales,
-                              c->times,   c->pos,     c->weight};
-    const int64_t n[7] = {k / 2, v / 2, k / 16, v / 16, R * 8, R * 4, R * 4};
-    for (int i = 0; i < 7; ++i) {
-      b[i].at = reinterpret_cast<uintptr_t>(p[i]);
-      b[i].end = b[i].at + uintptr_t(n[i]);
-    }
+    const Buf all[7] = {{c->k_codes, k / 2},   {c->v_codes, v / 2}, {c->k_scales, k / 16},
+                        {c->v_scales, v / 16}, {c->times, R * 8},   {c->pos, R * 4},
+                        {c->weight, R * 4}};
+    std::copy(all, all + 7, b);
   };
   Buf a[7], b[7];
   bufs(x, a);
   bufs(y, b);
   for (const Buf &i : a)
     for (const Buf &j : b)
-      if (std::max(i.at, j.at) < std::min(i.end, j.end)) return false;
+      if (overlap(i.at, i.bytes, j.at, j.bytes)) return false;
   return true;
 }
 
@@ -676,13 +679,20 @@ hstu_status_t hstu_layer_fwd_candidates_qcache(
   if (a.weight && !std::isfinite(weight_decay)) return HSTU_ERR_INVALID_ARG;
   const int64_t T = ap.batch > 0 ? cand_offsets_host[ap.batch] : 0;
   if (T > 0 && (!cand_timestamps_dev || !x_cand || !w1 || !b1 || !ln_gamma || !ln_beta || !w2 ||
-                !b2 || !rab_pos || !rab_time || !y_cand || x_cand == y_cand))
+                !b2 || !rab_pos || !rab_time || !y_cand))
     return HSTU_ERR_INVALID_ARG;
   if (!aligned(cand_timestamps_dev, 8) || !aligned(x_cand, 2) || !aligned(w1, 2) ||
       !aligned(w2, 2) || !aligned(y_cand, 2) || !aligned(b1, 4) || !aligned(ln_gamma, 4) ||
       !aligned(ln_beta, 4) || !aligned(b2, 4) || !aligned(rab_pos, 4) || !aligned(rab_time, 4))
     return HSTU_ERR_INVALID_ARG;
   if (proj_out && !aligned(proj_out, 16)) return HSTU_ERR_INVALID_ARG;
+  // x is read again behind the first rows of y, and the projection behind both
+  const int64_t x_bytes = T * params->d_model * 2,
+                p_bytes = T * 4 * ap.num_heads * (ap.d_v + ap.d_qk);
+  if (overlap(x_cand, x_bytes, y_cand, x_bytes) ||
+      (proj_out && (overlap(proj_out, p_bytes, x_cand, x_bytes) ||
+                    overlap(proj_out, p_bytes, y_cand, x_bytes))))
+    return HSTU_ERR_INVALID_ARG;
   const LayerQcWs lw = layer_layout(a);
   if (!workspace_ok(workspace, workspace_bytes, lw.total)) return HSTU_ERR_WORKSPACE;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);

@@ -402,6 +402,7 @@ hstu_status_t hstu_qcache_evict(const hstu_qcache_t *src, const hstu_qcache_t *d
  *  proj_out  may be NULL; else [Tc][N1] bf16, 16-byte aligned, receives the
  *            projection, whose K and V columns hstu_qcache_append stores once
  *            a candidate has become an event.
+ *  x_cand, y_cand and proj_out share no memory with one another.
  *  Other arguments as hstu_layer_fwd_candidates and
  *  hstu_attn_fwd_candidates_qcache; d_qk, d_v multiples of 32. */
 hstu_status_t hstu_layer_candidates_qcache_workspace_size(const hstu_layer_params_t *params,

@@ -137,3 +137,21 @@ def _layer_alignment():
 
 def test_layer_refuses_buffers_off_their_elements(hidden):  # noqa: F811
     assert not wrong(hidden.apply(_layer_alignment))
+
+
+def _layer_overlap():
+    x, out = 20 << 24, []
+    rows, proj = 5 * 64 * 2, 5 * 4 * 128 * 2            # bytes of x (or y) and of proj_out
+    for at, want in ((x, INVALID), (x + rows - 16, INVALID), (x - rows + 16, INVALID),
+                     (x + rows, CUDA), (x - rows, CUDA)):
+        out.append((want, _layer_call(x=x, y=at), ("y on x", at - x)))
+    for n in ("x", "y"):
+        for at, want in ((x, INVALID), (x + rows - 16, INVALID), (x - proj + 16, INVALID),
+                         (x + rows, CUDA), (x - proj, CUDA)):
+            out.append((want, _layer_call(**{n: x, "proj": at}), ("proj on " + n, at - x)))
+    return out
+
+
+def test_layer_refuses_outputs_that_share_memory(hidden):  # noqa: F811
+    """The residual reads x behind the first rows of y, and the gate the projection."""
+    assert not wrong(hidden.apply(_layer_overlap))
