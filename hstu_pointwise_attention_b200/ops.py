@@ -452,7 +452,8 @@ class QuantCache:
     hstu_qcache_t): k_codes, v_codes uint8 [H, rows, d / 2]; k_scales, v_scales
     int16 [H, rows, d / 32]; times int64, pos int32, weight float32 [rows]
     (weight may be None where no call updates or reads it).  Contiguous, on one
-    CUDA device.  ``QuantCache.empty`` allocates them."""
+    CUDA device, and the same for the object's life (their contents may change).
+    ``QuantCache.empty`` allocates them."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, times, pos, weight=None):
         H, rows, half_k = k_codes.shape
@@ -481,6 +482,11 @@ class QuantCache:
         self._c = _QCacheStruct(rows, H, self.d_qk, self.d_v, 0, _ptr(k_codes), _ptr(k_scales),
                                 _ptr(v_codes), _ptr(v_scales), _ptr(times), _ptr(pos),
                                 _ptr(weight))
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:      # the library's copy would keep the old address
+            raise AttributeError(f"QuantCache.{name} is fixed; make a new QuantCache")
+        super().__setattr__(name, value)
 
     @classmethod
     def empty(cls, rows, num_heads, d_qk, d_v, device="cuda"):

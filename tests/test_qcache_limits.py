@@ -155,3 +155,19 @@ def _layer_overlap():
 def test_layer_refuses_outputs_that_share_memory(hidden):  # noqa: F811
     """The residual reads x behind the first rows of y, and the gate the projection."""
     assert not wrong(hidden.apply(_layer_overlap))
+
+
+def test_a_caches_buffers_are_fixed():
+    """The library is given the buffers' addresses once: a buffer put in another's
+    place would not be the one that calls use."""
+    import torch
+    c = ops.QuantCache.empty(8, 2, 64, 32, device="cpu")
+    for f in FIELDS:
+        kept = getattr(c, f)
+        assert getattr(c._c, f) == kept.data_ptr()
+        with pytest.raises(AttributeError, match="QuantCache"):
+            setattr(c, f, torch.zeros_like(kept))
+        assert getattr(c, f) is kept
+    with pytest.raises(AttributeError):
+        c.rows = 4
+    c.weight.copy_(torch.ones(8))      # their contents are the caller's
