@@ -521,6 +521,9 @@ class _Launch:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream),
                                                    device=torch.device("cuda", index))
+            elif stream.device_index != index:
+                raise ValueError(f"the stream belongs to {stream.device}, the tensors to "
+                                 f"cuda:{index}")
             self._ctx = torch.cuda.stream(stream)
         else:
             self._ctx = None if index == torch.cuda.current_device() else \

@@ -171,3 +171,12 @@ def test_a_caches_buffers_are_fixed():
     with pytest.raises(AttributeError):
         c.rows = 4
     c.weight.copy_(torch.ones(8))      # their contents are the caller's
+
+
+def test_a_stream_of_another_device_is_refused():
+    import torch
+
+    class OnDevice1:
+        cuda_stream, device, device_index = 1234, torch.device("cuda", 1), 1
+    with pytest.raises(ValueError, match="stream"):
+        ops._Launch(0, OnDevice1())
