@@ -543,7 +543,11 @@ class _Launch:
 
 def _host_vec(a, n, dtype, name):
     if not (type(a) is np.ndarray and a.dtype == dtype and a.flags.c_contiguous):
-        a = _host_i64(a) if dtype is np.int64 else _host_i32(a)
+        raw = a.detach().cpu().numpy() if isinstance(a, torch.Tensor) else np.asarray(a)
+        with np.errstate(invalid="ignore"):
+            a = np.ascontiguousarray(raw.astype(dtype))
+        if not np.array_equal(a, raw):
+            raise ValueError(f"{name}: expected whole numbers that fit {np.dtype(dtype)}")
     if a.shape != (n,):
         raise ValueError(f"{name}: expected {n} entries, got shape {a.shape}")
     return a
@@ -625,7 +629,7 @@ def qcache_evict(cache, rows, lens, budgets, keep_pos, *, dst=None, dst_rows=Non
                  workspace=None, stream=None):
     """hstu_qcache_evict: keep each sequence's budgets[b] most used rows, in
     place or (dst, dst_rows) in another cache.  Returns the new lengths."""
-    lens = _host_i64(lens)
+    lens = _host_vec(lens, len(lens), np.int64, "lens")
     B = len(lens)
     rows = _host_vec(rows, B, np.int64, "rows")
     budgets = _host_vec(budgets, B, np.int64, "budgets")

@@ -180,3 +180,20 @@ def test_a_stream_of_another_device_is_refused():
         cuda_stream, device, device_index = 1234, torch.device("cuda", 1), 1
     with pytest.raises(ValueError, match="stream"):
         ops._Launch(0, OnDevice1())
+
+
+def test_host_numbers_that_do_not_fit_are_refused():
+    """A keep_pos of 2^31 as int64 is not -2^31 (which would keep every row)."""
+    import torch
+    c = ops.QuantCache.empty(8, 2, 32, 32, device="cpu")
+    for keep in (np.array([2 ** 31]), torch.tensor([2 ** 31]), [2 ** 31], [1.5], [float("nan")],
+                 np.array([-2 ** 31 - 1])):
+        with pytest.raises(ValueError, match="keep_pos"):
+            ops.qcache_evict(c, [0], [4], [2], keep)
+    for bad in ([0.5], np.array([2.0 ** 64])):
+        with pytest.raises(ValueError, match="lens"):
+            ops.qcache_evict(c, [0], bad, [2], [0])
+    for good in ([3], np.array([3.0]), torch.tensor([3], dtype=torch.int32), np.array([3], ">i8")):
+        got = ops._host_vec(good, 1, np.int32, "x")
+        assert got.tolist() == [3] and got.dtype == np.int32 and got.flags.c_contiguous
+    assert ops._host_vec([], 0, np.int64, "x").dtype == np.int64
