@@ -19,12 +19,6 @@ namespace qc {
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // rne(x / s) of the exact quotient, given inv ~ 1 / s (to 2^-22): the product
 // rounds to within one of it, and the remainder x - y s (exact in one fma)
 // settles it.

@@ -38,6 +38,12 @@ struct QCacheView {
   float *weight;                   // [rows], may be null
 };
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Sequences per launch: their table travels in the kernel's parameters, so a
 // call needs no upload and records whole under stream capture.
 constexpr int kQcMaxSeqs = 64;

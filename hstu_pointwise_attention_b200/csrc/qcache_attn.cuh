@@ -86,11 +86,9 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// SiLU(x) = x / (1 + 2^y), y = -x log2 e, to a few 2^-22 of itself.
+__device__ __forceinline__ float qc_silu(float x) {
+  return x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
 }
-
 
 }  // namespace hstu

@@ -87,9 +87,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ float silu(float x) {
-  return x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4)
@@ -193,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
       for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
       const float b = qc_bias(rp[0]) + qc_bias(rt[0]);
-      if (lane == 0) sm.own[i] = b == kQcHidden ? kQcNoOwn : silu(fmaf(p.alpha, dot, b));
+      if (lane == 0) sm.own[i] = b == kQcHidden ? kQcNoOwn : qc_silu(fmaf(p.alpha, dot, b));
     }
   } else if (tid < kQ) {
     sm.own[tid] = kQcNoOwn;
@@ -282,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       float pv[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = silu(fmaf(p.alpha, s[0][e] + s[1][e], b[e]));
+        const float x = qc_silu(fmaf(p.alpha, s[0][e] + s[1][e], b[e]));
         pv[e] = (e < 2 ? ok_a : ok_b) && b[e] != kQcHidden ? x : 0.f;
       }
       if (wp) {

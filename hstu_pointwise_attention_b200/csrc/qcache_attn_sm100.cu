@@ -178,13 +178,10 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
   return fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u), acc);
 }
 
-__device__ __forceinline__ float silu(float x) {
-  return x * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
-}
 // SiLU of a halved logit: by tanh, far below zero by the quotient.
 __device__ __forceinline__ float silu_tanh(float h) { return fmaf(h, tanh_approx(h), h); }
 __device__ __forceinline__ float silu_half(float h) {
-  return h < -3.5f ? silu(h + h) : silu_tanh(h);
+  return h < -3.5f ? qc_silu(h + h) : silu_tanh(h);
 }
 // Of four (out of line: seldom needed).
 __device__ __noinline__ float4 silu_half4(float a, float b, float c, float d) {
@@ -193,14 +190,14 @@ __device__ __noinline__ float4 silu_half4(float a, float b, float c, float d) {
 
 // 16 candidates of one key: P = SiLU(x) as bf16 pairs and, with weights, the sum of
 // |P|, ahead of its rounding, over the candidates.
-//   With weights SiLU is x / (1 + 2^y), y = -x log2 e, good to a few 2^-22 of itself.
-//   A reciprocal for every pair: two pairs that share one are NaN together, and sharing
-//   saves no time (8 x 256 candidates 82.1 us shared, 81.3 not).
+//   With weights SiLU is its quotient (qc_silu).  A reciprocal for every pair: two pairs
+//   that share one are NaN together, and sharing saves no time (8 x 256 candidates 82.1 us
+//   shared, 81.3 not).
 //   Without, it is h (1 + tanh h), h = x / 2, half the special-function work (4 x 1,024
-//   candidates 219 us, by the quotient 263).  Its sum cancels for negative x: over all
-//   floats of [-20, 12) the approximate tanh left SiLU at most 1e-5 off, from -7 up at
-//   most 0.035 of P's rounding to bf16, but below -8 up to 2.2 of it and at -16 all of P.
-//   So logits below -7 go by the quotient (looking for them costs 7 us).
+//   candidates 219 us, by the quotient 263).  Its sum cancels for negative x: at 2^20
+//   points of every unit of [-20, 12) the approximate tanh left SiLU at most 1e-5 off,
+//   from -7 up at most 0.035 of P's rounding to bf16, but below -8 up to 2.2 of it and at
+//   -16 all of P.  So logits below -7 go by the quotient (looking for them costs 7 us).
 template <int D, int NQ, bool WEIGHTS, int MODE>
 __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8],
                                       const Smem<D, NQ> &sm, int c0, float a, float c,
@@ -237,7 +234,7 @@ __device__ __forceinline__ void chunk(const uint32_t (&s)[16], uint32_t (&pk)[8]
   if constexpr (WEIGHTS) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      pv[e] = silu(x[e]);
+      pv[e] = qc_silu(x[e]);
       // padding has the bias of its key: left out, since 0 times it could be NaN
       if (c0 + e < nq) wsum += fabsf(pv[e]);
     }
@@ -657,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int m = 1; m < kRowLanes; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
         const float xs = fmaf(p.alpha, dot, b0);
-        if (u == 0) sm.own[r] = b0 == kQcHidden ? kQcNoOwn : silu(xs);
+        if (u == 0) sm.own[r] = b0 == kQcHidden ? kQcNoOwn : qc_silu(xs);
       }
     }
     const float a = half * p.alpha;

@@ -1,6 +1,6 @@
 // qcache_host.h -- launch parameters of the 4-bit cache kernels, filled by
 // qcache_api.cu.  Each holds the table of up to kQcMaxSeqs sequences by value
-// (kernel parameters, at most 4 KB), so no call uploads anything.
+// (kernel parameters, at most 8 KB), so no call uploads anything.
 #pragma once
 
 #include "internal.h"
