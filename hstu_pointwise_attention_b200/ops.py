@@ -177,11 +177,13 @@ def _host_i32(a) -> Optional[np.ndarray]:
 
 
 def _row_stride(t: torch.Tensor, H: int, d: int, name: str) -> int:
-    """t is [T, H, d] (or a [T, H*d] view) with contiguous heads."""
-    if t.shape[1:] == (H, d) and t.is_contiguous():
+    """t is [T, H, d] (or a [T, H*d] view) with contiguous heads.  Strides that carry no
+    meaning are not looked at: an empty tensor's, and in a contiguous one those of
+    dimensions of size 1."""
+    if t.dim() == 3 and t.shape[1:] == (H, d) and t.is_contiguous():
         return H * d
-    if t.shape[0] == 0 and tuple(t.shape[1:]) in ((H, d), (H * d,)):
-        return H * d        # no rows: strides carry no meaning
+    if t.dim() in (2, 3) and t.shape[0] == 0 and tuple(t.shape[1:]) in ((H, d), (H * d,)):
+        return H * d
     if t.dim() == 3:
         if t.shape[1:] != (H, d) or t.stride()[1:] != (d, 1):
             raise ValueError(f"{name}: expected [T, {H}, {d}] with contiguous heads")
