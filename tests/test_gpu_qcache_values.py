@@ -5,8 +5,10 @@ import numpy as np
 import pytest
 import torch
 
+from hstu_pointwise_attention_b200 import ops
+
 import qcache_ref as R
-from test_gpu_qcache import Problem, f64
+from test_gpu_qcache import Problem, f64, layer_params
 
 pytestmark = pytest.mark.gpu
 
@@ -267,3 +269,92 @@ def test_a_hidden_bucket_hides_whatever_the_candidate_holds(dtype, impl, n, t_ca
                     got, _ = run(p, decay, w0, impl=impl)
                     p.v[1, 1] = kept
                     assert torch.equal(bits(got), bits(clean)), bad
+
+
+@pytest.mark.parametrize("n", [5, 20, 100])
+@pytest.mark.parametrize("decay", [0.5, None])
+def test_own_values_with_the_keys_split_over_ctas(n, decay):
+    """Only the first key range adds the own pairs: the summing pass must see them once."""
+    p = Problem([6000, 2500], [n, 3], 1, 128, 128, "bf16", seed=640 + n)
+    check_values(p, decay)
+    w0 = p.c.weight.clone()
+    clean, w_clean = run(p, decay, w0)
+    p.v[n // 2, 0, 9] = float("inf")
+    got, w = run(p, decay, w0)
+    assert not torch.isfinite(got[n // 2, 0, 9])
+    got[n // 2, 0, 9] = clean[n // 2, 0, 9]
+    assert torch.equal(bits(got), bits(clean)) and torch.equal(bits(w), bits(w_clean))
+
+
+@pytest.mark.parametrize("n", [8, 40, 130])
+def test_a_nan_row_through_the_layer(n):
+    """One candidate's NaN input reaches its own row of the projection and of y."""
+    H, d, D = 2, 128, 64
+    rng = np.random.default_rng(650 + n)
+    p = Problem([260, 0], [n, 4], H, d, d, "bf16", seed=651)
+    P = layer_params(rng, H, d, D)
+    x = torch.from_numpy(rng.standard_normal((n + 4, D)).astype(np.float32)).cuda().bfloat16()
+
+    def layer():
+        proj = torch.empty((n + 4, 4 * H * d), dtype=torch.bfloat16, device="cuda")
+        y = ops.layer_fwd_candidates_qcache(
+            x, *P, p.c, p.rows, p.lens, p.off, p.cand_pos, p.ts, num_heads=H, d_qk=d, d_v=d,
+            max_seq_len=p.msl, time_bucket_sub_bits=2, silu_scale=p.scale, proj_out=proj)
+        return y, proj
+    y0, proj0 = layer()
+    for i in (0, n - 1, n + 1):
+        kept = x[i].clone()
+        x[i] = float("nan")
+        y, proj = layer()
+        x[i] = kept
+        assert torch.isnan(y[i]).all() and torch.isnan(proj[i]).all()
+        y[i], proj[i] = y0[i], proj0[i]
+        assert torch.equal(bits(y), bits(y0)) and torch.equal(bits(proj), bits(proj0))
+
+
+def test_a_captured_step_appends_scores_and_trims():
+    """Events stored, candidates scored with weights and the histories trimmed in one
+    graph: each replay does what the calls one behind the other do."""
+    H, d, D = 2, 64, 64
+    rng = np.random.default_rng(660)
+    p = Problem([300, 90], [33, 2], H, d, d, "bf16", seed=661)
+    P = layer_params(rng, H, d, D)
+    x = torch.from_numpy(rng.standard_normal((35, D)).astype(np.float32)).cuda().bfloat16()
+    FIELDS = ("k_codes", "k_scales", "v_codes", "v_scales", "times", "pos", "weight")
+    start = {f: getattr(p.c, f).clone() for f in FIELDS}
+    y = torch.empty((35, D), dtype=torch.bfloat16, device="cuda")
+    proj = torch.empty((35, 4 * H * d), dtype=torch.bfloat16, device="cuda")
+    F = H * d
+    pick = torch.tensor([0, 33], device="cuda")
+
+    def step():
+        ops.layer_fwd_candidates_qcache(
+            x, *P, p.c, p.rows, p.lens, p.off, p.cand_pos, p.ts, num_heads=H, d_qk=d, d_v=d,
+            max_seq_len=p.msl + 2, time_bucket_sub_bits=2, silu_scale=p.scale, weight_decay=0.5,
+            proj_out=proj, out=y)
+        ev = proj[pick]
+        ops.qcache_append(p.c, ev[:, 3 * F:], ev[:, F:2 * F], p.ts[pick], [0, 1, 2],
+                          p.rows + p.lens, p.cand_pos)
+        ops.qcache_evict(p.c, p.rows, p.lens + 1, [200, 50], p.cand_pos - 4)
+
+    def reset():
+        for f in FIELDS:
+            getattr(p.c, f).copy_(start[f])
+    step()
+    want = [y.clone(), proj.clone()] + [getattr(p.c, f).clone() for f in FIELDS]
+    reset()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g):
+            step()
+    for _ in range(2):
+        torch.cuda.synchronize()
+        reset()
+        y.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        got = [y, proj] + [getattr(p.c, f) for f in FIELDS]
+        for a, b in zip(got, want):
+            same = a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)
+            assert torch.equal(*same)
