@@ -215,6 +215,10 @@ cudaError_t launch_gemm_tc(const void *a, int64_t lda, const void *b, int64_t ld
 cudaError_t launch_ln_gate(const void *a, int64_t lda, const void *u, int64_t ldu,
                            const float *gamma, const float *beta, float eps, void *g,
                            int64_t ldg, int64_t T, int32_t F, cudaStream_t st);
+// The same of a float32 A (16-byte aligned, lda a multiple of 4).
+cudaError_t launch_ln_gate_f32(const float *a, int64_t lda, const void *u, int64_t ldu,
+                               const float *gamma, const float *beta, float eps, void *g,
+                               int64_t ldg, int64_t T, int32_t F, cudaStream_t st);
 
 // Backward of the LayerNorm gating (layer.cu): bf16 activations, float32
 // gamma / beta and their gradients (accumulated).

@@ -88,11 +88,12 @@ cudaError_t launch_gemm_simt(const void *a, int64_t lda, const void *b, int64_t 
 
 // ---------------------------------------------------------------------------
 // G = LayerNorm(A) * gamma + beta, then (.) U.  One warp per token, F <= 1024
-// features; float32 statistics (mean, biased variance), 16-byte loads.
+// features; float32 statistics (mean, biased variance), 16-byte loads.  A is bf16, or
+// float32 where its rounding would be magnified by 1 / (its deviation).
 // ---------------------------------------------------------------------------
-template <int F, bool VEC_P>
+template <typename TA, int F, bool VEC_P>
 __global__ void __launch_bounds__(256) ln_gate_kernel(
-    const __nv_bfloat16 *__restrict__ A, int64_t lda, const __nv_bfloat16 *__restrict__ U,
+    const TA *__restrict__ A, int64_t lda, const __nv_bfloat16 *__restrict__ U,
     int64_t ldu, const float *__restrict__ gamma, const float *__restrict__ beta, float eps,
     __nv_bfloat16 *__restrict__ G, int64_t ldg, int64_t T) {
   constexpr int kPer = F / 32;          // features per lane
@@ -101,26 +102,34 @@ __global__ void __launch_bounds__(256) ln_gate_kernel(
   const int lane = threadIdx.x % 32;
   if (t >= T) return;
   float a[kPer], u[kPer];
-  const __nv_bfloat16 *ar = A + t * lda;
+  const TA *ar = A + t * lda;
   const __nv_bfloat16 *ur = U + t * ldu;
   // lane owns features [v*32*kVec + lane*kVec, +kVec) for v = 0 .. kPer/kVec-1
 #pragma unroll
   for (int v = 0; v < kPer / kVec; ++v) {
     const int f0 = v * 32 * kVec + lane * kVec;
     if constexpr (kVec == 8) {
-      const uint4 ra = *reinterpret_cast<const uint4 *>(ar + f0);
       const uint4 ru = *reinterpret_cast<const uint4 *>(ur + f0);
-      const __nv_bfloat16 *pa = reinterpret_cast<const __nv_bfloat16 *>(&ra);
       const __nv_bfloat16 *pu = reinterpret_cast<const __nv_bfloat16 *>(&ru);
+      if constexpr (sizeof(TA) == 2) {
+        const uint4 ra = *reinterpret_cast<const uint4 *>(ar + f0);
+        const __nv_bfloat16 *pa = reinterpret_cast<const __nv_bfloat16 *>(&ra);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[v * kVec + e] = __bfloat162float(pa[e]);
-        u[v * kVec + e] = __bfloat162float(pu[e]);
+        for (int e = 0; e < 8; ++e) a[v * kVec + e] = __bfloat162float(pa[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 ra = *reinterpret_cast<const float4 *>(ar + f0 + e);
+          a[v * kVec + e] = ra.x, a[v * kVec + e + 1] = ra.y;
+          a[v * kVec + e + 2] = ra.z, a[v * kVec + e + 3] = ra.w;
+        }
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[v * kVec + e] = __bfloat162float(pu[e]);
     } else {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        a[v * kVec + e] = __bfloat162float(ar[f0 + e]);
+        a[v * kVec + e] = float(ar[f0 + e]);
         u[v * kVec + e] = __bfloat162float(ur[f0 + e]);
       }
     }
@@ -177,56 +186,48 @@ __global__ void __launch_bounds__(256) ln_gate_kernel(
   }
 }
 
-cudaError_t launch_ln_gate(const void *a, int64_t lda, const void *u, int64_t ldu,
-                           const float *gamma, const float *beta, float eps, void *g,
-                           int64_t ldg, int64_t T, int32_t F, cudaStream_t st) {
+template <typename TA, int F>
+static void launch_ln_gate_f(const TA *A, int64_t lda, const __nv_bfloat16 *U, int64_t ldu,
+                      const float *gamma, const float *beta, float eps, __nv_bfloat16 *G,
+                      int64_t ldg, int64_t T, cudaStream_t st) {
+  const unsigned grid = unsigned((T + 7) / 8);
+  const bool vec = ((reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(beta)) & 15) == 0;
+  if (vec)
+    ln_gate_kernel<TA, F, true><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
+  else
+    ln_gate_kernel<TA, F, false><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
+}
+
+template <typename TA>
+static cudaError_t launch_ln_gate_t(const void *a, int64_t lda, const void *u, int64_t ldu,
+                                    const float *gamma, const float *beta, float eps, void *g,
+                                    int64_t ldg, int64_t T, int32_t F, cudaStream_t st) {
   if (T == 0) return cudaSuccess;
-  const dim3 grid(unsigned((T + 7) / 8));
-  const auto *A = static_cast<const __nv_bfloat16 *>(a);
+  const auto *A = static_cast<const TA *>(a);
   const auto *U = static_cast<const __nv_bfloat16 *>(u);
   auto *G = static_cast<__nv_bfloat16 *>(g);
-  const bool vec = ((reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(beta)) & 15) == 0;
   switch (F) {
-    case 32:
-      if (vec)
-        ln_gate_kernel<32, true><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      else
-        ln_gate_kernel<32, false><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      break;
-    case 64:
-      if (vec)
-        ln_gate_kernel<64, true><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      else
-        ln_gate_kernel<64, false><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      break;
-    case 128:
-      if (vec)
-        ln_gate_kernel<128, true><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      else
-        ln_gate_kernel<128, false><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      break;
-    case 256:
-      if (vec)
-        ln_gate_kernel<256, true><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      else
-        ln_gate_kernel<256, false><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      break;
-    case 512:
-      if (vec)
-        ln_gate_kernel<512, true><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      else
-        ln_gate_kernel<512, false><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      break;
-    case 1024:
-      if (vec)
-        ln_gate_kernel<1024, true><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      else
-        ln_gate_kernel<1024, false><<<grid, 256, 0, st>>>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T);
-      break;
+    case 32: launch_ln_gate_f<TA, 32>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T, st); break;
+    case 64: launch_ln_gate_f<TA, 64>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T, st); break;
+    case 128: launch_ln_gate_f<TA, 128>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T, st); break;
+    case 256: launch_ln_gate_f<TA, 256>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T, st); break;
+    case 512: launch_ln_gate_f<TA, 512>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T, st); break;
+    case 1024: launch_ln_gate_f<TA, 1024>(A, lda, U, ldu, gamma, beta, eps, G, ldg, T, st); break;
     default: return cudaErrorInvalidValue;
   }
   count_launch();
   return cudaGetLastError();
+}
+
+cudaError_t launch_ln_gate(const void *a, int64_t lda, const void *u, int64_t ldu,
+                           const float *gamma, const float *beta, float eps, void *g,
+                           int64_t ldg, int64_t T, int32_t F, cudaStream_t st) {
+  return launch_ln_gate_t<__nv_bfloat16>(a, lda, u, ldu, gamma, beta, eps, g, ldg, T, F, st);
+}
+cudaError_t launch_ln_gate_f32(const float *a, int64_t lda, const void *u, int64_t ldu,
+                               const float *gamma, const float *beta, float eps, void *g,
+                               int64_t ldg, int64_t T, int32_t F, cudaStream_t st) {
+  return launch_ln_gate_t<float>(a, lda, u, ldu, gamma, beta, eps, g, ldg, T, F, st);
 }
 
 // ---------------------------------------------------------------------------

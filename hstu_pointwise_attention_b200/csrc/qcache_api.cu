@@ -360,7 +360,7 @@ AttnWs attn_layout(const AttnArgs &a) {
 
 hstu_status_t run_attn(const AttnArgs &a, const int64_t *cand_ts, const void *q, const void *k,
                        const void *v, const float *rab_pos, const float *rab_time, float decay,
-                       void *out, const AttnWs &w, uint8_t *ws, bool clear_err,
+                       void *out, bool out_f32, const AttnWs &w, uint8_t *ws, bool clear_err,
                        cudaStream_t st) {
   const hstu_attn_params_t &ap = *a.p;
   const bool bf16 = ap.dtype == HSTU_BF16;
@@ -392,6 +392,7 @@ hstu_status_t run_attn(const AttnArgs &a, const int64_t *cand_ts, const void *q,
           p.q_rs % per16 == 0 && p.k_rs % per16 == 0 && p.v_rs % per16 == 0 &&
           p.o_rs % per16 == 0;
   p.clear_err = clear_err;
+  p.out_f32 = out_f32;
   int64_t rows = 0, wp = 0;
   Share s{};
   for (int32_t b0 = 0; b0 < ap.batch; b0 += kQcMaxSeqs) {
@@ -418,6 +419,10 @@ bool workspace_ok(const void *ws, size_t bytes, size_t need) {
 // ---------------------------------------------------------------------------
 // Layer
 // ---------------------------------------------------------------------------
+// The attention's output A stays float32 up to the LayerNorm, which divides it by its
+// deviation over the features: long histories average v, so A differs little between
+// features (mean / deviation of 3 and more), and A in bf16 was most of y's error (of
+// 2.8e-3 relative to 64 bits, with 2.0e-3 left; 8 x 256 candidates 96.4 us, so 98.2).
 struct LayerQcWs {
   AttnWs attn;
   size_t proj, a, g, total;
@@ -449,7 +454,7 @@ LayerQcWs layer_layout(const AttnArgs &a) {
   w.attn = attn_layout(a);   // its error word (offset 0) serves the whole layer
   w.proj = align256(w.attn.total);
   w.a = align256(w.proj + size_t(T) * 2 * (F + H * ap.d_qk) * 2);
-  w.g = align256(w.a + size_t(T) * F * 2);
+  w.g = align256(w.a + size_t(T) * F * 4);
   w.total = align256(w.g + size_t(T) * F * 2);
   return w;
 }
@@ -645,8 +650,9 @@ hstu_status_t hstu_attn_fwd_candidates_qcache(
     return HSTU_ERR_INVALID_ARG;
   const AttnWs w = attn_layout(a);
   if (!workspace_ok(workspace, workspace_bytes, w.total)) return HSTU_ERR_WORKSPACE;
-  return run_attn(a, cand_timestamps_dev, q, k, v, rab_pos, rab_time, weight_decay, out, w,
-                  static_cast<uint8_t *>(workspace), true, static_cast<cudaStream_t>(stream));
+  return run_attn(a, cand_timestamps_dev, q, k, v, rab_pos, rab_time, weight_decay, out,
+                  false, w, static_cast<uint8_t *>(workspace), true,
+                  static_cast<cudaStream_t>(stream));
 }
 
 hstu_status_t hstu_layer_candidates_qcache_workspace_size(const hstu_layer_params_t *params,
@@ -701,7 +707,7 @@ hstu_status_t hstu_layer_fwd_candidates_qcache(
   if (cudaMemsetAsync(err, 0, 16, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   if (T == 0)   // no candidate rows; the weights still decay
     return run_attn(a, nullptr, nullptr, nullptr, nullptr, rab_pos, rab_time, weight_decay,
-                    nullptr, lw.attn, ws, false, cs);
+                    nullptr, true, lw.attn, ws, false, cs);
   const int64_t H = ap.num_heads, dqk = ap.d_qk, D = params->d_model, F = H * ap.d_v,
                 n1 = 2 * (F + H * dqk);
   uint8_t *proj = proj_out ? static_cast<uint8_t *>(proj_out) : ws + lw.proj;
@@ -711,9 +717,10 @@ hstu_status_t hstu_layer_fwd_candidates_qcache(
                               wc, cs);
   if (e != cudaSuccess) return HSTU_ERR_CUDA;
   st = run_attn(a, cand_timestamps_dev, proj + 2 * (2 * F), proj + 2 * (2 * F + H * dqk),
-                proj + 2 * F, rab_pos, rab_time, weight_decay, att, lw.attn, ws, false, cs);
+                proj + 2 * F, rab_pos, rab_time, weight_decay, att, true, lw.attn, ws, false, cs);
   if (st != HSTU_OK) return st;
-  e = launch_ln_gate(att, F, proj, n1, ln_gamma, ln_beta, params->ln_eps, g, F, T, int32_t(F), cs);
+  e = launch_ln_gate_f32(reinterpret_cast<const float *>(att), F, proj, n1, ln_gamma, ln_beta,
+                         params->ln_eps, g, F, T, int32_t(F), cs);
   if (e != cudaSuccess) return HSTU_ERR_CUDA;
   e = launch_gemm(g, F, w2, F, b2, params->residual ? x_cand : nullptr, D, y_cand, D, T, D, F,
                   params->residual ? kEpiBiasResidual : kEpiBias, wc, cs);

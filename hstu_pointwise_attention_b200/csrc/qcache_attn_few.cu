@@ -355,6 +355,8 @@ __global__ void __launch_bounds__(kThreads, 4)
                  sum);
     if (sq.splits > 1)
       p.acc[(sq.acc0 + (int64_t(it.split) * sq.n + it.qtile * kQ + i) * H + h) * D + e] = sum;
+    else if (p.out_f32)
+      static_cast<float *>(p.out)[row * p.o_rs + int64_t(h) * D + e] = sum * p.scale;
     else
       static_cast<__nv_bfloat16 *>(p.out)[row * p.o_rs + int64_t(h) * D + e] =
           __float2bfloat16_rn(sum * p.scale);

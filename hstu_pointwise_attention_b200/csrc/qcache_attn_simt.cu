@@ -207,6 +207,8 @@ __global__ void __launch_bounds__(kThreads)
         o = fmaf(sp[i], qc_float<T>(v[row * p.v_rs + int64_t(h) * dv + e]), o);
       if (sq.splits > 1)
         p.acc[(sq.acc0 + (int64_t(it.split) * sq.n + i0 + i) * H + h) * dv + e] = o;
+      else if (p.out_f32)
+        static_cast<float *>(p.out)[row * p.o_rs + int64_t(h) * dv + e] = o * p.scale;
       else
         out[row * p.o_rs + int64_t(h) * dv + e] = qc_round<T>(o * p.scale);
     }
@@ -307,7 +309,7 @@ cudaError_t launch_qcache_finish(const QcAttnParams &p, bool bf16, int plane, cu
   const int64_t ob = (p.fin_rows + kFinThreads / 32 - 1) / (kFinThreads / 32);
   const int64_t wb = (p.weight_rows + kFinThreads - 1) / kFinThreads;
   if (ob + wb == 0) return cudaSuccess;
-  if (bf16)
+  if (bf16 && !p.out_f32)
     finish_kernel<__nv_bfloat16><<<unsigned(ob + wb), kFinThreads, 0, st>>>(p, int(ob), plane);
   else
     finish_kernel<float><<<unsigned(ob + wb), kFinThreads, 0, st>>>(p, int(ob), plane);

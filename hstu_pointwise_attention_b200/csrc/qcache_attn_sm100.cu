@@ -763,11 +763,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[e] = fmaf(own, __uint_as_float(e & 1 ? vs[e / 2] & 0xFFFF0000u : vs[e / 2] << 16),
                         o[e]);
         }
-        if (sq.splits > 1) {
+        if (sq.splits > 1 || p.out_f32) {
+          const float f = sq.splits > 1 ? 1.0f : p.scale;
           float *dst =
-              p.acc + ((sq.acc0 + (int64_t(it.split) * sq.n + i0 + i) * H + h) * D + u * 8);
-          reinterpret_cast<float4 *>(dst)[0] = make_float4(o[0], o[1], o[2], o[3]);
-          reinterpret_cast<float4 *>(dst)[1] = make_float4(o[4], o[5], o[6], o[7]);
+              sq.splits > 1
+                  ? p.acc + ((sq.acc0 + (int64_t(it.split) * sq.n + i0 + i) * H + h) * D + u * 8)
+                  : static_cast<float *>(p.out) + (q_row + i) * p.o_rs + h * D + u * 8;
+          reinterpret_cast<float4 *>(dst)[0] =
+              make_float4(o[0] * f, o[1] * f, o[2] * f, o[3] * f);
+          reinterpret_cast<float4 *>(dst)[1] =
+              make_float4(o[4] * f, o[5] * f, o[6] * f, o[7] * f);
         } else {
           __nv_bfloat16 *dst =
               static_cast<__nv_bfloat16 *>(p.out) + (q_row + i) * p.o_rs + h * D + u * 8;

@@ -79,6 +79,7 @@ struct QcAttnParams {
   int32_t fin_rows;               // (candidate, head) rows of split sequences
   int64_t weight_rows;            // cached rows whose weight is updated (0: none)
   bool rab_per_head, vec, clear_err;
+  bool out_f32;                   // out is float32 though q, k, v are bf16
   QcAttnSeq seqs[kQcMaxSeqs];
 };
 static_assert(sizeof(QcRowsParams) <= 4096 && sizeof(QcEvictParams) <= 4096 + 512 &&

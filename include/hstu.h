@@ -397,7 +397,7 @@ hstu_status_t hstu_qcache_evict(const hstu_qcache_t *src, const hstu_qcache_t *d
 
 /* hstu_layer_fwd_candidates over the 4-bit cache of that layer's history:
  *   [U|V|Q|K]_c = SiLU(x_cand W1^T + b1)
- *   A_c = hstu_attn_fwd_candidates_qcache(Q_c, K_c, V_c)
+ *   A_c = hstu_attn_fwd_candidates_qcache(Q_c, K_c, V_c), in float32
  *   y_cand = x_cand + (LayerNorm(A_c) (.) U_c) W2^T + b2   (residual as flagged)
  *  proj_out  may be NULL; else [Tc][N1] bf16, 16-byte aligned, receives the
  *            projection, whose K and V columns hstu_qcache_append stores once

@@ -8,7 +8,7 @@ import torch
 from hstu_pointwise_attention_b200 import ops
 
 import qcache_ref as R
-from test_gpu_qcache import Problem, f64, layer_params
+from test_gpu_qcache import Problem, f64, layer_params, stored
 
 pytestmark = pytest.mark.gpu
 
@@ -358,3 +358,63 @@ def test_a_captured_step_appends_scores_and_trims():
         for a, b in zip(got, want):
             same = a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)
             assert torch.equal(*same)
+
+
+@pytest.mark.parametrize("decay", [None, 0.5])
+@pytest.mark.parametrize("H,d,L,n", [(2, 64, 20, 5), (2, 64, 20, 20), (2, 64, 20, 100),
+                                     (1, 128, 20, 40), (4, 32, 20, 20), (2, 64, 600, 5),
+                                     (2, 64, 900, 70)])
+def test_layer_norm_sees_the_attention_in_float32(decay, H, d, L, n):
+    """Attention outputs whose features differ by little against their size: the
+    LayerNorm takes the size away and leaves a rounding of it magnified.
+
+    All keys share one v row of 12..15 eighths, alpha is 0 and the own pair hidden, so
+    the attention is a multiple of that row (whatever P's rounding) and the LayerNorm
+    is known.  W2 is the identity: y is g, rounded once.  The bound: that rounding, and
+    float32 sums over keys (2 u a term) and features (u a term) against the deviation."""
+    F = H * d
+    rng = np.random.default_rng(670 + n)
+    p = Problem([L, 7], [n, 3], H, d, d, "bf16", seed=671)
+    P = list(layer_params(rng, H, d, F))
+    P[4] = torch.eye(F, dtype=torch.bfloat16, device="cuda")
+    P[5] = torch.zeros(F, device="cuda")
+    P[6] = P[6] + 1.0
+    P[6][0] = float("-inf")
+    v_row = (12 + rng.integers(0, 4, (1, H, d))) / 8.0
+    for b in range(2):
+        m = int(p.lens[b])
+        vt = torch.from_numpy(np.repeat(v_row, m, 0).astype(np.float32)).cuda().bfloat16()
+        t, pos = p.c.times.clone(), p.c.pos.clone()
+        kt, _ = ops.qcache_read(p.c, [p.rows[b]], [m])
+        ops.qcache_append(p.c, kt, vt, torch.zeros(m, dtype=torch.int64, device="cuda"), [0, m],
+                          [p.rows[b]], [0])
+        p.c.times.copy_(t)
+        p.c.pos.copy_(pos)
+    x = torch.from_numpy(rng.standard_normal((n + 3, F)).astype(np.float32)).cuda().bfloat16()
+    proj = torch.empty((n + 3, 4 * F), dtype=torch.bfloat16, device="cuda")
+    y = f64(ops.layer_fwd_candidates_qcache(
+        x, *P, p.c, p.rows, p.lens, p.off, p.cand_pos, p.ts, num_heads=H, d_qk=d, d_v=d,
+        max_seq_len=p.msl, time_bucket_sub_bits=2, alpha=0.0, silu_scale=1.0, residual=False,
+        proj_out=proj, weight_decay=decay))
+    u, _, q, k = (f64(proj)[:, i * F:(i + 1) * F].reshape(-1, H, d) for i in range(4))
+    rp, rt = f64(P[6]), f64(P[7])
+    ga, be = f64(P[2]), f64(P[3])
+    for b in range(2):
+        sl, a = slice(int(p.rows[b]), int(p.rows[b] + p.lens[b])), \
+            slice(int(p.off[b]), int(p.off[b + 1]))
+        kh, vh = stored(p.c, p.rows[b], p.lens[b])
+        np.testing.assert_array_equal(vh, np.repeat(v_row, int(p.lens[b]), 0))
+        with np.errstate(invalid="ignore"):      # (the bound of the hidden own pair)
+            out, _, _, _ = R.attend(q[a], k[a], np.zeros_like(q[a]), kh, vh,
+                                    p.c.pos[sl].cpu().numpy(), p.c.times[sl].cpu().numpy(),
+                                    int(p.cand_pos[b]), p.t[a], rp, rt, 2, 0.0, 1.0, 0.0)
+        A = out.reshape(-1, F)
+        mu, sd = A.mean(1, keepdims=True), np.sqrt(A.var(1, keepdims=True) + 1e-5)
+        ln = (A - mu) / sd
+        assert np.all(np.abs(mu) > 3 * sd)
+        err = 2 ** -23 * (int(p.lens[b]) + 8 + F) * np.abs(A).max(1, keepdims=True)
+        dln = 2 * err / sd * (1 + np.abs(ln)) + 2.0 ** -20 * (1 + np.abs(ln))
+        g = (ln * ga + be) * u[a].reshape(-1, F)
+        tol = np.abs(u[a].reshape(-1, F)) * np.abs(ga) * dln
+        assert np.all(np.abs(y[a] - g) <= tol + R.BF16_U * (np.abs(g) + tol)), \
+            float((np.abs(y[a] - g) / (np.abs(g) + 1e-3)).max())
