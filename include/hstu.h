@@ -358,7 +358,9 @@ hstu_status_t hstu_qcache_read(const hstu_qcache_t *cache, int32_t dtype, int32_
  *  workspace         >= hstu_attn_candidates_qcache_workspace_size bytes,
  *                    256-byte aligned, one per stream.
  * bf16 with d_qk = d_v in {64, 128} runs on the tensor cores (unless params
- * ask for HSTU_IMPL_SIMT), everything else on the CUDA cores. */
+ * ask for HSTU_IMPL_SIMT), everything else on the CUDA cores.  Kernel and key
+ * ranges follow from the counts of up to 64 sequences at a time, so a sequence
+ * may be rounded otherwise in another batch. */
 hstu_status_t hstu_attn_candidates_qcache_workspace_size(const hstu_attn_params_t *params,
                                                          const int64_t *cache_lens_host,
                                                          const int64_t *cand_offsets_host,

@@ -418,3 +418,17 @@ def test_layer_norm_sees_the_attention_in_float32(decay, H, d, L, n):
         tol = np.abs(u[a].reshape(-1, F)) * np.abs(ga) * dln
         assert np.all(np.abs(y[a] - g) <= tol + R.BF16_U * (np.abs(g) + tol)), \
             float((np.abs(y[a] - g) / (np.abs(g) + 1e-3)).max())
+
+
+@pytest.mark.parametrize("decay", [None, 0.0])
+@pytest.mark.parametrize("dtype,impl,n", KINDS)
+@pytest.mark.parametrize("t_cand", [None, "apart"])
+def test_rows_of_which_nothing_is_left_are_zero(decay, dtype, impl, n, t_cand):
+    for table in ("rab_p", "rab_t"):
+        p = problem(n, 128, dtype, t_cand, 690 + n)
+        getattr(p, table)[:] = -np.inf
+        got, w = run(p, decay, p.c.weight.clone(), impl=impl)
+        assert torch.all(got == 0)
+        if decay is not None:
+            for b in range(3):
+                assert torch.all(w[p.rows[b]:p.rows[b] + p.lens[b]] == 0)
