@@ -220,7 +220,9 @@ struct Share {
 
 // How the keys are split.  A CTA holds `nq` candidates of one (sequence, head)
 // and walks `chunk` 128-key tiles.  `slots` CTAs run at once.  A CTA's fixed
-// cost (tables, queries, the output) is worth `fixed` tiles, and a split adds
+// cost (tables, queries, the output) is worth `fixed` tiles (the tcgen05 kernel's 9: of
+// eleven shapes one depends on it, 4 x 1,024 on 8,192 with weights, 316 us up to 7
+// tiles and 289 from 9 to 16), and a split adds
 // the summing pass; the estimate below is the time in tiles: one chunk when all
 // CTAs run at once, else the shared work plus half a CTA for the uneven end.
 int32_t pick_chunk(const AttnArgs &a, int32_t b0, int32_t n_seqs, int nq, int64_t slots,
@@ -289,8 +291,8 @@ void make_share(const AttnArgs &a, int32_t b0, int64_t acc_row, int64_t wp, QcAt
     // Warp-level products while no sequence has more than 8 candidates, else tcgen05
     // tiles of 64, or of 128 where some sequence has more.  Measured at 8 / 64
     // histories of 4,096 events (8 heads of 128), warp-level against 64-wide tiles: 8
-    // candidates 20 / 100 us against 26 / 154, 9 (two of its tiles) 31 / 163
-    // against 26 / 154.
+    // candidates 21 / 104 us against 26 / 162, 9 (two of its tiles) 33 / 174
+    // against 26 / 163.
     int64_t most = 0;
     for (int32_t b = b0; b < b0 + p.n_seqs; ++b) most = std::max(most, a.coff[b + 1] - a.coff[b]);
     s.few = most <= kQcFewQueries;

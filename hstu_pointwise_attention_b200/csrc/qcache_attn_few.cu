@@ -28,10 +28,10 @@
 // The row permutation key_of (2 t + e -> t + 4 e) and the chunk swizzles below make
 // both reads of a stage free of bank conflicts.
 //
-// Bound by instructions: about 1,030 per 32 keys of 128, half of them decoding.  Measured
+// Bound by instructions: about 1,040 per 32 keys of 128, half of them decoding.  Measured
 // (64 histories of 1,024 to 8,192 events, one candidate each, 8 heads of 128, weights
-// updated): 80 us and 7 more to sum, 237 MB, 2.8 TB/s; issue slots 67 % busy, integer
-// unit 59 %.  The 64-wide tcgen05 tiles take 152 us there.  Two or eight warps per CTA
+// updated): 81 us and 7 more to sum, 237 MB, 2.8 TB/s; issue slots 67 % busy, integer
+// unit 60 %.  The 64-wide tcgen05 tiles take 155 us there.  Two or eight warps per CTA
 // take 5 to 10 us longer, a third stage or four chains of products change nothing.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

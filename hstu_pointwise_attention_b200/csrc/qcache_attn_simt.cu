@@ -12,8 +12,8 @@
 // columns over the 64 keys (with at most 64 columns, over every other key).  Bound
 // by shared-memory reads: 9 16-byte reads per 32 multiply-adds in the first step,
 // 5 per 16 in the second.  32 histories of 64 to 1,024 events, 1 to 24 candidates
-// each, 4 heads of 64, float32: 24 us and 5 more to sum, most of it the latency of
-// a CTA's few steps (issue slots 26 % busy).
+// each, 4 heads of 64, float32: 25 us and 5 more to sum, most of it the latency of
+// a CTA's few steps (issue slots 25 % busy).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

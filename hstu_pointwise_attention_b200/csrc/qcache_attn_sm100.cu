@@ -36,14 +36,14 @@
 // NQ = 128.
 // Tensor memory: S^T slots, then O^T, then two K tiles (Cfg).
 //
-// Bound by the elementwise warps and their hand-overs: at 128 candidates one of the
-// two groups takes 3,600 cycles for its tile of 128 x 128 pairs and then waits for
-// the next S^T (tensor memory has room for two, so one is made while the other is
-// read; a slot is free once its last columns are in registers: with the wait for P
-// in its place 8 x 256 took 85.5 us and 4 x 1,024 233).  Measured (8 heads of 128): 8
-// histories of 4,096 with 256 candidates and weights 75 us and 7 more to sum (455
-// TFLOP/s; issue slots 74 %, special functions 42 %, tensor cores 24 % busy); 4 of
-// 8,192 with 1,024 candidates 227 us (605 TFLOP/s; 78 %, 33 %, 33 %).
+// Bound by the elementwise warps and their hand-overs: at 128 candidates each of the
+// two groups works on its tile of 128 x 128 pairs and then waits for the next S^T
+// (tensor memory has room for two, so one is made while the other is read; a slot is
+// free once its last columns are in registers: with the wait for P in its place 8 x 256
+// took 3 us longer and 4 x 1,024 6).  Measured (8 heads of 128): 8 histories of 4,096
+// with 256 candidates and weights 72 us and 7 more to sum (477 TFLOP/s; issue slots
+// 77 %, special functions 50 %, tensor cores 25 % busy); 4 of 8,192 with 1,024 candidates
+// 234 us (588 TFLOP/s; 74 %, 33 %, 32 %).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
