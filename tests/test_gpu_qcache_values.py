@@ -8,6 +8,7 @@ import torch
 from hstu_pointwise_attention_b200 import ops
 
 import qcache_ref as R
+from gpu_common import assert_close
 from test_gpu_qcache import Problem, f64, layer_params, stored
 
 pytestmark = pytest.mark.gpu
@@ -363,7 +364,7 @@ def test_a_captured_step_appends_scores_and_trims():
 @pytest.mark.parametrize("decay", [None, 0.5])
 @pytest.mark.parametrize("H,d,L,n", [(2, 64, 20, 5), (2, 64, 20, 20), (2, 64, 20, 100),
                                      (1, 128, 20, 40), (4, 32, 20, 20), (2, 64, 600, 5),
-                                     (2, 64, 900, 70)])
+                                     (2, 64, 900, 70), (1, 32, 3000, 3)])
 def test_layer_norm_sees_the_attention_in_float32(decay, H, d, L, n):
     """Attention outputs whose features differ by little against their size: the
     LayerNorm takes the size away and leaves a rounding of it magnified.
@@ -432,3 +433,40 @@ def test_rows_of_which_nothing_is_left_are_zero(decay, dtype, impl, n, t_cand):
         if decay is not None:
             for b in range(3):
                 assert torch.all(w[p.rows[b]:p.rows[b] + p.lens[b]] == 0)
+
+
+@pytest.mark.parametrize("H,dk,dv,n", [(2, 64, 32, 5), (2, 64, 32, 40), (1, 32, 128, 3),
+                                       (4, 128, 64, 20), (2, 96, 64, 9)])
+def test_layer_of_unequal_key_and_value_sizes(H, dk, dv, n):
+    """The columns [U|V|Q|K] of the projection, by the attention on views of it."""
+    rng = np.random.default_rng(680 + n)
+    p = Problem([300, 0, 41], [n, 2, 1], H, dk, dv, "bf16", seed=681)
+    T, D, F = n + 3, 64, H * dv
+    n1 = 2 * (F + H * dk)
+    w = lambda *s: torch.from_numpy((rng.standard_normal(s) / 8).astype(np.float32)).cuda()
+    w1, w2 = w(n1, D).bfloat16(), w(D, F).bfloat16()
+    b1, ga, be, b2, rp, rt = w(n1), 1 + w(F), w(F), w(D), w(40), w(24)
+    x = (8 * w(T, D)).bfloat16()
+    proj = torch.empty((T, n1), dtype=torch.bfloat16, device="cuda")
+    kw = dict(max_seq_len=p.msl, time_bucket_sub_bits=2, silu_scale=p.scale)
+    y = ops.layer_fwd_candidates_qcache(
+        x, w1, b1, ga, be, w2, b2, rp, rt, p.c, p.rows, p.lens, p.off, p.cand_pos, p.ts,
+        num_heads=H, d_qk=dk, d_v=dv, proj_out=proj, **kw)
+    v, q, k = (proj[:, a:b] for a, b in ((F, 2 * F), (2 * F, 2 * F + H * dk), (2 * F + H * dk, n1)))
+    u_in = f64(x) @ f64(w1).T + f64(b1)
+    z = u_in / (1 + np.exp(-u_in))
+    # (half a step of bf16, and as much again with 1e-4 for float32 sums and the tanh)
+    assert np.all(np.abs(f64(proj) - z) <= 2.0 ** -7 * np.abs(z) + 1e-4)
+    q, k, v, u = (f64(t).reshape(T, H, -1) for t in (q, k, v, proj[:, :F]))
+    A = np.zeros((T, F))
+    for b in range(3):
+        a, sl = slice(int(p.off[b]), int(p.off[b + 1])), \
+            slice(int(p.rows[b]), int(p.rows[b] + p.lens[b]))
+        kh, vh = stored(p.c, p.rows[b], p.lens[b])
+        A[a] = R.attend(q[a], k[a], v[a], kh, vh, p.c.pos[sl].cpu().numpy(),
+                        p.c.times[sl].cpu().numpy(), int(p.cand_pos[b]), p.t[a], f64(rp), f64(rt),
+                        2, 1 / np.sqrt(dk), p.scale, 0.0)[0].reshape(-1, F)
+    mu = A.mean(1, keepdims=True)
+    g = (A - mu) / np.sqrt(((A - mu) ** 2).mean(1, keepdims=True) + 1e-5) * f64(ga) + f64(be)
+    want = f64(x) + (g * u.reshape(T, F)) @ f64(w2).T + f64(b2)
+    assert_close(f64(y), want, "bf16", "layer")
